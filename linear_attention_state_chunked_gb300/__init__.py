@@ -445,3 +445,12 @@ def lin_state_selftest_mma(A, B, D, a_mn=False, b_mn=False, bf16=False, status=N
 
 def lin_state_version() -> int:
     return int(lib.lin_state_version())
+
+
+# ---- the rest of a hybrid model's decode step (include/lin_step.h) -----------
+from .step import (  # noqa: E402,F401
+    LIN_ACT_NONE, LIN_ACT_SIGMOID, LIN_ACT_SILU, LIN_ST_BAD_PAGE, STEP_EXPORTED, AttnArgsT, KVAppendArgsT,
+    KVCache, KVCacheT, NormArgsT, lin_state_attn_decode, lin_state_attn_workspace, lin_state_block_norm,
+    lin_state_kv_append)
+
+EXPORTED += STEP_EXPORTED

@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblinstate.so")
 
-SOURCES = ["api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
-           "selftest.cu"]
+# step_api.cu holds api.cu, whose checks and error text it shares
+SOURCES = ["step_api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
+           "selftest.cu", "kv_cache.cu", "attn_decode.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -42,7 +43,8 @@ def _newer(target: str, deps) -> bool:
 
 def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hdrs.append(os.path.join(ROOT, "include", "lin_state.h"))
+    hdrs += [os.path.join(ROOT, "include", f) for f in ("lin_state.h", "lin_step.h")]
+    hdrs.append(os.path.join(CSRC, "api.cu"))
     return hdrs
 
 
