@@ -1,0 +1,14 @@
+// Decode attention kernels for heads of 64 channels (attn_kernel.cuh).
+
+#include "attn_kernel.cuh"
+
+namespace lin {
+namespace attn {
+
+cudaError_t launch_d64(const Plan& p, int row_tiles, int grid, cudaStream_t s) {
+  return p.c.dtype == LIN_BF16 ? launch_rows<64, LIN_BF16>(p, row_tiles, grid, s)
+                               : launch_rows<64, LIN_F32>(p, row_tiles, grid, s);
+}
+
+}  // namespace attn
+}  // namespace lin

@@ -1,116 +1,176 @@
-// Decode attention over a paged key-value cache (lin_step.h).
-//
-//   out[r][j][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q.k_t - m)
-//
-// in one pass over the visible tokens with the running maximum m and sum. One
-// CTA takes one (request, query token, query head); its warps take every
-// fourth token, a lane holds head_dim / 32 channels, and the warps' (m, sum,
-// values) are joined in shared memory at the end.
+// Decode attention over a paged key-value cache (lin_step.h): the join of split
+// items and the host side. The main kernel is in attn_kernel.cuh.
 
-#include <math.h>
-
-#include "common.cuh"
-#include "step_internal.h"
+#include "attn_kernel.cuh"
 
 namespace lin {
+namespace attn {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kJoinWarps = 4;
 
-template <int D, int DT>
-__global__ void __launch_bounds__(kWarps * 32)
-attn_simple_kernel(const lin_kv_cache_t c, const lin_attn_args_t a) {
-  constexpr int E = D / 32;
-  __shared__ float sm_m[kWarps], sm_l[kWarps], sm_o[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % a.num_q_heads, j = blockIdx.x / a.num_q_heads % a.n_q;
-  const int r = blockIdx.x / a.num_q_heads / a.n_q;
-  const int hk = h / (a.num_q_heads / c.num_kv_heads);
-  const int len = a.kv_len[r];
-  if (len < 0) return;
-  if (len > int64_t(a.max_pages) * c.page_size) {
-    if (threadIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
-    return;
+// Block (c, y): rows 4 y .. 4 y + 3 (a warp each) of the item that begins in
+// range c and goes on past it. Its parts, in token order: 2c + 1, then 2c' of
+// the ranges c' = c + 1, ... until one that does not go on.
+template <int D, int RT>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int V = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  const int64_t item = p.tail[c];
+  if (item < 0) return;
+  const int rb = static_cast<int>(item % p.row_blocks);
+  const int64_t head = item / p.row_blocks;
+  const int hk = static_cast<int>(head % p.c.num_kv_heads);
+  const int64_t r = head / p.c.num_kv_heads;
+  const int q = rb * 16 * RT + row;
+  if (row >= 16 * RT || q >= p.rows) return;
+  // the number of parts: lanes look at 32 ranges at a time
+  int parts = 1;
+  for (int at = c + 1;; at += 32) {
+    const int x = at + lane;
+    const bool stop = x >= static_cast<int>(gridDim.x) || p.more[x] == 0;
+    const uint32_t b = __ballot_sync(~0u, stop);
+    parts += b ? __ffs(b) : 32;
+    if (b) break;
   }
-  const int base = len - a.n_q;
-  uint32_t see = (2u << j) - 1u;
-  if (a.parent) {
-    const int par = lane < a.n_q ? a.parent[int64_t(r) * a.n_q + lane] : -1;
-    if (__any_sync(~0u, lane < a.n_q && (par < -1 || par >= lane))) {
-      if (threadIdx.x == 0) report(a.status, LIN_ST_BAD_TREE);
-      return;
+  auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * 16 * RT + row; };
+  float top = -INFINITY;
+  bool out = false;
+  for (int i = lane; i < parts; i += 32) {
+    const float2 ml = p.part_ml[index(i)];
+    top = fmaxf(top, ml.x);
+    out |= ml.y == -1.0f;
+  }
+  if (__any_sync(~0u, out)) return;  // a request left out
+#pragma unroll
+  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+  float sum = 0.0f, v[V];
+#pragma unroll
+  for (int x = 0; x < V; ++x) v[x] = 0.0f;
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+    float f = 0.0f;
+    if (i0 + lane < parts) {
+      const float2 ml = p.part_ml[index(i0 + lane)];
+      f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+      sum = fmaf(f, ml.y, sum);
     }
-    see = 0;
-    for (int at = j; at >= 0; at = __shfl_sync(~0u, par, at)) see |= 1u << at;
-  }
-  const char* qp = static_cast<const char*>(a.q) + r * a.req_stride + j * a.token_stride;
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
+    const int n = min(32, parts - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(~0u, f, i);
+      const float* src = p.part + index(i0 + i) * D + lane * V;
+      float x[V];
+      if constexpr (V == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        x[0] = y.x, x[1] = y.y;
+      } else {
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = load_elem(qp, h * D + lane + 32 * i, DT) * a.scale;
-    o[i] = 0.0f;
-  }
-  for (int t = warp; t < len; t += kWarps) {
-    if (t >= base && !((see >> (t - base)) & 1u)) continue;
-    const int pg = t / c.page_size;
-    const int id = a.page_table[r * a.page_table_stride + pg];
-    if (id < 0 || id >= c.num_pages) {
-      if (lane == 0) report(a.status, LIN_ST_BAD_PAGE);
-      continue;
+        for (int k = 0; k < V; k += 4) {
+          const float4 y = *reinterpret_cast<const float4*>(src + k);
+          x[k] = y.x, x[k + 1] = y.y, x[k + 2] = y.z, x[k + 3] = y.w;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[k] = fmaf(w, x[k], v[k]);
     }
-    const int64_t at = a.layer * c.layer_stride + id * c.page_stride +
-                       int64_t(t - pg * c.page_size) * c.token_stride + hk * c.head_stride;
-    const char* kp = static_cast<const char*>(c.k) + at;
-    const char* vp = static_cast<const char*>(c.v) + at;
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) s = fmaf(q[i], load_elem(kp, lane + 32 * i, DT), s);
-#pragma unroll
-    for (int w = 16; w; w >>= 1) s += __shfl_xor_sync(~0u, s, w);
-    const float m2 = fmaxf(m, s);
-    const float f = m == m2 ? 1.0f : expf(m - m2), p = expf(s - m2);
-    l = fmaf(l, f, p);
-#pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = fmaf(o[i], f, p * load_elem(vp, lane + 32 * i, DT));
-    m = m2;
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) sm_o[warp][lane + 32 * i] = o[i];
-  if (lane == 0) sm_m[warp] = m, sm_l[warp] = l;
-  __syncthreads();
-  float top = -INFINITY, sum = 0.0f, f[kWarps];
+  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = ((r * p.a.n_q + q / p.group) * p.a.num_q_heads + hk * p.group + q % p.group) * D + lane * V;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w]);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = sm_l[w] != 0.0f ? expf(sm_m[w] - top) : 0.0f;  // a NaN stays one
-    sum += f[w] * sm_l[w];
-  }
-  const int64_t out = ((int64_t(r) * a.n_q + j) * a.num_q_heads + h) * D;
-  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += f[w] * sm_o[w][d];
-    store_elem(a.out, out + d, a.out_dtype, sum != 0.0f ? v / sum : 0.0f);
+  for (int k = 0; k < V; k += 2) {
+    if (p.a.out_dtype == LIN_F32) {
+      *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at + k) = make_float2(v[k] * f, v[k + 1] * f);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[k] * f, v[k + 1] * f);
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + at + k) = h;
+    }
   }
 }
 
-}  // namespace
+// 16-row tiles of a row block: each warp of a group owns one.
+int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
-size_t attn_workspace(const lin_kv_cache_t&, const lin_attn_args_t&) { return 0; }
+template <int D, int DT>
+int ctas(int rt) {
+  return rt == 1 ? Cfg<D, DT, 1>::CTAS : rt == 2 ? Cfg<D, DT, 2>::CTAS : Cfg<D, DT, 4>::CTAS;
+}
 
-cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a, void*, cudaStream_t s) {
-  const int64_t blocks = int64_t(a.batch) * a.n_q * a.num_q_heads;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks));
+// CTAs of the main kernel: what is resident at once, or one per unit where the
+// longest request allowed would give fewer.
+int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
+  if (sms <= 0) sms = 152;  // no device: the size of a GB300
+  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads), rt = row_tiles(rows);
   const bool b = c.dtype == LIN_BF16;
-  if (c.head_dim == 64)
-    (b ? attn_simple_kernel<64, LIN_BF16> : attn_simple_kernel<64, LIN_F32>)<<<grid, kWarps * 32, 0, s>>>(c, a);
-  else if (c.head_dim == 128)
-    (b ? attn_simple_kernel<128, LIN_BF16> : attn_simple_kernel<128, LIN_F32>)<<<grid, kWarps * 32, 0, s>>>(c, a);
-  else
-    (b ? attn_simple_kernel<256, LIN_BF16> : attn_simple_kernel<256, LIN_F32>)<<<grid, kWarps * 32, 0, s>>>(c, a);
-  return cudaGetLastError();
+  const int per = c.head_dim == 64    ? (b ? ctas<64, LIN_BF16>(rt) : ctas<64, LIN_F32>(rt))
+                  : c.head_dim == 128 ? (b ? ctas<128, LIN_BF16>(rt) : ctas<128, LIN_F32>(rt))
+                                      : (b ? ctas<256, LIN_BF16>(rt) : ctas<256, LIN_F32>(rt));
+  const int64_t blocks = (rows + 16 * rt - 1) / (16 * rt);
+  const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
+  const int64_t items = int64_t(a.batch) * c.num_kv_heads * blocks;
+  const int64_t most = units > 1 && items < INT32_MAX ? items * units : items;
+  return static_cast<int>(most < int64_t(sms) * per && most > 0 ? most : int64_t(sms) * per);
+}
+
+size_t round16(size_t n) { return (n + 15) & ~size_t(15); }
+
+template <int D>
+cudaError_t launch_join(const cudaLaunchConfig_t& cfg, int rt, const Plan& p) {
+  return rt == 1   ? cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p)
+         : rt == 2 ? cudaLaunchKernelEx(&cfg, join_kernel<D, 2>, p)
+                   : cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, p);
+}
+
+}  // namespace
+}  // namespace attn
+
+size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+  const size_t grid = attn::grid_of(c, a);
+  const size_t rows = 16 * attn::row_tiles(a.n_q * (a.num_q_heads / c.num_kv_heads));
+  return 2 * grid * rows * (c.head_dim * sizeof(float) + sizeof(float2)) + attn::round16(grid * 8) +
+         attn::round16(grid * 4);
+}
+
+cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a, void* ws, cudaStream_t s) {
+  attn::Plan p;
+  p.c = c;
+  p.a = a;
+  p.group = a.num_q_heads / c.num_kv_heads;
+  p.rows = a.n_q * p.group;
+  const int rt = attn::row_tiles(p.rows), grid = attn::grid_of(c, a);
+  p.row_blocks = (p.rows + 16 * rt - 1) / (16 * rt);
+  p.scale_log2 = a.scale * 1.4426950408889634f;  // log2(e)
+  char* w = static_cast<char*>(ws);
+  p.part = reinterpret_cast<float*>(w);
+  w += size_t(2) * grid * 16 * rt * c.head_dim * sizeof(float);
+  p.part_ml = reinterpret_cast<float2*>(w);
+  w += size_t(2) * grid * 16 * rt * sizeof(float2);
+  p.tail = reinterpret_cast<int64_t*>(w);
+  w += attn::round16(size_t(grid) * 8);
+  p.more = reinterpret_cast<int32_t*>(w);
+  cudaError_t e = c.head_dim == 64    ? attn::launch_d64(p, rt, grid, s)
+                  : c.head_dim == 128 ? attn::launch_d128(p, rt, grid, s)
+                                      : attn::launch_d256(p, rt, grid, s);
+  if (e != cudaSuccess) return e;
+  // the join's launch overlaps the main kernel, and it waits there for its end
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = p.rows < 16 * rt ? p.rows : 16 * rt;
+  cfg.gridDim = dim3(grid, (rows + attn::kJoinWarps - 1) / attn::kJoinWarps);
+  cfg.blockDim = dim3(attn::kJoinWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return c.head_dim == 64    ? attn::launch_join<64>(cfg, rt, p)
+         : c.head_dim == 128 ? attn::launch_join<128>(cfg, rt, p)
+                             : attn::launch_join<256>(cfg, rt, p);
 }
 
 }  // namespace lin

@@ -1,0 +1,642 @@
+// Decode attention over a paged key-value cache: the main kernel (lin_step.h).
+//
+//   out[r][j][h] = sum_t p_t v_t / sum_t p_t,  p_t = 2^(s_t - m),
+//   s_t = scale log2(e) q.k_t over the tokens that query j sees,
+//
+// one pass over the cache with a running maximum m, sum and value sum per row.
+// The rows of one (request, key-value head) are its n_q x G queries (G query
+// heads share the head's keys), so every key is read once for all of them.
+//
+// Bound by HBM: 2 head_dim elements per token and key-value head are read for
+// 4 head_dim flops a row, a few tens of flops per byte. The tensor work
+// is warp-level MMA on 16 rows: a tile of 16 rows is what a decode step has,
+// and each warp keeps its rows' whole softmax state in registers, with no
+// barrier between warps of a step.
+//
+// Work split. A unit is 64 tokens of one item = (request, kv head, row block).
+// The units of the whole batch, laid end to end, are cut into one equal range
+// per CTA (lengths are read on the device), so a batch of ragged lengths and a
+// single long request load the SMs alike. An item inside one range is finished
+// there; one that crosses a border leaves (value sums, m, sum) of each piece in
+// the workspace and a second kernel joins them in range order, so results do
+// not depend on timing.
+//
+// Inside a CTA a group of RT warps (one per 16 rows) shares a ring of S slots of
+// 16 tokens' K and V, filled by 16-byte asynchronous copies of its own threads;
+// NW / RT groups take every KG-th slot of a piece and are joined in shared
+// memory at its end. Rows of a slot are swizzled (16-byte chunk c of row r at
+// c ^ (r % 8)), so every fragment load is free of bank conflicts. Tokens past
+// the length, or in a bad page, are filled with zeros and masked.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "step_internal.h"
+#include "umma.cuh"
+
+namespace lin {
+namespace attn {
+
+constexpr int kUnit = 64;  // tokens of a work unit
+constexpr int kSub = 16;   // tokens of a ring slot
+
+struct Plan {
+  lin_kv_cache_t c;
+  lin_attn_args_t a;
+  int group;          // query heads per key-value head
+  int rows;           // n_q * group
+  int row_blocks;     // of 16 RT rows
+  float scale_log2;
+  float* part;        // [2 grid][16 RT][D] value sums of unfinished pieces
+  float2* part_ml;    // [2 grid][16 RT] their (maximum, sum); sum -1: left out
+  int64_t* tail;      // [grid] item whose first piece is part 2c + 1, or -1
+  int32_t* more;      // [grid] part 2c goes on in range c + 1
+};
+
+template <int D_, int DT_, int RT_>
+struct Cfg {
+  static constexpr int D = D_, DT = DT_, RT = RT_;
+  static constexpr int ES = DT == LIN_BF16 ? 2 : 4;
+  static constexpr int ROWB = D * ES;                 // bytes of one key or value
+  static constexpr int SLOT = 2 * kSub * ROWB;        // K and V of 16 tokens
+  // two CTAs per SM where a slot is small enough for three slots per warp in
+  // half the shared memory
+  static constexpr int CTAS = SLOT <= 8192 ? 2 : 1;
+  static constexpr int NW0 = SLOT <= 16384 ? 4 : 2;
+  static constexpr int NW = NW0 > RT ? NW0 : RT;
+  static constexpr int KG = NW / RT;
+  static constexpr int QBYTES = 16 * RT * ROWB;
+  static constexpr int BUDGET = (CTAS == 2 ? 110 : 222) * 1024;
+  static constexpr int SLOTS = (BUDGET - QBYTES) / SLOT / KG;
+  static constexpr int S = SLOTS < 12 ? SLOTS : 12;
+  static constexpr int RING = KG * S * SLOT;
+  static constexpr int SMEM = RING + QBYTES;
+  static_assert(S >= 2 && RING >= KG * RT * 16 * (D + 2) * 4, "");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+template <int RT>
+__device__ __forceinline__ void group_sync(int kg) {
+  if constexpr (RT == 1)
+    __syncwarp();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RT * 32) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ float lds32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// x = hi + lo in two tf32 values (11 significant bits each, so the pair is off
+// by at most 2^-22 of x)
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+}
+// the next bf16 part of a pair of weights; the pair keeps what is left
+__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  a -= __low2float(h);
+  b -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// a pair of bf16 values with 0 for infinities and NaN
+__device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in rows of ROWB bytes.
+template <int ROWB>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  return static_cast<uint32_t>(r * ROWB + ((c ^ (r & 7)) << 4));
+}
+
+// Units of a request: at least one where it has an output to write.
+__device__ __forceinline__ int units_of(int len, int64_t most) {
+  return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
+}
+
+template <class C, int PT>
+__global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p) {
+  constexpr int D = C::D, RT = C::RT, KG = C::KG, S = C::S, NT = C::NW * 32, ROWB = C::ROWB;
+  constexpr bool BF = C::DT == LIN_BF16;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ uint32_t s_valid[KG][S];  // live tokens of each slot
+  __shared__ uint32_t s_see[32];       // drafts that each query sees
+  __shared__ int64_t s_scan[C::NW], s_first[2];
+  __shared__ int s_bad;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kg = warp / RT, rt = warp % RT, gtid = rt * 32 + lane;
+  const int g = lane >> 2, t4 = lane & 3;
+  const lin_kv_cache_t& c = p.c;
+  const lin_attn_args_t& a = p.a;
+  const int per_req = c.num_kv_heads * p.row_blocks;
+  // token indices stay clear of the 32-bit end
+  const int64_t most = min(int64_t(a.max_pages) * c.page_size, int64_t(INT32_MAX - 65536));
+
+  // ---- this CTA's range of units: a scan over the requests' lengths ----------
+  const int span = (a.batch + NT - 1) / NT;
+  const int r0 = min(a.batch, tid * span), r1 = min(a.batch, r0 + span);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int len = a.kv_len[r];
+    if (len > most && blockIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
+    mine += units_of(len, most);
+  }
+  mine *= per_req;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_scan[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < C::NW; ++w) {
+    if (w < warp) upto += s_scan[w];
+    total += s_scan[w];
+  }
+  const int64_t ranges = total < gridDim.x ? total : gridDim.x;
+  if (blockIdx.x >= ranges) {
+    if (tid == 0) p.tail[blockIdx.x] = -1, p.more[blockIdx.x] = 0;
+    return;
+  }
+  int64_t cur = total * blockIdx.x / ranges;
+  const int64_t end = total * (blockIdx.x + 1) / ranges;
+  if (cur >= upto - mine && cur < upto) {
+    int64_t at = upto - mine;
+    int r = r0;
+    for (;; ++r) {
+      const int64_t n = int64_t(units_of(a.kv_len[r], most)) * per_req;
+      if (cur < at + n) break;
+      at += n;
+    }
+    s_first[0] = r;
+    s_first[1] = cur - at;
+  }
+  __syncthreads();
+  int r = static_cast<int>(s_first[0]);
+  int len = a.kv_len[r];
+  int u = units_of(len, most);
+  int it = static_cast<int>(s_first[1] / u);    // item of the request
+  int t0 = static_cast<int>(s_first[1] % u);    // its first unit here
+  int64_t tail = -1;
+  int more = 0;
+
+  const uint32_t ring = umma::smem_u32(smem) + kg * (S * C::SLOT);
+  const uint32_t qs = umma::smem_u32(smem) + C::RING;
+  float* merge = reinterpret_cast<float*>(smem);                       // [KG][16 RT][D]
+  float2* merge_ml = reinterpret_cast<float2*>(merge + KG * 16 * RT * D);  // [KG][16 RT]
+
+  while (true) {
+    const int t1 = static_cast<int>(min(int64_t(u), t0 + (end - cur)));
+    const int hk = it / p.row_blocks, row0 = (it % p.row_blocks) * 16 * RT;
+    const int key_begin = t0 * kUnit, key_end = t1 == u ? len : t1 * kUnit;
+    const int base = len - a.n_q;  // tokens that every query sees
+    const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
+    const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
+    const int32_t* table = a.page_table + r * a.page_table_stride;
+
+    // ---- slots: lane l of every warp looks up token l % 16 of the slot --------
+    const int subs = (key_end - key_begin + kSub - 1) / kSub;
+    const int count = subs > kg ? (subs - kg + KG - 1) / KG : 0;  // this group's
+    int key = key_begin + kg * kSub + (lane & 15);
+    int page = 0, in_page = 0, id = -1;
+    auto look = [&]() {  // page id of the next slot's token
+      page = key / c.page_size;
+      in_page = key - page * c.page_size;
+      id = key < key_end ? table[page] : -1;
+    };
+    auto fill = [&](int slot) {
+      const bool live = id >= 0 && id < c.num_pages;
+      if (key < key_end && !live && gtid == (lane & 15)) report(a.status, LIN_ST_BAD_PAGE);
+      const int64_t off = live ? id * c.page_stride + in_page * c.token_stride : 0;
+      const uint32_t valid = __ballot_sync(~0u, live) & 0xffffu;
+      if (gtid == 0) s_valid[kg][slot] = valid;
+      constexpr int CPR = ROWB / 16;
+      const uint32_t dst = ring + slot * C::SLOT;
+#pragma unroll
+      for (int i = 0; i < kSub * CPR / (RT * 32); ++i) {
+        const int x = i * (RT * 32) + gtid, row = x / CPR, ch = x % CPR;
+        const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
+        const bool ok = (valid >> row) & 1u;
+        cp16(dst + chunk_at<ROWB>(row, ch), kb + o, ok);
+        cp16(dst + kSub * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
+      }
+      key += KG * kSub;
+      look();
+    };
+    look();
+#pragma unroll 1
+    for (int i = 0; i < S - 1; ++i) {
+      if (i < count) fill(i);
+      cp_commit();
+    }
+
+    // ---- queries and what they see ------------------------------------------
+    {
+      constexpr int CPR = ROWB / 16;
+      const char* qb = static_cast<const char*>(a.q) + r * a.req_stride;
+      for (int x = tid; x < 16 * RT * CPR; x += NT) {
+        const int row = x / CPR, ch = x % CPR, q = row0 + row;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q < p.rows) {
+          const int j = q / p.group, h = hk * p.group + q % p.group;
+          v = *reinterpret_cast<const uint4*>(qb + j * a.token_stride + h * ROWB + ch * 16);
+        }
+        *reinterpret_cast<uint4*>(smem + C::RING + chunk_at<ROWB>(row, ch)) = v;
+      }
+      if (warp == 0) {
+        uint32_t see = (2u << lane) - 1u;
+        bool bad = false;
+        if (a.parent) {
+          const int par = lane < a.n_q ? a.parent[int64_t(r) * a.n_q + lane] : -1;
+          bad = __any_sync(~0u, lane < a.n_q && (par < -1 || par >= lane));
+          see = 1u << lane;
+          if (!bad)
+            // parents come first: in n_q rounds every node has its parent's set
+            for (int j = 0; j < a.n_q; ++j) {
+              const uint32_t s = __shfl_sync(~0u, see, j);
+              if (par == j) see |= s;
+            }
+        }
+        s_see[lane] = see;
+        if (lane == 0) {
+          s_bad = bad;
+          if (bad) report(a.status, LIN_ST_BAD_TREE);
+        }
+      }
+    }
+    __syncthreads();
+    const bool bad = s_bad;
+    const int qa = row0 + rt * 16 + g, qb2 = qa + 8;
+    const uint32_t see0 = qa < p.rows ? s_see[qa / p.group] : 0u;
+    const uint32_t see1 = qb2 < p.rows ? s_see[qb2 / p.group] : 0u;
+
+    constexpr bool QREG = BF && D <= 128;
+    uint32_t qf[QREG ? D / 16 : 1][4];
+    if constexpr (QREG) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        ldsm4(qf[k], qs + chunk_at<ROWB>(rt * 16 + (lane & 15), 2 * k + (lane >> 4)));
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+
+    // ---- the pass over this group's slots --------------------------------------
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+      cp_wait<S - 2>();
+      group_sync<RT>(kg);  // slot i has landed; slot i - 1 is free
+      if (i + S - 1 < count) fill(slot == 0 ? S - 1 : slot - 1);
+      cp_commit();
+      const uint32_t ks = ring + slot * C::SLOT, vs = ks + kSub * ROWB;
+      float s[2][4], s2[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[n][x] = s2[n][x] = 0.0f;
+      if constexpr (BF) {
+        // keys 0-7 | 8-15 of the slot are the two column tiles
+        const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t b[4];
+          ldsm4(b, ks + chunk_at<ROWB>(krow, 2 * k + kch));
+          if constexpr (QREG) {
+            mma_bf16(k & 1 ? s2[0] : s[0], qf[k], b[0], b[1]);
+            mma_bf16(k & 1 ? s2[1] : s[1], qf[k], b[2], b[3]);
+          } else {
+            uint32_t q[4];
+            ldsm4(q, qs + chunk_at<ROWB>(rt * 16 + (lane & 15), 2 * k + (lane >> 4)));
+            mma_bf16(k & 1 ? s2[0] : s[0], q, b[0], b[1]);
+            mma_bf16(k & 1 ? s2[1] : s[1], q, b[2], b[3]);
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int k = 0; k < D / 8; ++k) {
+          uint32_t qh[4], ql[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            split_tf32(lds32(qs + chunk_at<ROWB>(rt * 16 + g + (x & 1) * 8, 2 * k + (x >> 1)) + t4 * 4), qh[x], ql[x]);
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            uint32_t h0, w0, h1, w1;
+            split_tf32(lds32(ks + chunk_at<ROWB>(n * 8 + g, 2 * k) + t4 * 4), h0, w0);
+            split_tf32(lds32(ks + chunk_at<ROWB>(n * 8 + g, 2 * k + 1) + t4 * 4), h1, w1);
+            mma_tf32(s[n], qh, h0, h1);
+            mma_tf32(s2[n], ql, h0, h1);
+            mma_tf32(s2[n], qh, w0, w1);
+          }
+        }
+      }
+      // which of the 16 tokens the two rows see
+      const int key0 = key_begin + (i * KG + kg) * kSub;
+      const uint32_t valid = s_valid[kg][slot];
+      const int sh = key0 - base;
+      uint32_t vis0 = valid, vis1 = valid;
+      const bool drafts = sh + kSub > 0;
+      if (drafts) {
+        if (sh >= 0) {
+          vis0 &= see0 >> sh;
+          vis1 &= see1 >> sh;
+        } else {
+          const uint32_t old = (1u << -sh) - 1u;
+          vis0 &= (see0 << -sh) | old;
+          vis1 &= (see1 << -sh) | old;
+        }
+      }
+      // column n * 8 + 2 t4 + e of the tile
+      float mx0 = -INFINITY, mx1 = -INFINITY;
+      vis0 >>= 2 * t4;
+      vis1 >>= 2 * t4;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s[n][e] = (vis0 >> (8 * n + e)) & 1u ? (s[n][e] + s2[n][e]) * p.scale_log2 : -INFINITY;
+          s[n][2 + e] = (vis1 >> (8 * n + e)) & 1u ? (s[n][2 + e] + s2[n][2 + e]) * p.scale_log2 : -INFINITY;
+          mx0 = fmaxf(mx0, s[n][e]);
+          mx1 = fmaxf(mx1, s[n][2 + e]);
+        }
+#pragma unroll
+      for (int w = 1; w < 4; w <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, w));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, w));
+      }
+      if (__any_sync(~0u, mx0 > m0 || mx1 > m1)) {
+        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+        const float f0 = n0 == m0 ? 1.0f : exp2_fast(m0 - n0), f1 = n1 == m1 ? 1.0f : exp2_fast(m1 - n1);
+        m0 = n0, m1 = n1;
+        l0 *= f0, l1 *= f1;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= f0, o[n][1] *= f0;
+          o[n][2] *= f1, o[n][3] *= f1;
+        }
+      }
+      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l0 += s[n][e] = exp2_fast(s[n][e] - z0);
+          l1 += s[n][2 + e] = exp2_fast(s[n][2 + e] - z1);
+        }
+      // A value that some rows do not see may be infinite or NaN, and 0 times
+      // that is NaN: slots of drafts are looked over, and where one holds such
+      // values they are 0 in the products and are added to the rows that see
+      // them by themselves.
+      bool wild = false;
+      if (drafts && a.n_q > 1) {
+        for (int x = lane; x < kSub * ROWB / 16; x += 32) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + x * 16) : "memory");
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            wild |= (w[y] & 0x7f800000u) == 0x7f800000u;
+            if (BF) wild |= (w[y] & 0x7f80u) == 0x7f80u;
+          }
+        }
+        wild = __any_sync(~0u, wild);
+      }
+      if (wild) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+            for (int w = 0; w < 4; ++w) {  // token n * 8 + 2 w + e
+              const int kk = n * 8 + 2 * w + e, from = (lane & ~3) | w;
+              const float p0 = __shfl_sync(~0u, s[n][e], from), p1 = __shfl_sync(~0u, s[n][2 + e], from);
+              const bool v0 = __shfl_sync(~0u, (vis0 >> (8 * n + e)) & 1u, from);
+              const bool v1 = __shfl_sync(~0u, (vis1 >> (8 * n + e)) & 1u, from);
+#pragma unroll
+              for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                  const int d = x * 8 + 2 * t4 + y;
+                  float v;
+                  if constexpr (BF) {
+                    uint16_t h;
+                    asm volatile("ld.shared.u16 %0, [%1];"
+                                 : "=h"(h) : "r"(vs + chunk_at<ROWB>(kk, d >> 3) + (d & 7) * 2) : "memory");
+                    v = bf16_bits_to_f32(h);
+                  } else {
+                    v = lds32(vs + chunk_at<ROWB>(kk, d >> 2) + (d & 3) * 4);
+                  }
+                  if (isfinite(v)) continue;
+                  if (v0) o[x][y] = fmaf(p0, v, o[x][y]);
+                  if (v1) o[x][2 + y] = fmaf(p1, v, o[x][2 + y]);
+                }
+            }
+      }
+      if constexpr (BF) {
+        uint32_t pf[PT][4];
+#pragma unroll
+        for (int x = 0; x < PT; ++x) {
+          pf[x][0] = take_bf16(s[0][0], s[0][1]);
+          pf[x][1] = take_bf16(s[0][2], s[0][3]);
+          pf[x][2] = take_bf16(s[1][0], s[1][1]);
+          pf[x][3] = take_bf16(s[1][2], s[1][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          ldsm4t(b, vs + chunk_at<ROWB>(lane & 15, 2 * n + (lane >> 4)));
+          if (wild) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) b[x] = finite_bf16(b[x]);
+          }
+#pragma unroll
+          for (int x = PT - 1; x >= 0; --x) {
+            mma_bf16(o[2 * n], pf[x], b[0], b[1]);
+            mma_bf16(o[2 * n + 1], pf[x], b[2], b[3]);
+          }
+        }
+      } else {
+        // k index t4 | t4 + 4 of a product stands for token 2 t4 | 2 t4 + 1, as
+        // the scores lie in registers
+        uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          split_tf32(s[k][0], ph[k][0], pl[k][0]);
+          split_tf32(s[k][2], ph[k][1], pl[k][1]);
+          split_tf32(s[k][1], ph[k][2], pl[k][2]);
+          split_tf32(s[k][3], ph[k][3], pl[k][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int key_a = k * 8 + 2 * t4;
+            uint32_t h0, w0, h1, w1;
+            float va = lds32(vs + chunk_at<ROWB>(key_a, 2 * n + (g >> 2)) + (g & 3) * 4);
+            float vc = lds32(vs + chunk_at<ROWB>(key_a + 1, 2 * n + (g >> 2)) + (g & 3) * 4);
+            if (wild) va = isfinite(va) ? va : 0.0f, vc = isfinite(vc) ? vc : 0.0f;
+            split_tf32(va, h0, w0);
+            split_tf32(vc, h1, w1);
+            mma_tf32(o[n], pl[k], h0, h1);
+            mma_tf32(o[n], ph[k], w0, w1);
+            mma_tf32(o[n], ph[k], h0, h1);
+          }
+      }
+      slot = slot + 1 == S ? 0 : slot + 1;
+    }
+
+    // ---- join the groups ---------------------------------------------------------
+#pragma unroll
+    for (int w = 1; w < 4; w <<= 1) {
+      l0 += __shfl_xor_sync(~0u, l0, w);
+      l1 += __shfl_xor_sync(~0u, l1, w);
+    }
+    cp_wait<0>();
+    __syncthreads();  // every slot is read
+    {
+      const int row = kg * 16 * RT + rt * 16 + g;
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        *reinterpret_cast<float2*>(merge + row * D + n * 8 + 2 * t4) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(merge + (row + 8) * D + n * 8 + 2 * t4) = make_float2(o[n][2], o[n][3]);
+      }
+      if (t4 == 0) {
+        merge_ml[row] = make_float2(m0, l0);
+        merge_ml[row + 8] = make_float2(m1, l1);
+      }
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == u;
+    const int64_t part = 2 * int64_t(blockIdx.x) + (t0 == 0 ? 1 : 0);
+    for (int x = tid; x < 16 * RT * (D / 4); x += NT) {
+      const int row = x / (D / 4), d = (x % (D / 4)) * 4, q = row0 + row;
+      if (q >= p.rows) continue;
+      float top = -INFINITY, sum = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < KG; ++k) top = fmaxf(top, merge_ml[k * 16 * RT + row].x);
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        const float2 ml = merge_ml[k * 16 * RT + row];
+        if (ml.y == 0.0f) continue;  // saw nothing (a NaN sum goes on)
+        const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+        const float4 w = *reinterpret_cast<const float4*>(merge + (k * 16 * RT + row) * D + d);
+        sum = fmaf(f, ml.y, sum);
+        v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y);
+        v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
+      }
+      if (whole) {
+        if (bad) continue;
+        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t at = ((int64_t(r) * a.n_q + q / p.group) * a.num_q_heads + hk * p.group + q % p.group) * D + d;
+        if (a.out_dtype == LIN_F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+        } else {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+      } else {
+        *reinterpret_cast<float4*>(p.part + (part * 16 * RT + row) * D + d) = v;
+        if (d == 0) p.part_ml[part * 16 * RT + row] = make_float2(top, bad ? -1.0f : sum);
+      }
+    }
+    if (!whole) {
+      if (t0 == 0)
+        tail = int64_t(r) * per_req + it;
+      else
+        more = t1 < u;
+    }
+    cur += t1 - t0;
+    if (cur >= end) break;
+    t0 = 0;
+    if (++it == per_req) {
+      it = 0;
+      do {
+        len = a.kv_len[++r];
+        u = units_of(len, most);
+      } while (u == 0);
+    }
+    __syncthreads();  // the join is read before the ring is filled again
+  }
+  if (tid == 0) p.tail[blockIdx.x] = tail, p.more[blockIdx.x] = more;
+}
+
+template <class C, int PT>
+cudaError_t launch_main(const Plan& p, int grid, cudaStream_t s) {
+  auto kern = attn_kernel<C, PT>;
+  static bool ready[kMaxDevices];  // set twice at worst, to the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  kern<<<grid, C::NW * 32, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int DT>
+cudaError_t launch_rows(const Plan& p, int row_tiles, int grid, cudaStream_t s) {
+  constexpr int PT3 = DT == LIN_BF16 ? 3 : 1, PT2 = DT == LIN_BF16 ? 2 : 1;
+  const bool f32 = p.a.out_dtype == LIN_F32;
+  switch (row_tiles) {
+    case 1: return f32 ? launch_main<Cfg<D, DT, 1>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 1>, PT2>(p, grid, s);
+    case 2: return f32 ? launch_main<Cfg<D, DT, 2>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 2>, PT2>(p, grid, s);
+    default: return f32 ? launch_main<Cfg<D, DT, 4>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 4>, PT2>(p, grid, s);
+  }
+}
+
+// One translation unit per head_dim.
+cudaError_t launch_d64(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+cudaError_t launch_d128(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+cudaError_t launch_d256(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace lin
