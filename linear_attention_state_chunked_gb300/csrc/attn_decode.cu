@@ -7,60 +7,49 @@ namespace lin {
 namespace attn {
 namespace {
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 16;  // most rows side by side in the grid
 
-// Block (c, y): rows 4 y .. 4 y + 3 (a warp each) of the item that begins in
-// range c and goes on past it. Its parts, in token order: 2c + 1, then 2c' of
-// the ranges c' = c + 1, ... until one that does not go on.
+// Block (c, y): rows y, y + gridDim.y, ... of the item that begins in range c
+// and goes on past it. Its parts, in token order: 2c + 1, then 2c' of the ranges
+// c' = c + 1, ... The warps take every eighth part and are joined in shared
+// memory, always in the same order.
 template <int D, int RT>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int V = D / 32;
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  const int64_t item = p.tail[c];
+  __shared__ float s_v[kJoinWarps][D], s_sum[kJoinWarps];
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const longlong2 split = p.split[c];
+  const int64_t item = split.x;
   if (item < 0) return;
+  const int parts = static_cast<int>(split.y);
   const int rb = static_cast<int>(item % p.row_blocks);
   const int64_t head = item / p.row_blocks;
   const int hk = static_cast<int>(head % p.c.num_kv_heads);
   const int64_t r = head / p.c.num_kv_heads;
-  const int q = rb * 16 * RT + row;
-  if (row >= 16 * RT || q >= p.rows) return;
-  // the number of parts: lanes look at 32 ranges at a time
-  int parts = 1;
-  for (int at = c + 1;; at += 32) {
-    const int x = at + lane;
-    const bool stop = x >= static_cast<int>(gridDim.x) || p.more[x] == 0;
-    const uint32_t b = __ballot_sync(~0u, stop);
-    parts += b ? __ffs(b) : 32;
-    if (b) break;
-  }
-  auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * 16 * RT + row; };
-  float top = -INFINITY;
-  bool out = false;
-  for (int i = lane; i < parts; i += 32) {
-    const float2 ml = p.part_ml[index(i)];
-    top = fmaxf(top, ml.x);
-    out |= ml.y == -1.0f;
-  }
-  if (__any_sync(~0u, out)) return;  // a request left out
-#pragma unroll
-  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-  float sum = 0.0f, v[V];
-#pragma unroll
-  for (int x = 0; x < V; ++x) v[x] = 0.0f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {
-    float f = 0.0f;
-    if (i0 + lane < parts) {
-      const float2 ml = p.part_ml[index(i0 + lane)];
-      f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
+  for (int row = blockIdx.y; row < 16 * RT; row += gridDim.y) {
+    const int q = rb * 16 * RT + row;
+    if (q >= p.rows) return;
+    auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * 16 * RT + row; };
+    float top = -INFINITY;
+    bool out = false;
+    for (int i = lane; i < parts; i += 32) {
+      const float2 ml = p.part_ml[index(i)];
+      top = fmaxf(top, ml.x);
+      out |= ml.y == -1.0f;
     }
-    const int n = min(32, parts - i0);
+    if (__any_sync(~0u, out)) return;  // a request left out
+#pragma unroll
+    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+    float sum = 0.0f, v[V];
+#pragma unroll
+    for (int x = 0; x < V; ++x) v[x] = 0.0f;
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float w = __shfl_sync(~0u, f, i);
-      const float* src = p.part + index(i0 + i) * D + lane * V;
+    for (int i = warp; i < parts; i += kJoinWarps) {
+      const int64_t at = index(i);
+      const float2 ml = p.part_ml[at];
+      const float* src = p.part + at * D + lane * V;
       float x[V];
       if constexpr (V == 2) {
         const float2 y = *reinterpret_cast<const float2*>(src);
@@ -72,22 +61,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
           x[k] = y.x, x[k + 1] = y.y, x[k + 2] = y.z, x[k + 3] = y.w;
         }
       }
+      const float f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+      sum = fmaf(f, ml.y, sum);
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = fmaf(w, x[k], v[k]);
+      for (int k = 0; k < V; ++k) v[k] = fmaf(f, x[k], v[k]);
     }
-  }
 #pragma unroll
-  for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t at = ((r * p.a.n_q + q / p.group) * p.a.num_q_heads + hk * p.group + q % p.group) * D + lane * V;
+    for (int k = 0; k < V; ++k) s_v[warp][lane * V + k] = v[k];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
 #pragma unroll
-  for (int k = 0; k < V; k += 2) {
-    if (p.a.out_dtype == LIN_F32) {
-      *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at + k) = make_float2(v[k] * f, v[k + 1] * f);
-    } else {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[k] * f, v[k + 1] * f);
-      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + at + k) = h;
+    for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = ((r * p.a.n_q + q / p.group) * p.a.num_q_heads + hk * p.group + q % p.group) * D;
+    for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+      float x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) x += s_v[w][d];
+      store_elem(p.a.out, at + d, p.a.out_dtype, x * f);
     }
+    __syncthreads();
   }
 }
 
@@ -117,8 +111,6 @@ int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
   return static_cast<int>(most < int64_t(sms) * per && most > 0 ? most : int64_t(sms) * per);
 }
 
-size_t round16(size_t n) { return (n + 15) & ~size_t(15); }
-
 template <int D>
 cudaError_t launch_join(const cudaLaunchConfig_t& cfg, int rt, const Plan& p) {
   return rt == 1   ? cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p)
@@ -132,8 +124,7 @@ cudaError_t launch_join(const cudaLaunchConfig_t& cfg, int rt, const Plan& p) {
 size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
   const size_t grid = attn::grid_of(c, a);
   const size_t rows = 16 * attn::row_tiles(a.n_q * (a.num_q_heads / c.num_kv_heads));
-  return 2 * grid * rows * (c.head_dim * sizeof(float) + sizeof(float2)) + attn::round16(grid * 8) +
-         attn::round16(grid * 4);
+  return 2 * grid * rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
 }
 
 cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a, void* ws, cudaStream_t s) {
@@ -144,15 +135,20 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.rows = a.n_q * p.group;
   const int rt = attn::row_tiles(p.rows), grid = attn::grid_of(c, a);
   p.row_blocks = (p.rows + 16 * rt - 1) / (16 * rt);
-  p.scale_log2 = a.scale * 1.4426950408889634f;  // log2(e)
+  p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;  // log2(e)
+  p.slack = attn::kSlack / p.scale_log2;  // infinite where scale is 0: one reference does
+  p.negate = !(a.scale < 0.0f) ? 0u : c.dtype == LIN_BF16 ? 0x80008000u : 0x80000000u;
+  // Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
+  // mul = floor(2^32 (2^s - d) / d) + 1
+  p.page_shift = 0;
+  while ((int64_t(1) << p.page_shift) < c.page_size) ++p.page_shift;
+  p.page_mul = static_cast<uint32_t>((((uint64_t(1) << p.page_shift) - c.page_size) << 32) / c.page_size + 1);
   char* w = static_cast<char*>(ws);
   p.part = reinterpret_cast<float*>(w);
   w += size_t(2) * grid * 16 * rt * c.head_dim * sizeof(float);
   p.part_ml = reinterpret_cast<float2*>(w);
   w += size_t(2) * grid * 16 * rt * sizeof(float2);
-  p.tail = reinterpret_cast<int64_t*>(w);
-  w += attn::round16(size_t(grid) * 8);
-  p.more = reinterpret_cast<int32_t*>(w);
+  p.split = reinterpret_cast<longlong2*>(w);
   cudaError_t e = c.head_dim == 64    ? attn::launch_d64(p, rt, grid, s)
                   : c.head_dim == 128 ? attn::launch_d128(p, rt, grid, s)
                                       : attn::launch_d256(p, rt, grid, s);
@@ -162,8 +158,7 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int rows = p.rows < 16 * rt ? p.rows : 16 * rt;
-  cfg.gridDim = dim3(grid, (rows + attn::kJoinWarps - 1) / attn::kJoinWarps);
+  cfg.gridDim = dim3(grid, p.rows < attn::kJoinRows ? p.rows : attn::kJoinRows);
   cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = attr;

@@ -22,7 +22,7 @@
 // not depend on timing.
 //
 // Inside a CTA a group of RT warps (one per 16 rows) shares a ring of S slots of
-// 16 tokens' K and V, filled by 16-byte asynchronous copies of its own threads;
+// SUB tokens' K and V, filled by 16-byte asynchronous copies of its own threads;
 // NW / RT groups take every KG-th slot of a piece and are joined in shared
 // memory at its end. Rows of a slot are swizzled (16-byte chunk c of row r at
 // c ^ (r % 8)), so every fragment load is free of bank conflicts. Tokens past
@@ -38,8 +38,8 @@
 namespace lin {
 namespace attn {
 
+constexpr float kSlack = 8.0f;
 constexpr int kUnit = 64;  // tokens of a work unit
-constexpr int kSub = 16;   // tokens of a ring slot
 
 struct Plan {
   lin_kv_cache_t c;
@@ -47,32 +47,44 @@ struct Plan {
   int group;          // query heads per key-value head
   int rows;           // n_q * group
   int row_blocks;     // of 16 RT rows
-  float scale_log2;
+  float scale_log2;   // |scale| log2(e); q is negated where scale < 0
+  uint32_t negate;
+  float slack;        // kSlack in units of q.k
+  uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, mul) + t) >> shift, t < 2^31
   float* part;        // [2 grid][16 RT][D] value sums of unfinished pieces
   float2* part_ml;    // [2 grid][16 RT] their (maximum, sum); sum -1: left out
-  int64_t* tail;      // [grid] item whose first piece is part 2c + 1, or -1
-  int32_t* more;      // [grid] part 2c goes on in range c + 1
+  longlong2* split;   // [grid] the item that begins in range c and goes on past
+                      // it (or -1), and its number of parts
 };
 
+// Warps of one CTA: KG groups x RT row tiles x DS parts of head_dim. DS 2 halves
+// a warp's value sums (it computes the scores twice) where rows of 256 channels
+// would otherwise leave one warp per scheduler.
 template <int D_, int DT_, int RT_>
 struct Cfg {
   static constexpr int D = D_, DT = DT_, RT = RT_;
-  static constexpr int ES = DT == LIN_BF16 ? 2 : 4;
+  static constexpr bool BF = DT == LIN_BF16;
+  static constexpr int ES = BF ? 2 : 4;
   static constexpr int ROWB = D * ES;                 // bytes of one key or value
-  static constexpr int SLOT = 2 * kSub * ROWB;        // K and V of 16 tokens
-  // two CTAs per SM where a slot is small enough for three slots per warp in
-  // half the shared memory
-  static constexpr int CTAS = SLOT <= 8192 ? 2 : 1;
-  static constexpr int NW0 = SLOT <= 16384 ? 4 : 2;
-  static constexpr int NW = NW0 > RT ? NW0 : RT;
-  static constexpr int KG = NW / RT;
-  static constexpr int QBYTES = 16 * RT * ROWB;
-  static constexpr int BUDGET = (CTAS == 2 ? 110 : 222) * 1024;
+  static constexpr int SUB = 16;                      // tokens of a ring slot
+  static constexpr int SLOT = 2 * SUB * ROWB;         // their K and V
+  static constexpr int QP = BF ? 1 : 2;               // planes of q: fp32 as two tf32 parts
+  static constexpr int QBYTES = QP * 16 * RT * ROWB;
+  static constexpr bool MANY = RT >= 2;
+  static constexpr int CTAS = ROWB > 256 ? 1 : MANY ? 2 : ROWB == 128 ? 4 : BF ? 2 : 3;
+  static constexpr int DS = ROWB <= 256 ? 1 : ROWB == 512 ? 2 : RT == 4 ? 2 : 4;
+  static constexpr int NW = ROWB <= 256 ? (MANY ? 8 : 4) : ROWB == 512 ? (MANY ? 16 : 8) : 8;
+  // a warp keeps its queries' operands in registers where that costs no occupancy
+  static constexpr bool QREG = BF && (D == 64 || (D == 128 && !MANY));
+  static constexpr int KG = NW / (RT * DS);
+  static constexpr int GT = RT * DS * 32;             // threads of a group
+  static constexpr int BUDGET = (CTAS == 4 ? 55 : CTAS == 3 ? 73 : CTAS == 2 ? 110 : 222) * 1024;
   static constexpr int SLOTS = (BUDGET - QBYTES) / SLOT / KG;
   static constexpr int S = SLOTS < 12 ? SLOTS : 12;
   static constexpr int RING = KG * S * SLOT;
   static constexpr int SMEM = RING + QBYTES;
-  static_assert(S >= 2 && RING >= KG * RT * 16 * (D + 2) * 4, "");
+  // the groups are joined where the ring and the queries were
+  static_assert(S >= 2 && SMEM >= KG * RT * 16 * (D + 2) * 4, "");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
@@ -83,12 +95,12 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-template <int RT>
+template <int GT>
 __device__ __forceinline__ void group_sync(int kg) {
-  if constexpr (RT == 1)
+  if constexpr (GT == 32)
     __syncwarp();
   else
-    asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RT * 32) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(GT) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -104,12 +116,12 @@ __device__ __forceinline__ float lds32(uint32_t at) {
   return v;
 }
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -118,11 +130,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// x = hi + lo in two tf32 values (11 significant bits each, so the pair is off
-// by at most 2^-22 of x)
+// x = hi + lo in two tf32 values of 11 significant bits, each rounded to nearest
+// (the unit reads the upper 19 bits of an operand), so the pair is off by at
+// most 2^-22 of x. Integer additions: the conversion instruction is slower.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
 // the next bf16 part of a pair of weights; the pair keeps what is left
 __device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
@@ -145,6 +158,12 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * ROWB + ((c ^ (r & 7)) << 4));
 }
 
+// The same from the offset `at` of chunk 0 of a row r with (r & 7) << 4 added:
+// a constant exclusive-or and a constant sum.
+__device__ __forceinline__ uint32_t chunk_from(uint32_t at, int c) {
+  return (at ^ ((c & 7) << 4)) + (c >> 3) * 128;
+}
+
 // Units of a request: at least one where it has an output to write.
 __device__ __forceinline__ int units_of(int len, int64_t most) {
   return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
@@ -152,8 +171,9 @@ __device__ __forceinline__ int units_of(int len, int64_t most) {
 
 template <class C, int PT>
 __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p) {
-  constexpr int D = C::D, RT = C::RT, KG = C::KG, S = C::S, NT = C::NW * 32, ROWB = C::ROWB;
-  constexpr bool BF = C::DT == LIN_BF16;
+  constexpr int D = C::D, RT = C::RT, DS = C::DS, KG = C::KG, S = C::S, NT = C::NW * 32, ROWB = C::ROWB;
+  constexpr int SUB = C::SUB, GT = C::GT, DW = D / DS;  // a warp sums DW channels of the values
+  constexpr bool BF = C::BF;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_valid[KG][S];  // live tokens of each slot
   __shared__ uint32_t s_see[32];       // drafts that each query sees
@@ -162,7 +182,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   asm volatile("griddepcontrol.launch_dependents;");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kg = warp / RT, rt = warp % RT, gtid = rt * 32 + lane;
+  const int kg = warp / (RT * DS), gtid = tid - kg * GT, rt = gtid / 32 / DS, ds = gtid / 32 % DS;
   const int g = lane >> 2, t4 = lane & 3;
   const lin_kv_cache_t& c = p.c;
   const lin_attn_args_t& a = p.a;
@@ -196,7 +216,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   }
   const int64_t ranges = total < gridDim.x ? total : gridDim.x;
   if (blockIdx.x >= ranges) {
-    if (tid == 0) p.tail[blockIdx.x] = -1, p.more[blockIdx.x] = 0;
+    if (tid == 0) p.split[blockIdx.x].x = -1;
     return;
   }
   int64_t cur = total * blockIdx.x / ranges;
@@ -218,8 +238,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   int u = units_of(len, most);
   int it = static_cast<int>(s_first[1] / u);    // item of the request
   int t0 = static_cast<int>(s_first[1] % u);    // its first unit here
-  int64_t tail = -1;
-  int more = 0;
+  longlong2 split = make_longlong2(-1, 0);
 
   const uint32_t ring = umma::smem_u32(smem) + kg * (S * C::SLOT);
   const uint32_t qs = umma::smem_u32(smem) + C::RING;
@@ -235,33 +254,33 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
     const int32_t* table = a.page_table + r * a.page_table_stride;
 
-    // ---- slots: lane l of every warp looks up token l % 16 of the slot --------
-    const int subs = (key_end - key_begin + kSub - 1) / kSub;
+    // ---- slots: lane l of every warp looks up token l % SUB of the slot --------
+    const int subs = (key_end - key_begin + SUB - 1) / SUB;
     const int count = subs > kg ? (subs - kg + KG - 1) / KG : 0;  // this group's
-    int key = key_begin + kg * kSub + (lane & 15);
-    int page = 0, in_page = 0, id = -1;
+    int key = key_begin + kg * SUB + (lane & (SUB - 1));
+    int in_page = 0, id = -1;
     auto look = [&]() {  // page id of the next slot's token
-      page = key / c.page_size;
+      const uint32_t page = (__umulhi(key, p.page_mul) + key) >> p.page_shift;
       in_page = key - page * c.page_size;
       id = key < key_end ? table[page] : -1;
     };
     auto fill = [&](int slot) {
-      const bool live = id >= 0 && id < c.num_pages;
-      if (key < key_end && !live && gtid == (lane & 15)) report(a.status, LIN_ST_BAD_PAGE);
+      const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
+      if (key < key_end && !live && gtid == (lane & (SUB - 1))) report(a.status, LIN_ST_BAD_PAGE);
       const int64_t off = live ? id * c.page_stride + in_page * c.token_stride : 0;
-      const uint32_t valid = __ballot_sync(~0u, live) & 0xffffu;
+      const uint32_t valid = __ballot_sync(~0u, live) & (SUB == 32 ? ~0u : (1u << (SUB & 31)) - 1u);
       if (gtid == 0) s_valid[kg][slot] = valid;
       constexpr int CPR = ROWB / 16;
       const uint32_t dst = ring + slot * C::SLOT;
 #pragma unroll
-      for (int i = 0; i < kSub * CPR / (RT * 32); ++i) {
-        const int x = i * (RT * 32) + gtid, row = x / CPR, ch = x % CPR;
+      for (int i = 0; i < SUB * CPR / GT; ++i) {
+        const int x = i * GT + gtid, row = x / CPR, ch = x % CPR;
         const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
         const bool ok = (valid >> row) & 1u;
         cp16(dst + chunk_at<ROWB>(row, ch), kb + o, ok);
-        cp16(dst + kSub * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
+        cp16(dst + SUB * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
       }
-      key += KG * kSub;
+      key += KG * SUB;
       look();
     };
     look();
@@ -281,8 +300,16 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         if (q < p.rows) {
           const int j = q / p.group, h = hk * p.group + q % p.group;
           v = *reinterpret_cast<const uint4*>(qb + j * a.token_stride + h * ROWB + ch * 16);
+          v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
         }
-        *reinterpret_cast<uint4*>(smem + C::RING + chunk_at<ROWB>(row, ch)) = v;
+        unsigned char* dst = smem + C::RING + chunk_at<ROWB>(row, ch);
+        if constexpr (!BF) {
+          uint4 lo;
+          split_tf32(__uint_as_float(v.x), v.x, lo.x), split_tf32(__uint_as_float(v.y), v.y, lo.y);
+          split_tf32(__uint_as_float(v.z), v.z, lo.z), split_tf32(__uint_as_float(v.w), v.w, lo.w);
+          *reinterpret_cast<uint4*>(dst + 16 * RT * ROWB) = lo;
+        }
+        *reinterpret_cast<uint4*>(dst) = v;
       }
       if (warp == 0) {
         uint32_t see = (2u << lane) - 1u;
@@ -311,194 +338,237 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     const uint32_t see0 = qa < p.rows ? s_see[qa / p.group] : 0u;
     const uint32_t see1 = qb2 < p.rows ? s_see[qb2 / p.group] : 0u;
 
-    constexpr bool QREG = BF && D <= 128;
+    constexpr bool QREG = C::QREG;
+    const uint32_t qat = qs + (BF ? chunk_at<ROWB>(rt * 16 + (lane & 15), lane >> 4)
+                                  : chunk_at<ROWB>(rt * 16 + g, 0) + t4 * 4);
     uint32_t qf[QREG ? D / 16 : 1][4];
     if constexpr (QREG) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        ldsm4(qf[k], qs + chunk_at<ROWB>(rt * 16 + (lane & 15), 2 * k + (lane >> 4)));
+      for (int k = 0; k < D / 16; ++k) ldsm4(qf[k], chunk_from(qat, 2 * k));
     }
-    float o[D / 8][4];
+    float o[DW / 8][4];
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < DW / 8; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+    float c0 = -INFINITY, c1 = -INFINITY;  // scores past these move the reference
+    float l0 = 0.0f, l1 = 0.0f, z0 = 0.0f, z1 = 0.0f;
 
     // ---- the pass over this group's slots --------------------------------------
     int slot = 0;
 #pragma unroll 1
     for (int i = 0; i < count; ++i) {
       cp_wait<S - 2>();
-      group_sync<RT>(kg);  // slot i has landed; slot i - 1 is free
+      group_sync<GT>(kg);  // slot i has landed; slot i - 1 is free
       if (i + S - 1 < count) fill(slot == 0 ? S - 1 : slot - 1);
       cp_commit();
-      const uint32_t ks = ring + slot * C::SLOT, vs = ks + kSub * ROWB;
-      float s[2][4], s2[2][4];
+      const uint32_t ks = ring + slot * C::SLOT, vs = ks + SUB * ROWB;
+      constexpr int NT8 = SUB / 8;  // tiles of 8 tokens
+      float s[NT8][4], s2[2][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT8; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[n][x] = s2[n][x] = 0.0f;
+        for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
       if constexpr (BF) {
-        // keys 0-7 | 8-15 of the slot are the two column tiles
-        const int krow = (lane & 7) + ((lane >> 4) << 3), kch = (lane >> 3) & 1;
+        // tokens 0-7 | 8-15 of 16 are two column tiles; with one such pair the
+        // even and odd steps sum apart, for chains half as long
+        const uint32_t kat = ks + chunk_at<ROWB>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+        if constexpr (NT8 == 2)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s2[0][x] = s2[1][x] = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          uint32_t b[4];
-          ldsm4(b, ks + chunk_at<ROWB>(krow, 2 * k + kch));
-          if constexpr (QREG) {
-            mma_bf16(k & 1 ? s2[0] : s[0], qf[k], b[0], b[1]);
-            mma_bf16(k & 1 ? s2[1] : s[1], qf[k], b[2], b[3]);
-          } else {
-            uint32_t q[4];
-            ldsm4(q, qs + chunk_at<ROWB>(rt * 16 + (lane & 15), 2 * k + (lane >> 4)));
-            mma_bf16(k & 1 ? s2[0] : s[0], q, b[0], b[1]);
-            mma_bf16(k & 1 ? s2[1] : s[1], q, b[2], b[3]);
+          uint32_t q[4];
+          if constexpr (!QREG) ldsm4(q, chunk_from(qat, 2 * k));
+#pragma unroll
+          for (int n = 0; n < NT8; n += 2) {
+            uint32_t b[4];
+            ldsm4(b, chunk_from(kat + n * 8 * ROWB, 2 * k));
+            const bool odd = NT8 == 2 && (k & 1);
+            mma_bf16(odd ? s2[0] : s[n], QREG ? qf[QREG ? k : 0] : q, b[0], b[1]);
+            mma_bf16(odd ? s2[1] : s[n + 1], QREG ? qf[QREG ? k : 0] : q, b[2], b[3]);
           }
         }
+        if constexpr (NT8 == 2)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[0][x] += s2[0][x], s[1][x] += s2[1][x];
       } else {
-#pragma unroll 4
+        const uint32_t kat = ks + chunk_at<ROWB>(g, 0) + t4 * 4;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s2[0][x] = s2[1][x] = 0.0f;
+#pragma unroll 8
         for (int k = 0; k < D / 8; ++k) {
           uint32_t qh[4], ql[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            split_tf32(lds32(qs + chunk_at<ROWB>(rt * 16 + g + (x & 1) * 8, 2 * k + (x >> 1)) + t4 * 4), qh[x], ql[x]);
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t at = chunk_from(qat + (x & 1) * 8 * ROWB, 2 * k + (x >> 1));
+            qh[x] = __float_as_uint(lds32(at));
+            ql[x] = __float_as_uint(lds32(at + 16 * RT * ROWB));
+          }
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             uint32_t h0, w0, h1, w1;
-            split_tf32(lds32(ks + chunk_at<ROWB>(n * 8 + g, 2 * k) + t4 * 4), h0, w0);
-            split_tf32(lds32(ks + chunk_at<ROWB>(n * 8 + g, 2 * k + 1) + t4 * 4), h1, w1);
+            split_tf32(lds32(chunk_from(kat + n * 8 * ROWB, 2 * k)), h0, w0);
+            split_tf32(lds32(chunk_from(kat + n * 8 * ROWB, 2 * k + 1)), h1, w1);
             mma_tf32(s[n], qh, h0, h1);
             mma_tf32(s2[n], ql, h0, h1);
             mma_tf32(s2[n], qh, w0, w1);
           }
         }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[0][x] += s2[0][x], s[1][x] += s2[1][x];
       }
-      // which of the 16 tokens the two rows see
-      const int key0 = key_begin + (i * KG + kg) * kSub;
+      // which of the slot's tokens the two rows see; token n * 8 + 2 t4 + e is
+      // bit 8 n + e of the shifted masks
       const uint32_t valid = s_valid[kg][slot];
-      const int sh = key0 - base;
+      const int sh = key_begin + (i * KG + kg) * SUB - base;
+      const bool drafts = sh + SUB > 0;
+      const bool masked = drafts || valid != (SUB == 32 ? ~0u : (1u << (SUB & 31)) - 1u);
       uint32_t vis0 = valid, vis1 = valid;
-      const bool drafts = sh + kSub > 0;
-      if (drafts) {
-        if (sh >= 0) {
-          vis0 &= see0 >> sh;
-          vis1 &= see1 >> sh;
-        } else {
-          const uint32_t old = (1u << -sh) - 1u;
-          vis0 &= (see0 << -sh) | old;
-          vis1 &= (see1 << -sh) | old;
+      if (masked) {
+        if (drafts) {
+          const uint32_t old = sh < 0 ? (1u << -sh) - 1u : 0u;
+          vis0 &= sh < 0 ? (see0 << -sh) | old : see0 >> sh;
+          vis1 &= sh < 0 ? (see1 << -sh) | old : see1 >> sh;
+        }
+        vis0 >>= 2 * t4;
+        vis1 >>= 2 * t4;
+#pragma unroll
+        for (int n = 0; n < NT8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (!((vis0 >> (8 * n + e)) & 1u)) s[n][e] = -INFINITY;
+            if (!((vis1 >> (8 * n + e)) & 1u)) s[n][2 + e] = -INFINITY;
+          }
+      }
+      float mx0 = s[0][0], mx1 = s[0][2];
+#pragma unroll
+      for (int n = 0; n < NT8; ++n) {
+        mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
+        mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
+      }
+      // The weights' reference m follows the maximum only where a score passes it
+      // by more than 2^kSlack: weights up to that size lose nothing in fp32, and
+      // most slots need neither the rows' maximum nor a rescaling of the sums.
+      if (__any_sync(~0u, mx0 > c0 || mx1 > c1)) {
+#pragma unroll
+        for (int w = 1; w < 4; w <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, w));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, w));
+        }
+        // z = -m scale_log2, 0 while a row has seen nothing
+        if (mx0 > c0) {
+          const float y = -mx0 * p.scale_log2, f = c0 == -INFINITY ? 0.0f : exp2_fast(y - z0);
+          z0 = y, c0 = mx0 + p.slack, l0 *= f;
+#pragma unroll
+          for (int n = 0; n < DW / 8; ++n) o[n][0] *= f, o[n][1] *= f;
+        }
+        if (mx1 > c1) {
+          const float y = -mx1 * p.scale_log2, f = c1 == -INFINITY ? 0.0f : exp2_fast(y - z1);
+          z1 = y, c1 = mx1 + p.slack, l1 *= f;
+#pragma unroll
+          for (int n = 0; n < DW / 8; ++n) o[n][2] *= f, o[n][3] *= f;
         }
       }
-      // column n * 8 + 2 t4 + e of the tile
-      float mx0 = -INFINITY, mx1 = -INFINITY;
-      vis0 >>= 2 * t4;
-      vis1 >>= 2 * t4;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < NT8; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[n][e] = (vis0 >> (8 * n + e)) & 1u ? (s[n][e] + s2[n][e]) * p.scale_log2 : -INFINITY;
-          s[n][2 + e] = (vis1 >> (8 * n + e)) & 1u ? (s[n][2 + e] + s2[n][2 + e]) * p.scale_log2 : -INFINITY;
-          mx0 = fmaxf(mx0, s[n][e]);
-          mx1 = fmaxf(mx1, s[n][2 + e]);
-        }
-#pragma unroll
-      for (int w = 1; w < 4; w <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, w));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, w));
-      }
-      if (__any_sync(~0u, mx0 > m0 || mx1 > m1)) {
-        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-        const float f0 = n0 == m0 ? 1.0f : exp2_fast(m0 - n0), f1 = n1 == m1 ? 1.0f : exp2_fast(m1 - n1);
-        m0 = n0, m1 = n1;
-        l0 *= f0, l1 *= f1;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[n][0] *= f0, o[n][1] *= f0;
-          o[n][2] *= f1, o[n][3] *= f1;
-        }
-      }
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l0 += s[n][e] = exp2_fast(s[n][e] - z0);
-          l1 += s[n][2 + e] = exp2_fast(s[n][2 + e] - z1);
+          s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, z0));
+          s[n][2 + e] = exp2_fast(fmaf(s[n][2 + e], p.scale_log2, z1));
         }
       // A value that some rows do not see may be infinite or NaN, and 0 times
       // that is NaN: slots of drafts are looked over, and where one holds such
       // values they are 0 in the products and are added to the rows that see
       // them by themselves.
       bool wild = false;
-      if (drafts && a.n_q > 1) {
-        for (int x = lane; x < kSub * ROWB / 16; x += 32) {
-          uint32_t w[4];
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + x * 16) : "memory");
+      if (masked) {
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            wild |= (w[y] & 0x7f800000u) == 0x7f800000u;
-            if (BF) wild |= (w[y] & 0x7f80u) == 0x7f80u;
+        for (int n = 0; n < NT8; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // scale 0 makes NaN of a hidden score
+            if (!((vis0 >> (8 * n + e)) & 1u)) s[n][e] = 0.0f;
+            if (!((vis1 >> (8 * n + e)) & 1u)) s[n][2 + e] = 0.0f;
           }
-        }
-        wild = __any_sync(~0u, wild);
-      }
-      if (wild) {
+        if (drafts && a.n_q > 1) {
+          for (int x = lane; x < SUB * ROWB / 16; x += 32) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + x * 16) : "memory");
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll 1
-            for (int w = 0; w < 4; ++w) {  // token n * 8 + 2 w + e
-              const int kk = n * 8 + 2 * w + e, from = (lane & ~3) | w;
-              const float p0 = __shfl_sync(~0u, s[n][e], from), p1 = __shfl_sync(~0u, s[n][2 + e], from);
-              const bool v0 = __shfl_sync(~0u, (vis0 >> (8 * n + e)) & 1u, from);
-              const bool v1 = __shfl_sync(~0u, (vis1 >> (8 * n + e)) & 1u, from);
-#pragma unroll
-              for (int x = 0; x < D / 8; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int d = x * 8 + 2 * t4 + y;
-                  float v;
-                  if constexpr (BF) {
-                    uint16_t h;
-                    asm volatile("ld.shared.u16 %0, [%1];"
-                                 : "=h"(h) : "r"(vs + chunk_at<ROWB>(kk, d >> 3) + (d & 7) * 2) : "memory");
-                    v = bf16_bits_to_f32(h);
-                  } else {
-                    v = lds32(vs + chunk_at<ROWB>(kk, d >> 2) + (d & 3) * 4);
-                  }
-                  if (isfinite(v)) continue;
-                  if (v0) o[x][y] = fmaf(p0, v, o[x][y]);
-                  if (v1) o[x][2 + y] = fmaf(p1, v, o[x][2 + y]);
-                }
+            for (int y = 0; y < 4; ++y) {
+              wild |= (w[y] & 0x7f800000u) == 0x7f800000u;
+              if (BF) wild |= (w[y] & 0x7f80u) == 0x7f80u;
             }
+          }
+          wild = __any_sync(~0u, wild);
+        }
+        if (wild) {
+#pragma unroll
+          for (int n = 0; n < NT8; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll 1
+              for (int w = 0; w < 4; ++w) {  // token n * 8 + 2 w + e
+                const int kk = n * 8 + 2 * w + e, from = (lane & ~3) | w;
+                const float p0 = __shfl_sync(~0u, s[n][e], from), p1 = __shfl_sync(~0u, s[n][2 + e], from);
+                const bool v0 = __shfl_sync(~0u, (vis0 >> (8 * n + e)) & 1u, from);
+                const bool v1 = __shfl_sync(~0u, (vis1 >> (8 * n + e)) & 1u, from);
+#pragma unroll
+                for (int x = 0; x < DW / 8; ++x)
+#pragma unroll
+                  for (int y = 0; y < 2; ++y) {
+                    const int d = ds * DW + x * 8 + 2 * t4 + y;
+                    float v;
+                    if constexpr (BF) {
+                      uint16_t h;
+                      asm volatile("ld.shared.u16 %0, [%1];"
+                                   : "=h"(h) : "r"(vs + chunk_at<ROWB>(kk, d >> 3) + (d & 7) * 2) : "memory");
+                      v = bf16_bits_to_f32(h);
+                    } else {
+                      v = lds32(vs + chunk_at<ROWB>(kk, d >> 2) + (d & 3) * 4);
+                    }
+                    if (isfinite(v)) continue;
+                    if (v0) o[x][y] = fmaf(p0, v, o[x][y]);
+                    if (v1) o[x][2 + y] = fmaf(p1, v, o[x][2 + y]);
+                  }
+              }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT8; ++n) {
+        l0 += s[n][0] + s[n][1];
+        l1 += s[n][2] + s[n][3];
       }
       if constexpr (BF) {
-        uint32_t pf[PT][4];
+        const uint32_t vat = vs + chunk_at<ROWB>(lane & 15, lane >> 4);
+        uint32_t pf[NT8 / 2][PT][4];
 #pragma unroll
-        for (int x = 0; x < PT; ++x) {
-          pf[x][0] = take_bf16(s[0][0], s[0][1]);
-          pf[x][1] = take_bf16(s[0][2], s[0][3]);
-          pf[x][2] = take_bf16(s[1][0], s[1][1]);
-          pf[x][3] = take_bf16(s[1][2], s[1][3]);
-        }
+        for (int k = 0; k < NT8 / 2; ++k)
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t b[4];
-          ldsm4t(b, vs + chunk_at<ROWB>(lane & 15, 2 * n + (lane >> 4)));
-          if (wild) {
-#pragma unroll
-            for (int x = 0; x < 4; ++x) b[x] = finite_bf16(b[x]);
+          for (int x = 0; x < PT; ++x) {
+            pf[k][x][0] = take_bf16(s[2 * k][0], s[2 * k][1]);
+            pf[k][x][1] = take_bf16(s[2 * k][2], s[2 * k][3]);
+            pf[k][x][2] = take_bf16(s[2 * k + 1][0], s[2 * k + 1][1]);
+            pf[k][x][3] = take_bf16(s[2 * k + 1][2], s[2 * k + 1][3]);
           }
 #pragma unroll
-          for (int x = PT - 1; x >= 0; --x) {
-            mma_bf16(o[2 * n], pf[x], b[0], b[1]);
-            mma_bf16(o[2 * n + 1], pf[x], b[2], b[3]);
+        for (int n = 0; n < DW / 16; ++n)
+#pragma unroll
+          for (int k = 0; k < NT8 / 2; ++k) {
+            uint32_t b[4];
+            ldsm4t(b, DS == 1 ? chunk_from(vat + k * 16 * ROWB, 2 * n)
+                              : chunk_from(vat + k * 16 * ROWB + ds * (DW * C::ES), 2 * n));
+            if (wild) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) b[x] = finite_bf16(b[x]);
+            }
+#pragma unroll
+            for (int x = PT - 1; x >= 0; --x) {
+              mma_bf16(o[2 * n], pf[k][x], b[0], b[1]);
+              mma_bf16(o[2 * n + 1], pf[k][x], b[2], b[3]);
+            }
           }
-        }
       } else {
         // k index t4 | t4 + 4 of a product stands for token 2 t4 | 2 t4 + 1, as
         // the scores lie in registers
@@ -510,17 +580,17 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
           split_tf32(s[k][1], ph[k][2], pl[k][2]);
           split_tf32(s[k][3], ph[k][3], pl[k][3]);
         }
+        const uint32_t va = vs + ds * (DW * C::ES) + chunk_at<ROWB>(2 * t4, g >> 2) + (g & 3) * 4;
+        const uint32_t vb1 = vs + ds * (DW * C::ES) + chunk_at<ROWB>(2 * t4 + 1, g >> 2) + (g & 3) * 4;
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+        for (int n = 0; n < DW / 8; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int key_a = k * 8 + 2 * t4;
             uint32_t h0, w0, h1, w1;
-            float va = lds32(vs + chunk_at<ROWB>(key_a, 2 * n + (g >> 2)) + (g & 3) * 4);
-            float vc = lds32(vs + chunk_at<ROWB>(key_a + 1, 2 * n + (g >> 2)) + (g & 3) * 4);
-            if (wild) va = isfinite(va) ? va : 0.0f, vc = isfinite(vc) ? vc : 0.0f;
-            split_tf32(va, h0, w0);
-            split_tf32(vc, h1, w1);
+            float x0 = lds32(chunk_from(va + k * 8 * ROWB, 2 * n)), x1 = lds32(chunk_from(vb1 + k * 8 * ROWB, 2 * n));
+            if (wild) x0 = isfinite(x0) ? x0 : 0.0f, x1 = isfinite(x1) ? x1 : 0.0f;
+            split_tf32(x0, h0, w0);
+            split_tf32(x1, h1, w1);
             mma_tf32(o[n], pl[k], h0, h1);
             mma_tf32(o[n], ph[k], w0, w1);
             mma_tf32(o[n], ph[k], h0, h1);
@@ -538,15 +608,15 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     cp_wait<0>();
     __syncthreads();  // every slot is read
     {
-      const int row = kg * 16 * RT + rt * 16 + g;
+      const int row = kg * 16 * RT + rt * 16 + g, d = ds * DW + 2 * t4;
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        *reinterpret_cast<float2*>(merge + row * D + n * 8 + 2 * t4) = make_float2(o[n][0], o[n][1]);
-        *reinterpret_cast<float2*>(merge + (row + 8) * D + n * 8 + 2 * t4) = make_float2(o[n][2], o[n][3]);
+      for (int n = 0; n < DW / 8; ++n) {
+        *reinterpret_cast<float2*>(merge + row * D + n * 8 + d) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(merge + (row + 8) * D + n * 8 + d) = make_float2(o[n][2], o[n][3]);
       }
-      if (t4 == 0) {
-        merge_ml[row] = make_float2(m0, l0);
-        merge_ml[row + 8] = make_float2(m1, l1);
+      if (t4 == 0 && ds == 0) {
+        merge_ml[row] = make_float2(c0 == -INFINITY ? c0 : -z0, l0);
+        merge_ml[row + 8] = make_float2(c1 == -INFINITY ? c1 : -z1, l1);
       }
     }
     __syncthreads();
@@ -585,11 +655,11 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         if (d == 0) p.part_ml[part * 16 * RT + row] = make_float2(top, bad ? -1.0f : sum);
       }
     }
-    if (!whole) {
-      if (t0 == 0)
-        tail = int64_t(r) * per_req + it;
-      else
-        more = t1 < u;
+    if (!whole && t0 == 0) {
+      // the item's last unit lies in the range whose end is the first past it
+      const int64_t last = cur + u - 1;
+      split.x = int64_t(r) * per_req + it;
+      split.y = ((last + 1) * ranges - 1) / total - blockIdx.x + 1;
     }
     cur += t1 - t0;
     if (cur >= end) break;
@@ -603,7 +673,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     }
     __syncthreads();  // the join is read before the ring is filled again
   }
-  if (tid == 0) p.tail[blockIdx.x] = tail, p.more[blockIdx.x] = more;
+  if (tid == 0) p.split[blockIdx.x] = split;
 }
 
 template <class C, int PT>

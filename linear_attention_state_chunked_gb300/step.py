@@ -6,11 +6,12 @@ path's binding: caller's tensors, the C entry points' names, LinStateError."""
 from __future__ import annotations
 
 import ctypes
+import struct
 from typing import Optional
 
 import torch
 
-from . import _check, _stream, dtype_code, lib
+from . import LIN_BF16, LIN_F32, LinStateError, dtype_code, lib
 
 LIN_ST_BAD_PAGE = 512
 LIN_ACT_NONE, LIN_ACT_SILU, LIN_ACT_SIGMOID = 0, 1, 2
@@ -65,6 +66,42 @@ lib.lin_state_block_norm.argtypes = [_P(NormArgsT), _vp]
 lib.lin_state_block_norm.restype = ctypes.c_int
 
 
+# A decode step makes these calls once per layer, so what a call costs on the
+# host counts: the argument structures are packed in one go (a ctypes Structure
+# of 20 fields takes several times as long) and handed over as bytes.
+_CODE = {"c_int": "i", "c_long": "q", "c_longlong": "q", "c_void_p": "P", "c_float": "f"}
+
+
+def _packer(cls) -> struct.Struct:
+    p = struct.Struct("@" + "".join(_CODE[t.__name__] for _, t in cls._fields_))
+    assert p.size <= ctypes.sizeof(cls) < p.size + 8  # tail padding alone may differ
+    return struct.Struct(p.format + f"{ctypes.sizeof(cls) - p.size}x")
+
+
+_pack_append, _pack_attn, _pack_norm = (_packer(c).pack for c in (KVAppendArgsT, AttnArgsT, NormArgsT))
+
+
+def _entry(name, *argtypes):
+    f = lib[name]  # a handle of its own, with these argument types
+    f.argtypes, f.restype = argtypes, ctypes.c_int
+    return f
+
+
+_call_append = _entry("lin_state_kv_append", _vp, ctypes.c_char_p, _vp)
+_call_attn = _entry("lin_state_attn_decode", _vp, ctypes.c_char_p, _vp, ctypes.c_size_t, _vp)
+_call_norm = _entry("lin_state_block_norm", ctypes.c_char_p, _vp)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
+def _stream_of(stream, t: torch.Tensor):
+    """The given stream's handle, or that of the current stream of t's device."""
+    if stream is None:
+        if t.is_cuda and _raw_stream is not None:
+            return _raw_stream(t.get_device())
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 class KVCache:
     """The paged key-value cache: k, v torch tensors [layers][pages][page_size]
     [kv_heads][head_dim], allocated here (zeros) or given as views of any
@@ -85,43 +122,66 @@ class KVCache:
                                  f"got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
         if k.stride() != v.stride():
             raise ValueError(f"cache: k and v must have the same strides, got {k.stride()} and {v.stride()}")
-        self.k, self.v, self.dtype = k, v, dtype
+        self._k, self._v, self.dtype = k, v, dtype
         self.num_layers, self.num_pages, self.page_size = num_layers, num_pages, page_size
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
 
+        es, st = k.element_size(), k.stride()
+        self._desc = KVCacheT(num_layers, num_pages, page_size, num_kv_heads, head_dim,
+                              dtype_code(dtype), k.data_ptr(), v.data_ptr(),
+                              st[0] * es, st[1] * es, st[2] * es, st[3] * es)
+        self._addr = ctypes.addressof(self._desc)
+
+    @property
+    def k(self) -> torch.Tensor:
+        return self._k
+
+    @property
+    def v(self) -> torch.Tensor:
+        return self._v
+
     def desc(self) -> KVCacheT:
-        k, v = self.k, self.v
-        es = k.element_size()
-        s = k.stride()
-        return KVCacheT(self.num_layers, self.num_pages, self.page_size, self.num_kv_heads,
-                        self.head_dim, dtype_code(k.dtype), k.data_ptr(), v.data_ptr(),
-                        s[0] * es, s[1] * es, s[2] * es, s[3] * es)
+        return self._desc
 
 
-def _ptr32(t: Optional[torch.Tensor], name: str, shape):
-    """Address of a contiguous int32 tensor of this shape, or None."""
+_DT = {torch.float32: LIN_F32, torch.bfloat16: LIN_BF16}
+
+
+def _dt(dtype) -> int:
+    code = _DT.get(dtype)
+    return dtype_code(dtype) if code is None else code  # raises
+
+
+def _raise(rc: int, where: str):
+    raise LinStateError(rc, where)
+
+
+def _ptr32(t: Optional[torch.Tensor], name: str, shape) -> int:
+    """Address of a contiguous int32 tensor of this shape, or 0 for None."""
     if t is None:
-        return None
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        return 0
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous int32 tensor {shape}, got {tuple(t.shape)} of {t.dtype}")
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype):
-    """[B][n][heads][dim] with the heads of a token contiguous."""
-    if t.dim() != 4 or t.shape[2] != heads or t.shape[3] != dim or t.dtype != dtype:
-        raise ValueError(f"{name}: want [batch][n][{heads}][{dim}] of {dtype}, got {tuple(t.shape)} of {t.dtype}")
+    """Shape and strides of [B][n][heads][dim] with a token's heads contiguous."""
+    shape = t.shape
+    if len(shape) != 4 or shape[2] != heads or shape[3] != dim or t.dtype is not dtype:
+        raise ValueError(f"{name}: want [batch][n][{heads}][{dim}] of {dtype}, got {tuple(shape)} of {t.dtype}")
     s = t.stride()
     if s[3] != 1 or (heads > 1 and s[2] != dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {s}")
-    return s
+    return shape, s
 
 
 def _table(t: torch.Tensor, batch: int):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != batch or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, s = t.shape, t.stride()
+    if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and s[1] != 1):
         raise ValueError(f"page_table: want int32 [{batch}][max_pages] with contiguous rows, got "
-                         f"{tuple(t.shape)} of {t.dtype}")
-    return t.shape[1], t.stride(0)
+                         f"{tuple(shape)} of {t.dtype}")
+    return shape[1], t.data_ptr(), s[0]
 
 
 def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_tok=None,
@@ -131,19 +191,20 @@ def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_
     all n, the first n_tok[r], or the accepted path of a draft tree (parent
     [B][n], accept_node [B])."""
     H, D = cache.num_kv_heads, cache.head_dim
-    s = _rows(k, "k", H, D, cache.dtype)
-    if _rows(v, "v", H, D, cache.dtype) != s or v.shape != k.shape:
+    shape, s = _rows(k, "k", H, D, cache.dtype)
+    vshape, vs = _rows(v, "v", H, D, cache.dtype)
+    if vs != s or vshape != shape:
         raise ValueError("k and v must have the same shape and strides")
-    B, n = k.shape[0], k.shape[1]
-    es = k.element_size()
-    pages, pstride = _table(page_table, B)
-    a = KVAppendArgsT(layer, B, n, pages, k.data_ptr(), v.data_ptr(), s[0] * es, s[1] * es,
-                      page_table.data_ptr(), pstride, _ptr32(pos, "pos", (B,)),
-                      _ptr32(n_tok, "n_tok", (B,)), _ptr32(parent, "parent", (B, n)),
-                      _ptr32(accept_node, "accept_node", (B,)),
-                      None if status is None else status.data_ptr())
-    _check(lib.lin_state_kv_append(ctypes.byref(cache.desc()), ctypes.byref(a), _stream(stream)),
-           "lin_state_kv_append")
+    B, n = shape[0], shape[1]
+    es = 2 if cache.dtype is torch.bfloat16 else 4
+    pages, table, pstride = _table(page_table, B)
+    a = _pack_append(layer, B, n, pages, k.data_ptr(), v.data_ptr(), s[0] * es, s[1] * es, table, pstride,
+                     _ptr32(pos, "pos", (B,)), _ptr32(n_tok, "n_tok", (B,)),
+                     _ptr32(parent, "parent", (B, n)), _ptr32(accept_node, "accept_node", (B,)),
+                     0 if status is None else status.data_ptr())
+    rc = _call_append(cache._addr, a, _stream_of(stream, k))
+    if rc:
+        _raise(rc, "lin_state_kv_append")
 
 
 def lin_state_attn_workspace(cache: KVCache, *, batch: int, n_q: int, num_q_heads: int,
@@ -167,28 +228,51 @@ def lin_state_attn_decode(cache: KVCache, *, layer: int, q, out, page_table, kv_
     D = cache.head_dim
     if q.dim() != 4:
         raise ValueError(f"q: want [batch][n_q][q_heads][{D}], got {tuple(q.shape)}")
-    B, n, Hq, _ = q.shape
-    s = _rows(q, "q", Hq, D, cache.dtype)
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"out: want a contiguous tensor {tuple(q.shape)}, got {tuple(out.shape)}")
-    es = q.element_size()
-    pages, pstride = _table(page_table, B)
-    a = AttnArgsT(layer, B, n, Hq, dtype_code(out.dtype), pages,
-                  D ** -0.5 if scale is None else scale, q.data_ptr(), s[0] * es, s[1] * es,
-                  out.data_ptr(), page_table.data_ptr(), pstride, _ptr32(kv_len, "kv_len", (B,)),
-                  _ptr32(parent, "parent", (B, n)), None if status is None else status.data_ptr())
-    d = cache.desc()
+    shape, s = _rows(q, "q", q.shape[2], D, cache.dtype)
+    B, n, Hq, _ = shape
+    if out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out: want a contiguous tensor {tuple(shape)}, got {tuple(out.shape)}")
+    es = 2 if cache.dtype is torch.bfloat16 else 4
+    pages, table, pstride = _table(page_table, B)
+    a = _pack_attn(layer, B, n, Hq, _dt(out.dtype), pages, D ** -0.5 if scale is None else scale,
+                   q.data_ptr(), s[0] * es, s[1] * es, out.data_ptr(), table, pstride,
+                   _ptr32(kv_len, "kv_len", (B,)), _ptr32(parent, "parent", (B, n)),
+                   0 if status is None else status.data_ptr())
     if workspace is None:
-        need = int(lib.lin_state_attn_workspace(ctypes.byref(d), ctypes.byref(a)))
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            if stream is not None:  # freed here while the launch on `stream` may still run
-                workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                        else torch.cuda.ExternalStream(int(stream)))
-    ptr, size = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                     workspace.numel() * workspace.element_size())
-    _check(lib.lin_state_attn_decode(ctypes.byref(d), ctypes.byref(a), ptr, size, _stream(stream)),
-           "lin_state_attn_decode")
+        need = lin_state_attn_workspace(cache, batch=B, n_q=n, num_q_heads=Hq, max_pages=pages,
+                                        out_dtype=out.dtype)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None and need:  # freed here while the launch on `stream` may still run
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream)))
+    rc = _call_attn(cache._addr, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                    _stream_of(stream, q))
+    if rc:
+        _raise(rc, "lin_state_attn_decode")
+
+
+def _norm_row(t, name: str, shape, dtype):
+    """(address, row stride, dtype) of a [T][C] tensor, or of None."""
+    if t is None:
+        return 0, 0, dtype
+    s = t.stride()
+    if t.shape != shape or (s[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name}: want {list(shape)} with contiguous rows, got {tuple(t.shape)}, strides {s}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name}: gate, the weights and y must have one dtype, and residual and h_out "
+                         f"one: got {t.dtype} beside {dtype}")
+    return t.data_ptr(), s[0], t.dtype
+
+
+def _norm_weight(w, name: str, channels: Optional[int], dtype):
+    if w is None:
+        return 0, dtype
+    if w.dim() != 1 or not w.is_contiguous() or (channels is not None and w.shape[0] != channels):
+        raise ValueError(f"{name}: want a contiguous vector{'' if channels is None else f' of {channels}'}, "
+                         f"got {tuple(w.shape)}")
+    if dtype is not None and w.dtype is not dtype:
+        raise ValueError(f"{name}: gate, the weights and y must have one dtype, got {w.dtype} beside {dtype}")
+    return w.data_ptr(), w.dtype
 
 
 def lin_state_block_norm(*, x, gate=None, gate_act: Optional[str] = None, w_post=None,
@@ -198,44 +282,23 @@ def lin_state_block_norm(*, x, gate=None, gate_act: Optional[str] = None, w_post
     t = x, normed over groups of w_post.numel() channels, times act(gate)
     ("silu" / "sigmoid"); h_out = residual + scale * scale_w * t;
     y = the norm of h over the row, times w_pre. Every part but x is optional."""
-    if x.dim() != 2:
-        raise ValueError(f"x: want [rows][channels], got {tuple(x.shape)}")
-    T, C = x.shape
-    if gate_act not in _ACTS:
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: want [rows][channels], got {tuple(shape)}")
+    T, C = shape
+    act = _ACTS.get(gate_act)
+    if act is None:
         raise ValueError(f"gate_act: want None, 'silu' or 'sigmoid', got {gate_act!r}")
-    io = hd = None
-    ptr, stride = [], []
-    for name, t in (("x", x), ("gate", gate), ("residual", residual), ("h_out", h_out), ("y", y)):
-        if t is None:
-            ptr.append(None)
-            stride.append(0)
-            continue
-        if t.shape != x.shape or (C > 1 and t.stride(1) != 1):
-            raise ValueError(f"{name}: want [{T}][{C}] with contiguous rows, got {tuple(t.shape)}, "
-                             f"strides {t.stride()}")
-        if name in ("gate", "y"):
-            if io is not None and t.dtype != io:
-                raise ValueError(f"gate, the weights and y must have one dtype, got {io} and {t.dtype}")
-            io = t.dtype
-        elif name != "x":
-            if hd is not None and t.dtype != hd:
-                raise ValueError(f"residual and h_out must have one dtype, got {hd} and {t.dtype}")
-            hd = t.dtype
-        ptr.append(t.data_ptr())
-        stride.append(t.stride(0))
-    weights = []
-    for name, w in (("w_post", w_post), ("scale_w", scale_w), ("w_pre", w_pre)):
-        if w is None:
-            weights.append(None)
-            continue
-        if w.dim() != 1 or not w.is_contiguous() or (name != "w_post" and w.numel() != C):
-            raise ValueError(f"{name}: want a contiguous vector"
-                             f"{'' if name == 'w_post' else f' of {C}'}, got {tuple(w.shape)}")
-        if io is not None and w.dtype != io:
-            raise ValueError(f"gate, the weights and y must have one dtype, got {io} and {w.dtype}")
-        io = w.dtype
-        weights.append(w.data_ptr())
-    a = NormArgsT(T, C, w_post.numel() if w_post is not None else 0, dtype_code(x.dtype),
-                  dtype_code(io or x.dtype), dtype_code(hd or x.dtype), _ACTS[gate_act], eps, scale,
-                  ptr[0], ptr[1], weights[0], ptr[2], weights[1], weights[2], ptr[3], ptr[4], *stride)
-    _check(lib.lin_state_block_norm(ctypes.byref(a), _stream(stream)), "lin_state_block_norm")
+    px, sx, xd = _norm_row(x, "x", shape, None)
+    pg, sg, io = _norm_row(gate, "gate", shape, None)
+    py, sy, io = _norm_row(y, "y", shape, io)
+    pr, sr, hd = _norm_row(residual, "residual", shape, None)
+    ph, sh, hd = _norm_row(h_out, "h_out", shape, hd)
+    pw, io = _norm_weight(w_post, "w_post", None, io)
+    ps, io = _norm_weight(scale_w, "scale_w", C, io)
+    pp, io = _norm_weight(w_pre, "w_pre", C, io)
+    a = _pack_norm(T, C, w_post.shape[0] if w_post is not None else 0, _dt(xd), _dt(io or xd), _dt(hd or xd),
+                   act, eps, scale, px, pg, pw, pr, ps, pp, ph, py, sx, sg, sr, sh, sy)
+    rc = _call_norm(a, _stream_of(stream, x))
+    if rc:
+        _raise(rc, "lin_state_block_norm")
