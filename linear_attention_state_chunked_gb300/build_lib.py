@@ -22,7 +22,7 @@ LIB = os.path.join(PKG, "liblinstate.so")
 # step_api.cu holds api.cu, whose checks and error text it shares
 SOURCES = ["step_api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
            "selftest.cu", "kv_cache.cu", "attn_decode.cu", "attn_d64.cu", "attn_d128.cu",
-           "attn_d256.cu", "block_norm.cu"]
+           "attn_d256.cu", "attn_umma_d64.cu", "attn_umma_d128.cu", "attn_umma_d256.cu", "block_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

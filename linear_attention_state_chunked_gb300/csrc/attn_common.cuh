@@ -1,0 +1,245 @@
+// What the kernels of decode attention share: the plan of a call, the split of
+// a batch's work over the CTAs, and the end of a piece of work.
+//
+// A unit is kUnit tokens of one item = (request, kv head, block of rows). The
+// units of the whole batch, laid end to end, are cut into one equal range per
+// CTA (lengths are read on the device), so a batch of ragged lengths and a
+// single long request load the SMs alike. An item inside one range is finished
+// there; one that crosses a border leaves (value sums, m, sum) of each piece in
+// the workspace, and a second kernel joins them in range order, so results do
+// not depend on timing.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "step_internal.h"
+#include "umma.cuh"
+
+namespace lin {
+namespace attn {
+
+constexpr float kSlack = 8.0f;
+constexpr int kUnit = 64;  // tokens of a work unit
+
+struct Plan {
+  lin_kv_cache_t c;
+  lin_attn_args_t a;
+  int group;          // query heads per key-value head
+  int rows;           // n_q * group
+  int block_rows;     // rows of an item
+  int row_blocks;     // items of one (request, kv head)
+  float scale_log2;   // |scale| log2(e); q is negated where scale < 0
+  uint32_t negate;
+  float slack;        // kSlack in units of q.k
+  uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, mul) + t) >> shift, t < 2^31
+  float* part;        // [2 grid][block_rows][D] value sums of unfinished pieces
+  float2* part_ml;    // [2 grid][block_rows] their (maximum, sum); sum -1: left out
+  longlong2* split;   // [grid] the item that begins in range c and goes on past
+                      // it (or -1), and its number of parts
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// the next bf16 part of a pair of weights; the pair keeps what is left
+__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  a -= __low2float(h);
+  b -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Units of a request: at least one where it has an output to write.
+__device__ __forceinline__ int units_of(int len, int64_t most) {
+  return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
+}
+
+// Where a CTA is in its range.
+struct Walk {
+  int64_t cur, end, total, ranges;
+  int64_t most;   // longest request allowed
+  int per_req;    // items of a request
+  int r, len, u;  // the request, its length and units
+  int it, t0;     // its item, and the item's first unit here
+  longlong2 split;
+};
+
+// The CTA's range, from a scan over the requests' lengths by all NT threads.
+// False where there is no work for it.
+template <int NT>
+__device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_scan)[NT / 32], int64_t (&s_first)[2]) {
+  const lin_attn_args_t& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // token indices stay clear of the 32-bit end
+  w.most = min(int64_t(a.max_pages) * p.c.page_size, int64_t(INT32_MAX - 65536));
+  w.per_req = p.c.num_kv_heads * p.row_blocks;
+  w.split = make_longlong2(-1, 0);
+  const int span = (a.batch + NT - 1) / NT;
+  const int r0 = min(a.batch, tid * span), r1 = min(a.batch, r0 + span);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const int len = a.kv_len[r];
+    if (len > w.most && blockIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
+    mine += units_of(len, w.most);
+  }
+  mine *= w.per_req;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) s_scan[warp] = upto;
+  __syncthreads();
+  w.total = 0;
+#pragma unroll
+  for (int x = 0; x < NT / 32; ++x) {
+    if (x < warp) upto += s_scan[x];
+    w.total += s_scan[x];
+  }
+  w.ranges = w.total < gridDim.x ? w.total : gridDim.x;
+  if (blockIdx.x >= w.ranges) {
+    if (tid == 0) p.split[blockIdx.x].x = -1;
+    return false;
+  }
+  w.cur = w.total * blockIdx.x / w.ranges;
+  w.end = w.total * (blockIdx.x + 1) / w.ranges;
+  if (w.cur >= upto - mine && w.cur < upto) {
+    int64_t at = upto - mine;
+    int r = r0;
+    for (;; ++r) {
+      const int64_t n = int64_t(units_of(a.kv_len[r], w.most)) * w.per_req;
+      if (w.cur < at + n) break;
+      at += n;
+    }
+    s_first[0] = r;
+    s_first[1] = w.cur - at;
+  }
+  __syncthreads();
+  w.r = static_cast<int>(s_first[0]);
+  w.len = a.kv_len[w.r];
+  w.u = units_of(w.len, w.most);
+  w.it = static_cast<int>(s_first[1] / w.u);
+  w.t0 = static_cast<int>(s_first[1] % w.u);
+  return true;
+}
+
+// The piece's end: the first unit past it.
+__device__ __forceinline__ int walk_until(const Walk& w) {
+  return static_cast<int>(min(int64_t(w.u), w.t0 + (w.end - w.cur)));
+}
+
+// On to the next piece; false at the range's end.
+__device__ __forceinline__ bool walk_next(const Plan& p, Walk& w, int t1) {
+  if (w.t0 == 0 && t1 < w.u) {
+    // the item goes on: its last unit lies in the range whose end is the first past it
+    const int64_t last = w.cur + w.u - 1;
+    w.split.x = int64_t(w.r) * w.per_req + w.it;
+    w.split.y = ((last + 1) * w.ranges - 1) / w.total - blockIdx.x + 1;
+  }
+  w.cur += t1 - w.t0;
+  if (w.cur >= w.end) return false;
+  w.t0 = 0;
+  if (++w.it == w.per_req) {
+    w.it = 0;
+    do {
+      w.len = p.a.kv_len[++w.r];
+      w.u = units_of(w.len, w.most);
+    } while (w.u == 0);
+  }
+  return true;
+}
+
+// What each draft sees of the drafts, by one warp: lane j's set goes to see[j].
+__device__ __forceinline__ void draft_sets(const Plan& p, int r, uint32_t (&see)[32], int& bad_out) {
+  const lin_attn_args_t& a = p.a;
+  const int lane = threadIdx.x & 31;
+  uint32_t set = (2u << lane) - 1u;
+  bool bad = false;
+  if (a.parent) {
+    const int par = lane < a.n_q ? a.parent[int64_t(r) * a.n_q + lane] : -1;
+    bad = __any_sync(~0u, lane < a.n_q && (par < -1 || par >= lane));
+    set = 1u << lane;
+    if (!bad)
+      // parents come first: in n_q rounds every node has its parent's set
+      for (int j = 0; j < a.n_q; ++j) {
+        const uint32_t s = __shfl_sync(~0u, set, j);
+        if (par == j) set |= s;
+      }
+  }
+  see[lane] = set;
+  if (lane == 0) {
+    bad_out = bad;
+    if (bad) report(a.status, LIN_ST_BAD_TREE);
+  }
+}
+
+// Joins the KG value sums [KG][ROWS][PITCH >= D] and (m, sum) [KG][ROWS] of a piece in
+// shared memory and writes the outputs of a whole item, or the piece's part.
+// All NT threads.
+template <int D, int KG, int ROWS, int NT, int PITCH = D>
+__device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t1, const float* merge,
+                                             const float2* merge_ml, bool bad) {
+  const lin_attn_args_t& a = p.a;
+  const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * ROWS;
+  const bool whole = w.t0 == 0 && t1 == w.u;
+  const int64_t part = 2 * int64_t(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+  for (int x = threadIdx.x; x < ROWS * (D / 4); x += NT) {
+    const int row = x / (D / 4), d = (x % (D / 4)) * 4, q = row0 + row;
+    if (q >= p.rows) continue;
+    float top = -INFINITY, sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) top = fmaxf(top, merge_ml[k * ROWS + row].x);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+      const float2 ml = merge_ml[k * ROWS + row];
+      if (ml.y == 0.0f) continue;  // saw nothing (a NaN sum goes on)
+      const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+      const float4 y = *reinterpret_cast<const float4*>(merge + (k * ROWS + row) * PITCH + d);
+      sum = fmaf(f, ml.y, sum);
+      v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
+      v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
+    }
+    if (whole) {
+      if (bad) continue;
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int64_t at = ((int64_t(w.r) * a.n_q + q / p.group) * a.num_q_heads + hk * p.group + q % p.group) * D + d;
+      if (a.out_dtype == LIN_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      }
+    } else {
+      *reinterpret_cast<float4*>(p.part + (part * ROWS + row) * D + d) = v;
+      if (d == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? -1.0f : sum);
+    }
+  }
+}
+
+// t / page_size
+__device__ __forceinline__ int page_of(const Plan& p, int t) { return (__umulhi(t, p.page_mul) + t) >> p.page_shift; }
+
+// One translation unit per head_dim and kind of kernel.
+cudaError_t launch_d64(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+cudaError_t launch_d128(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+cudaError_t launch_d256(const Plan& p, int row_tiles, int grid, cudaStream_t s);
+cudaError_t launch_umma_d64(const Plan& p, int grid, cudaStream_t s);
+cudaError_t launch_umma_d128(const Plan& p, int grid, cudaStream_t s);
+cudaError_t launch_umma_d256(const Plan& p, int grid, cudaStream_t s);
+
+}  // namespace attn
+}  // namespace lin

@@ -14,7 +14,7 @@ constexpr int kJoinRows = 16;  // most rows side by side in the grid
 // and goes on past it. Its parts, in token order: 2c + 1, then 2c' of the ranges
 // c' = c + 1, ... The warps take every eighth part and are joined in shared
 // memory, always in the same order.
-template <int D, int RT>
+template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   constexpr int V = D / 32;
   __shared__ float s_v[kJoinWarps][D], s_sum[kJoinWarps];
@@ -28,10 +28,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   const int64_t head = item / p.row_blocks;
   const int hk = static_cast<int>(head % p.c.num_kv_heads);
   const int64_t r = head / p.c.num_kv_heads;
-  for (int row = blockIdx.y; row < 16 * RT; row += gridDim.y) {
-    const int q = rb * 16 * RT + row;
+  for (int row = blockIdx.y; row < p.block_rows; row += gridDim.y) {
+    const int q = rb * p.block_rows + row;
     if (q >= p.rows) return;
-    auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * 16 * RT + row; };
+    auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * p.block_rows + row; };
     float top = -INFINITY;
     bool out = false;
     for (int i = lane; i < parts; i += 32) {
@@ -85,46 +85,51 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   }
 }
 
-// 16-row tiles of a row block: each warp of a group owns one.
-int row_tiles(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Which kernel a call takes, the rows of its items and its CTAs per SM.
+struct Shape {
+  bool umma;
+  int block_rows, ctas;
+};
 
-template <int D, int DT>
-int ctas(int rt) {
-  return rt == 1 ? Cfg<D, DT, 1>::CTAS : rt == 2 ? Cfg<D, DT, 2>::CTAS : Cfg<D, DT, 4>::CTAS;
+template <int D>
+int ctas_of(bool bf16, int rt) {
+  return bf16      ? Cfg<D, LIN_BF16, 1>::CTAS
+         : rt == 1 ? Cfg<D, LIN_F32, 1>::CTAS
+         : rt == 2 ? Cfg<D, LIN_F32, 2>::CTAS
+                   : Cfg<D, LIN_F32, 4>::CTAS;
+}
+
+// bf16 caches: up to 16 rows per (request, kv head) on warp-level MMA, more on
+// tcgen05 in blocks of 32, 64 or 128. fp32 caches: warp-level MMA in blocks of 16,
+// 32 or 64.
+Shape shape_of(const lin_kv_cache_t& c, int rows) {
+  const bool b = c.dtype == LIN_BF16;
+  if (b && rows > 16) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1};
+  const int rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt)};
 }
 
 // CTAs of the main kernel: what is resident at once, or one per unit where the
 // longest request allowed would give fewer.
-int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a, const Shape& f) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
   if (sms <= 0) sms = 152;  // no device: the size of a GB300
-  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads), rt = row_tiles(rows);
-  const bool b = c.dtype == LIN_BF16;
-  const int per = c.head_dim == 64    ? (b ? ctas<64, LIN_BF16>(rt) : ctas<64, LIN_F32>(rt))
-                  : c.head_dim == 128 ? (b ? ctas<128, LIN_BF16>(rt) : ctas<128, LIN_F32>(rt))
-                                      : (b ? ctas<256, LIN_BF16>(rt) : ctas<256, LIN_F32>(rt));
-  const int64_t blocks = (rows + 16 * rt - 1) / (16 * rt);
+  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads);
+  const int64_t blocks = (rows + f.block_rows - 1) / f.block_rows;
   const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
   const int64_t items = int64_t(a.batch) * c.num_kv_heads * blocks;
   const int64_t most = units > 1 && items < INT32_MAX ? items * units : items;
-  return static_cast<int>(most < int64_t(sms) * per && most > 0 ? most : int64_t(sms) * per);
-}
-
-template <int D>
-cudaError_t launch_join(const cudaLaunchConfig_t& cfg, int rt, const Plan& p) {
-  return rt == 1   ? cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p)
-         : rt == 2 ? cudaLaunchKernelEx(&cfg, join_kernel<D, 2>, p)
-                   : cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, p);
+  return static_cast<int>(most < int64_t(sms) * f.ctas && most > 0 ? most : int64_t(sms) * f.ctas);
 }
 
 }  // namespace
 }  // namespace attn
 
 size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
-  const size_t grid = attn::grid_of(c, a);
-  const size_t rows = 16 * attn::row_tiles(a.n_q * (a.num_q_heads / c.num_kv_heads));
-  return 2 * grid * rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
+  const attn::Shape f = attn::shape_of(c, a.n_q * (a.num_q_heads / c.num_kv_heads));
+  const size_t grid = attn::grid_of(c, a, f);
+  return 2 * grid * f.block_rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
 }
 
 cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a, void* ws, cudaStream_t s) {
@@ -133,8 +138,10 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.a = a;
   p.group = a.num_q_heads / c.num_kv_heads;
   p.rows = a.n_q * p.group;
-  const int rt = attn::row_tiles(p.rows), grid = attn::grid_of(c, a);
-  p.row_blocks = (p.rows + 16 * rt - 1) / (16 * rt);
+  const attn::Shape f = attn::shape_of(c, p.rows);
+  const int grid = attn::grid_of(c, a, f);
+  p.block_rows = f.block_rows;
+  p.row_blocks = (p.rows + f.block_rows - 1) / f.block_rows;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;  // log2(e)
   p.slack = attn::kSlack / p.scale_log2;  // infinite where scale is 0: one reference does
   p.negate = !(a.scale < 0.0f) ? 0u : c.dtype == LIN_BF16 ? 0x80008000u : 0x80000000u;
@@ -145,13 +152,20 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.page_mul = static_cast<uint32_t>((((uint64_t(1) << p.page_shift) - c.page_size) << 32) / c.page_size + 1);
   char* w = static_cast<char*>(ws);
   p.part = reinterpret_cast<float*>(w);
-  w += size_t(2) * grid * 16 * rt * c.head_dim * sizeof(float);
+  w += size_t(2) * grid * f.block_rows * c.head_dim * sizeof(float);
   p.part_ml = reinterpret_cast<float2*>(w);
-  w += size_t(2) * grid * 16 * rt * sizeof(float2);
+  w += size_t(2) * grid * f.block_rows * sizeof(float2);
   p.split = reinterpret_cast<longlong2*>(w);
-  cudaError_t e = c.head_dim == 64    ? attn::launch_d64(p, rt, grid, s)
-                  : c.head_dim == 128 ? attn::launch_d128(p, rt, grid, s)
-                                      : attn::launch_d256(p, rt, grid, s);
+  const int rt = f.block_rows / 16;
+  cudaError_t e;
+  if (f.umma)
+    e = c.head_dim == 64    ? attn::launch_umma_d64(p, grid, s)
+        : c.head_dim == 128 ? attn::launch_umma_d128(p, grid, s)
+                            : attn::launch_umma_d256(p, grid, s);
+  else
+    e = c.head_dim == 64    ? attn::launch_d64(p, rt, grid, s)
+        : c.head_dim == 128 ? attn::launch_d128(p, rt, grid, s)
+                            : attn::launch_d256(p, rt, grid, s);
   if (e != cudaSuccess) return e;
   // the join's launch overlaps the main kernel, and it waits there for its end
   cudaLaunchAttribute attr[1];
@@ -163,9 +177,9 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return c.head_dim == 64    ? attn::launch_join<64>(cfg, rt, p)
-         : c.head_dim == 128 ? attn::launch_join<128>(cfg, rt, p)
-                             : attn::launch_join<256>(cfg, rt, p);
+  return c.head_dim == 64    ? cudaLaunchKernelEx(&cfg, attn::join_kernel<64>, p)
+         : c.head_dim == 128 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<128>, p)
+                             : cudaLaunchKernelEx(&cfg, attn::join_kernel<256>, p);
 }
 
 }  // namespace lin

@@ -29,33 +29,10 @@
 // the length, or in a bad page, are filled with zeros and masked.
 #pragma once
 
-#include <math.h>
-
-#include "common.cuh"
-#include "step_internal.h"
-#include "umma.cuh"
+#include "attn_common.cuh"
 
 namespace lin {
 namespace attn {
-
-constexpr float kSlack = 8.0f;
-constexpr int kUnit = 64;  // tokens of a work unit
-
-struct Plan {
-  lin_kv_cache_t c;
-  lin_attn_args_t a;
-  int group;          // query heads per key-value head
-  int rows;           // n_q * group
-  int row_blocks;     // of 16 RT rows
-  float scale_log2;   // |scale| log2(e); q is negated where scale < 0
-  uint32_t negate;
-  float slack;        // kSlack in units of q.k
-  uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, mul) + t) >> shift, t < 2^31
-  float* part;        // [2 grid][16 RT][D] value sums of unfinished pieces
-  float2* part_ml;    // [2 grid][16 RT] their (maximum, sum); sum -1: left out
-  longlong2* split;   // [grid] the item that begins in range c and goes on past
-                      // it (or -1), and its number of parts
-};
 
 // Warps of one CTA: KG groups x RT row tiles x DS parts of head_dim. DS 2 halves
 // a warp's value sums (it computes the scores twice) where rows of 256 channels
@@ -87,14 +64,6 @@ struct Cfg {
   static_assert(S >= 2 && SMEM >= KG * RT * 16 * (D + 2) * 4, "");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 template <int GT>
 __device__ __forceinline__ void group_sync(int kg) {
   if constexpr (GT == 32)
@@ -125,11 +94,6 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // x = hi + lo in two tf32 values of 11 significant bits, each rounded to nearest
 // (the unit reads the upper 19 bits of an operand), so the pair is off by at
 // most 2^-22 of x. Integer additions: the conversion instruction is slower.
@@ -137,14 +101,6 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
 }
-// the next bf16 part of a pair of weights; the pair keeps what is left
-__device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  a -= __low2float(h);
-  b -= __high2float(h);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // a pair of bf16 values with 0 for infinities and NaN
 __device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
   if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
@@ -164,11 +120,6 @@ __device__ __forceinline__ uint32_t chunk_from(uint32_t at, int c) {
   return (at ^ ((c & 7) << 4)) + (c >> 3) * 128;
 }
 
-// Units of a request: at least one where it has an output to write.
-__device__ __forceinline__ int units_of(int len, int64_t most) {
-  return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
-}
-
 template <class C, int PT>
 __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p) {
   constexpr int D = C::D, RT = C::RT, DS = C::DS, KG = C::KG, S = C::S, NT = C::NW * 32, ROWB = C::ROWB;
@@ -186,59 +137,8 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   const int g = lane >> 2, t4 = lane & 3;
   const lin_kv_cache_t& c = p.c;
   const lin_attn_args_t& a = p.a;
-  const int per_req = c.num_kv_heads * p.row_blocks;
-  // token indices stay clear of the 32-bit end
-  const int64_t most = min(int64_t(a.max_pages) * c.page_size, int64_t(INT32_MAX - 65536));
-
-  // ---- this CTA's range of units: a scan over the requests' lengths ----------
-  const int span = (a.batch + NT - 1) / NT;
-  const int r0 = min(a.batch, tid * span), r1 = min(a.batch, r0 + span);
-  int64_t mine = 0;
-  for (int r = r0; r < r1; ++r) {
-    const int len = a.kv_len[r];
-    if (len > most && blockIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
-    mine += units_of(len, most);
-  }
-  mine *= per_req;
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(~0u, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) s_scan[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < C::NW; ++w) {
-    if (w < warp) upto += s_scan[w];
-    total += s_scan[w];
-  }
-  const int64_t ranges = total < gridDim.x ? total : gridDim.x;
-  if (blockIdx.x >= ranges) {
-    if (tid == 0) p.split[blockIdx.x].x = -1;
-    return;
-  }
-  int64_t cur = total * blockIdx.x / ranges;
-  const int64_t end = total * (blockIdx.x + 1) / ranges;
-  if (cur >= upto - mine && cur < upto) {
-    int64_t at = upto - mine;
-    int r = r0;
-    for (;; ++r) {
-      const int64_t n = int64_t(units_of(a.kv_len[r], most)) * per_req;
-      if (cur < at + n) break;
-      at += n;
-    }
-    s_first[0] = r;
-    s_first[1] = cur - at;
-  }
-  __syncthreads();
-  int r = static_cast<int>(s_first[0]);
-  int len = a.kv_len[r];
-  int u = units_of(len, most);
-  int it = static_cast<int>(s_first[1] / u);    // item of the request
-  int t0 = static_cast<int>(s_first[1] % u);    // its first unit here
-  longlong2 split = make_longlong2(-1, 0);
+  Walk w;
+  if (!walk_begin<NT>(p, w, s_scan, s_first)) return;
 
   const uint32_t ring = umma::smem_u32(smem) + kg * (S * C::SLOT);
   const uint32_t qs = umma::smem_u32(smem) + C::RING;
@@ -246,10 +146,10 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   float2* merge_ml = reinterpret_cast<float2*>(merge + KG * 16 * RT * D);  // [KG][16 RT]
 
   while (true) {
-    const int t1 = static_cast<int>(min(int64_t(u), t0 + (end - cur)));
-    const int hk = it / p.row_blocks, row0 = (it % p.row_blocks) * 16 * RT;
-    const int key_begin = t0 * kUnit, key_end = t1 == u ? len : t1 * kUnit;
-    const int base = len - a.n_q;  // tokens that every query sees
+    const int t1 = walk_until(w), r = w.r;
+    const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * 16 * RT;
+    const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
+    const int base = w.len - a.n_q;  // tokens that every query sees
     const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
     const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
     const int32_t* table = a.page_table + r * a.page_table_stride;
@@ -260,7 +160,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     int key = key_begin + kg * SUB + (lane & (SUB - 1));
     int in_page = 0, id = -1;
     auto look = [&]() {  // page id of the next slot's token
-      const uint32_t page = (__umulhi(key, p.page_mul) + key) >> p.page_shift;
+      const int page = page_of(p, key);
       in_page = key - page * c.page_size;
       id = key < key_end ? table[page] : -1;
     };
@@ -311,26 +211,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         }
         *reinterpret_cast<uint4*>(dst) = v;
       }
-      if (warp == 0) {
-        uint32_t see = (2u << lane) - 1u;
-        bool bad = false;
-        if (a.parent) {
-          const int par = lane < a.n_q ? a.parent[int64_t(r) * a.n_q + lane] : -1;
-          bad = __any_sync(~0u, lane < a.n_q && (par < -1 || par >= lane));
-          see = 1u << lane;
-          if (!bad)
-            // parents come first: in n_q rounds every node has its parent's set
-            for (int j = 0; j < a.n_q; ++j) {
-              const uint32_t s = __shfl_sync(~0u, see, j);
-              if (par == j) see |= s;
-            }
-        }
-        s_see[lane] = see;
-        if (lane == 0) {
-          s_bad = bad;
-          if (bad) report(a.status, LIN_ST_BAD_TREE);
-        }
-      }
+      if (warp == 0) draft_sets(p, r, s_see, s_bad);
     }
     __syncthreads();
     const bool bad = s_bad;
@@ -452,9 +333,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       // most slots need neither the rows' maximum nor a rescaling of the sums.
       if (__any_sync(~0u, mx0 > c0 || mx1 > c1)) {
 #pragma unroll
-        for (int w = 1; w < 4; w <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, w));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, w));
+        for (int o2 = 1; o2 < 4; o2 <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(~0u, mx0, o2));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(~0u, mx1, o2));
         }
         // z = -m scale_log2, 0 while a row has seen nothing
         if (mx0 > c0) {
@@ -509,8 +390,8 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll 1
-              for (int w = 0; w < 4; ++w) {  // token n * 8 + 2 w + e
-                const int kk = n * 8 + 2 * w + e, from = (lane & ~3) | w;
+              for (int pair = 0; pair < 4; ++pair) {  // token n * 8 + 2 pair + e
+                const int kk = n * 8 + 2 * pair + e, from = (lane & ~3) | pair;
                 const float p0 = __shfl_sync(~0u, s[n][e], from), p1 = __shfl_sync(~0u, s[n][2 + e], from);
                 const bool v0 = __shfl_sync(~0u, (vis0 >> (8 * n + e)) & 1u, from);
                 const bool v1 = __shfl_sync(~0u, (vis1 >> (8 * n + e)) & 1u, from);
@@ -601,9 +482,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
 
     // ---- join the groups ---------------------------------------------------------
 #pragma unroll
-    for (int w = 1; w < 4; w <<= 1) {
-      l0 += __shfl_xor_sync(~0u, l0, w);
-      l1 += __shfl_xor_sync(~0u, l1, w);
+    for (int o2 = 1; o2 < 4; o2 <<= 1) {
+      l0 += __shfl_xor_sync(~0u, l0, o2);
+      l1 += __shfl_xor_sync(~0u, l1, o2);
     }
     cp_wait<0>();
     __syncthreads();  // every slot is read
@@ -620,60 +501,11 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       }
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == u;
-    const int64_t part = 2 * int64_t(blockIdx.x) + (t0 == 0 ? 1 : 0);
-    for (int x = tid; x < 16 * RT * (D / 4); x += NT) {
-      const int row = x / (D / 4), d = (x % (D / 4)) * 4, q = row0 + row;
-      if (q >= p.rows) continue;
-      float top = -INFINITY, sum = 0.0f;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < KG; ++k) top = fmaxf(top, merge_ml[k * 16 * RT + row].x);
-#pragma unroll
-      for (int k = 0; k < KG; ++k) {
-        const float2 ml = merge_ml[k * 16 * RT + row];
-        if (ml.y == 0.0f) continue;  // saw nothing (a NaN sum goes on)
-        const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-        const float4 w = *reinterpret_cast<const float4*>(merge + (k * 16 * RT + row) * D + d);
-        sum = fmaf(f, ml.y, sum);
-        v.x = fmaf(f, w.x, v.x), v.y = fmaf(f, w.y, v.y);
-        v.z = fmaf(f, w.z, v.z), v.w = fmaf(f, w.w, v.w);
-      }
-      if (whole) {
-        if (bad) continue;
-        const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const int64_t at = ((int64_t(r) * a.n_q + q / p.group) * a.num_q_heads + hk * p.group + q % p.group) * D + d;
-        if (a.out_dtype == LIN_F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-        } else {
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        }
-      } else {
-        *reinterpret_cast<float4*>(p.part + (part * 16 * RT + row) * D + d) = v;
-        if (d == 0) p.part_ml[part * 16 * RT + row] = make_float2(top, bad ? -1.0f : sum);
-      }
-    }
-    if (!whole && t0 == 0) {
-      // the item's last unit lies in the range whose end is the first past it
-      const int64_t last = cur + u - 1;
-      split.x = int64_t(r) * per_req + it;
-      split.y = ((last + 1) * ranges - 1) / total - blockIdx.x + 1;
-    }
-    cur += t1 - t0;
-    if (cur >= end) break;
-    t0 = 0;
-    if (++it == per_req) {
-      it = 0;
-      do {
-        len = a.kv_len[++r];
-        u = units_of(len, most);
-      } while (u == 0);
-    }
+    finish_piece<D, KG, 16 * RT, NT>(p, w, t1, merge, merge_ml, bad);
+    if (!walk_next(p, w, t1)) break;
     __syncthreads();  // the join is read before the ring is filled again
   }
-  if (tid == 0) p.split[blockIdx.x] = split;
+  if (tid == 0) p.split[blockIdx.x] = w.split;
 }
 
 template <class C, int PT>
@@ -694,19 +526,14 @@ cudaError_t launch_main(const Plan& p, int grid, cudaStream_t s) {
 
 template <int D, int DT>
 cudaError_t launch_rows(const Plan& p, int row_tiles, int grid, cudaStream_t s) {
-  constexpr int PT3 = DT == LIN_BF16 ? 3 : 1, PT2 = DT == LIN_BF16 ? 2 : 1;
-  const bool f32 = p.a.out_dtype == LIN_F32;
-  switch (row_tiles) {
-    case 1: return f32 ? launch_main<Cfg<D, DT, 1>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 1>, PT2>(p, grid, s);
-    case 2: return f32 ? launch_main<Cfg<D, DT, 2>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 2>, PT2>(p, grid, s);
-    default: return f32 ? launch_main<Cfg<D, DT, 4>, PT3>(p, grid, s) : launch_main<Cfg<D, DT, 4>, PT2>(p, grid, s);
+  if constexpr (DT == LIN_BF16) {  // one row tile; more rows take the kernels of attn_umma.cuh
+    return p.a.out_dtype == LIN_F32 ? launch_main<Cfg<D, DT, 1>, 3>(p, grid, s) : launch_main<Cfg<D, DT, 1>, 2>(p, grid, s);
+  } else {
+    return row_tiles == 1   ? launch_main<Cfg<D, DT, 1>, 1>(p, grid, s)
+           : row_tiles == 2 ? launch_main<Cfg<D, DT, 2>, 1>(p, grid, s)
+                            : launch_main<Cfg<D, DT, 4>, 1>(p, grid, s);
   }
 }
-
-// One translation unit per head_dim.
-cudaError_t launch_d64(const Plan& p, int row_tiles, int grid, cudaStream_t s);
-cudaError_t launch_d128(const Plan& p, int row_tiles, int grid, cudaStream_t s);
-cudaError_t launch_d256(const Plan& p, int row_tiles, int grid, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace lin

@@ -1,0 +1,456 @@
+// Decode attention for more than 16 rows per (request, kv head) over a bf16
+// cache: a verify of several drafts, or many query heads to a key-value head.
+// The products run on the 5th-generation tensor cores.
+//
+// What bounds it is HBM, as for few rows (attn_kernel.cuh); but warp-level MMA
+// of 16 rows, one m16n8k16 in 8 cycles per scheduler, takes as long as the loads
+// at about 24 rows, and tcgen05 some twentieth of that. So its M = 128 need not
+// be filled with work: the RP (32, 64 or 128) rows are repeated 128 / RP times
+// along M, and copy c only ever looks at the c-th share of a tile's tokens:
+//   S  = Q K^T      [128 lanes][TK tokens], every lane against every token;
+//   P               lane of copy c: weights of its share, 0 elsewhere (the zero
+//                   blocks are written once);
+//   O += P V        [128 lanes][D]: one online softmax per lane.
+// A thread owns a lane: its row's maximum, sum and weights need no exchange
+// between threads, and the four softmax warps share the tile's tokens evenly.
+// The copies are joined as the pieces of a split are.
+//
+// Roles: warps 0-3 softmax (thread = TMEM lane), 4-7 load, 8 issues the MMAs.
+// K and V tiles pass through a ring of U units (16-byte asynchronous copies, as
+// pages may end anywhere); S has two buffers, so S of tile t + 1 is made while
+// the weights of tile t are. The weights go in PT bf16 parts (2^-16, 2^-24), each
+// a product of its own.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace lin {
+namespace attn {
+
+template <int D_, int RP_, int PT_>
+struct UCfg {
+  static constexpr int D = D_, RP = RP_, PT = PT_;
+  static constexpr int TK = D == 64 ? 128 : 64;  // tokens of a tile
+  static constexpr int UNIT = TK * D * 2;        // its K, or its V
+  static constexpr int COPIES = 128 / RP;
+  static constexpr int KW = TK / COPIES;         // a copy's tokens
+  static constexpr int QB = 128 * D * 2;
+  static constexpr int PB = 128 * TK * 2;        // one part of the weights
+  static constexpr int FREE = 224 * 1024 - QB - PT * PB;
+  static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
+  static constexpr int AHEAD = U >= 7 ? U - 4 : U - 2;  // units in flight
+  static constexpr int SMEM = U * UNIT + QB + PT * PB;
+  static constexpr int PITCH = D + 4;            // of the joined sums, for the banks
+  static constexpr int TMEM = 2 * TK + D <= 256 ? 256 : 512;
+  static constexpr int THREADS = 288;
+  static_assert(U >= 3 && U * UNIT + QB >= 128 * (PITCH + 2) * 4, "");
+};
+
+constexpr uint32_t kUmmaWaitTries = 1u << 26;
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) {
+  constexpr int D = C::D, RP = C::RP, PT = C::PT, TK = C::TK, KW = C::KW, U = C::U, NT = C::THREADS;
+  constexpr int CH = KW < 32 ? KW : 32;  // tokens a thread looks at together
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ uint64_t b_full[U], b_empty[U], b_s[2], b_sfree[2], b_p, b_pfree, b_q, b_drain;
+  __shared__ uint16_t s_valid[16][8];  // live tokens of a tile, 16 to a word; a ring of tiles
+  __shared__ uint32_t s_see[32];
+  __shared__ int64_t s_scan[NT / 32], s_first[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_bad, s_dead;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const lin_kv_cache_t& c = p.c;
+  const lin_attn_args_t& a = p.a;
+  if (tid == 0) {
+    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 4), umma::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_sfree[i], 4);
+    umma::mbar_init(&b_p, 4);
+    umma::mbar_init(&b_pfree, 1);
+    umma::mbar_init(&b_q, 4);
+    umma::mbar_init(&b_drain, 1);
+    umma::mbar_fence_init();
+    s_dead = 0;
+  }
+  Walk w;
+  if (!walk_begin<NT>(p, w, s_scan, s_first)) return;
+  if (warp == 8) umma::tmem_alloc(&s_tmem, C::TMEM);
+  unsigned char* const qbuf = smem + U * C::UNIT;
+  unsigned char* const pbuf = qbuf + C::QB;
+  if (warp < 4)
+    for (int x = tid; x < PT * C::PB / 16; x += 128) reinterpret_cast<uint4*>(pbuf)[x] = make_uint4(0, 0, 0, 0);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = s_tmem, t_o = tmem + 2 * TK;
+  float* merge = reinterpret_cast<float*>(smem);
+  float2* merge_ml = reinterpret_cast<float2*>(merge + 128 * C::PITCH);
+
+  // the next unit of the ring and its phase, and tiles and pieces so far
+  int slot = 0, done_slot = 0;
+  uint32_t phase = 0, piece = 0, tile0 = 0;
+  auto next = [](int& s, uint32_t& ph) {
+    if (++s == U) s = 0, ph ^= 1;
+  };
+  // A thread whose wait runs out waits for nothing more and goes on to the
+  // piece's end, where all leave: every barrier is still met.
+  bool gone = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (gone || umma::mbar_wait(bar, parity, kUmmaWaitTries)) return;
+    gone = true;
+    s_dead = 1;
+    report(a.status, LIN_ST_TIMEOUT);
+  };
+
+  while (true) {
+    const int t1 = walk_until(w), r = w.r;
+    const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * RP;
+    const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
+    const int base = w.len - a.n_q;  // tokens that every query sees
+    const int tiles = (key_end - key_begin + TK - 1) / TK;
+
+    if (warp < 4) {
+      // ---- softmax ---------------------------------------------------------------
+      constexpr int CPR = D / 8;
+      const char* qb = static_cast<const char*>(a.q) + r * a.req_stride;
+      for (int x = tid; x < 128 * CPR; x += 128) {
+        const int row = x / CPR, ch = x % CPR, q = row0 + row % RP;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q < p.rows) {
+          v = *reinterpret_cast<const uint4*>(qb + (q / p.group) * a.token_stride +
+                                              (hk * p.group + q % p.group) * (D * 2) + ch * 16);
+          v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
+        }
+        *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(row, ch * 8, 128)) = v;
+      }
+      if (warp == 0) draft_sets(p, r, s_see, s_bad);
+      const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
+      {
+        float z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D; i += 32) umma::tmem_st32(t_o + t_lane + i, z);
+      }
+      umma::fence_smem_to_async();
+      umma::fence_before_sync();
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      if (lane == 0) mbar_arrive(&b_q);
+      const int copy = tid / RP, q = row0 + tid % RP;
+      const uint32_t see = q < p.rows ? s_see[q / p.group] : 0u;
+      float cut = -INFINITY, z = 0.0f, l = 0.0f;  // as in attn_kernel.cuh
+      for (int i = 0; i < tiles; ++i) {
+        const uint32_t gt = tile0 + i;
+        wait(&b_s[gt & 1], (gt >> 1) & 1);
+        umma::fence_after_sync();
+        const uint32_t t_s = tmem + t_lane + (gt & 1) * TK + copy * KW;
+        const int key0 = key_begin + i * TK + copy * KW;  // this copy's first token
+        float s[CH];
+        // what this row sees of the CH tokens from key0 + x on
+        auto sees = [&](int x) {
+          const uint16_t* v = &s_valid[gt & 15][(copy * KW + x) / 16];
+          uint32_t vis = CH == 16 ? v[0] : v[0] | uint32_t(v[1]) << 16;
+          const int sh = key0 + x - base;
+          if (sh + CH > 0) vis &= sh >= 0 ? (sh < 32 ? see >> sh : 0u) : (see << -sh) | ((1u << -sh) - 1u);
+          return vis;
+        };
+        auto load = [&](int x) {
+          if constexpr (CH == 16)
+            umma::tmem_ld16(t_s + x, s);
+          else
+            umma::tmem_ld32(t_s + x, s);
+        };
+        constexpr uint32_t ALL = CH == 32 ? ~0u : (1u << (CH & 31)) - 1u;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < KW; x += CH) {
+          load(x);
+          const uint32_t vis = sees(x);
+          if (vis != ALL) {
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+              if (!((vis >> k) & 1u)) s[k] = -INFINITY;
+          }
+#pragma unroll
+          for (int k = 0; k < CH; ++k) mx = fmaxf(mx, s[k]);
+        }
+        float f = 1.0f;
+        if (mx > cut) {
+          const float y = -mx * p.scale_log2;
+          f = cut == -INFINITY ? 0.0f : exp2_fast(y - z);
+          z = y, cut = mx + p.slack, l *= f;
+        }
+        // the product before this one has read the weights and written O
+        if (i > 0) wait(&b_pfree, (gt - 1) & 1);
+        umma::fence_after_sync();
+        if (i > 0 && __any_sync(~0u, f != 1.0f)) {
+#pragma unroll
+          for (int x = 0; x < D; x += 32) {
+            float o[32];
+            umma::tmem_ld32(t_o + t_lane + x, o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            umma::tmem_st32(t_o + t_lane + x, o);
+          }
+        }
+        // values that are infinite or NaN: 0 in the product, added by hand to the
+        // rows that see them (only drafts can be hidden from some rows)
+        bool wild = false;
+        unsigned char* vbuf = nullptr;
+        if (key_begin + (i + 1) * TK > base && a.n_q > 1) {
+          // this tile's V is the unit after its K
+          int sl = slot;
+          uint32_t ph = phase;
+          next(sl, ph);
+          vbuf = smem + sl * C::UNIT;
+          wait(&b_full[sl], ph);
+          for (int x = tid; x < C::UNIT / 16; x += 128) {
+            const uint4 v = reinterpret_cast<const uint4*>(vbuf)[x];
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              wild |= (y[k] & 0x7f800000u) == 0x7f800000u || (y[k] & 0x7f80u) == 0x7f80u;
+          }
+          int any;
+          asm volatile(
+              "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, 1, 128, p;\n\t"
+              "selp.b32 %0, 1, 0, q;\n\t}"
+              : "=r"(any)
+              : "r"(static_cast<int>(wild))
+              : "memory");
+          wild = any != 0;
+        }
+#pragma unroll
+        for (int x = 0; x < KW; x += CH) {
+          if (KW > CH) load(x);
+          const uint32_t vis = sees(x);
+#pragma unroll
+          for (int k = 0; k < CH; ++k) s[k] = exp2_fast(fmaf(s[k], p.scale_log2, z));
+          if (vis != ALL) {
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+              if (!((vis >> k) & 1u)) s[k] = 0.0f;
+          }
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int k = 0; k < CH; ++k) sum[k & 3] += s[k];
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          if (wild) {
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              float o[32];
+              umma::tmem_ld32(t_o + t_lane + d, o);
+#pragma unroll 1
+              for (int k = 0; k < CH; ++k) {
+                float pk = 0.0f;
+#pragma unroll
+                for (int y = 0; y < CH; ++y) pk = y == k ? s[y] : pk;
+                const bool seen = (vis >> k) & 1u;
+#pragma unroll
+                for (int y = 0; y < 32; ++y) {
+                  const float v = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(
+                      vbuf + umma::rp_offset(copy * KW + x + k, d + y, TK)));
+                  if (seen && !isfinite(v)) o[y] = fmaf(pk, v, o[y]);
+                }
+              }
+              umma::tmem_st32(t_o + t_lane + d, o);
+            }
+          }
+#pragma unroll
+          for (int part = 0; part < PT; ++part)
+#pragma unroll
+            for (int k = 0; k < CH; k += 8) {
+              uint4 v;
+              v.x = take_bf16(s[k], s[k + 1]);
+              v.y = take_bf16(s[k + 2], s[k + 3]);
+              v.z = take_bf16(s[k + 4], s[k + 5]);
+              v.w = take_bf16(s[k + 6], s[k + 7]);
+              *reinterpret_cast<uint4*>(pbuf + part * C::PB + umma::rp_offset(tid, copy * KW + x + k, 128)) = v;
+            }
+        }
+        if (wild) {
+          asm volatile("bar.sync 1, 128;" ::: "memory");  // every row has read V
+          for (int x = tid; x < C::UNIT / 4; x += 128) {
+            uint32_t& v = reinterpret_cast<uint32_t*>(vbuf)[x];
+            if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
+            if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
+          }
+        }
+        umma::fence_smem_to_async();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_sfree[gt & 1]), mbar_arrive(&b_p);
+        next(slot, phase);
+        next(slot, phase);
+      }
+      if (tiles > 0) wait(&b_pfree, (tile0 + tiles - 1) & 1);
+      umma::fence_after_sync();
+      asm volatile("bar.sync 1, 128;" ::: "memory");  // every lane's products are done
+#pragma unroll
+      for (int x = 0; x < D; x += 32) {
+        float o[32];
+        umma::tmem_ld32(t_o + t_lane + x, o);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+          *reinterpret_cast<float4*>(merge + tid * C::PITCH + x + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+      }
+      merge_ml[tid] = make_float2(cut == -INFINITY ? cut : -z, l);
+      umma::fence_before_sync();
+    } else if (warp < 8) {
+      // ---- loads: warp 4 + x brings the x-th quarter of a tile's tokens ------------
+      constexpr int RW = TK / 4, CPR = D / 8;
+      const int lw = warp - 4;
+      const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
+      const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
+      const int32_t* table = a.page_table + r * a.page_table_stride;
+      int key = key_begin + lw * RW + (lane & (RW - 1));
+      int id = key < key_end ? table[page_of(p, key)] : -1;
+      int flying = 0;
+      auto land = [&]() {  // the oldest unit in flight has landed
+        umma::fence_smem_to_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_full[done_slot]);
+        if (++done_slot == U) done_slot = 0;
+        --flying;
+      };
+      for (int i = 0; i < tiles; ++i) {
+        const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
+        if (key < key_end && !live && lane < RW) report(a.status, LIN_ST_BAD_PAGE);
+        const int64_t off = live ? id * c.page_stride + (key - page_of(p, key) * c.page_size) * c.token_stride : 0;
+        const uint32_t valid = __ballot_sync(~0u, live);
+        key += TK;
+        id = key < key_end ? table[page_of(p, key)] : -1;
+        if (lane == 0) {
+          uint16_t* v = &s_valid[(tile0 + i) & 15][lw * (RW / 16)];
+          v[0] = static_cast<uint16_t>(valid);
+          if (RW == 32) v[1] = static_cast<uint16_t>(valid >> 16);
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          wait(&b_empty[slot], phase ^ 1);
+          const uint32_t dst = umma::smem_u32(smem) + slot * C::UNIT;
+          const char* src = kv ? vb : kb;
+#pragma unroll 8
+          for (int x = 0; x < RW * CPR / 32; ++x) {
+            const int y = x * 32 + lane, row = y / CPR, ch = y % CPR;
+            const int64_t o = __shfl_sync(~0u, off, row);
+            cp16(dst + umma::rp_offset(lw * RW + row, ch * 8, TK), src + o + ch * 16, (valid >> row) & 1u);
+          }
+          cp_commit();
+          next(slot, phase);
+          if (++flying == C::AHEAD) {
+            cp_wait<C::AHEAD - 1>();
+            land();
+          }
+        }
+      }
+      cp_wait<0>();
+      while (flying > 0) land();
+    } else {
+      // ---- MMA issue ----------------------------------------------------------------
+      if (lane == 0) {
+        const uint32_t ring = umma::smem_u32(smem), qd = umma::smem_u32(qbuf), pd = umma::smem_u32(pbuf);
+        constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
+        constexpr int NV = D < 128 ? D : 128;
+        constexpr uint32_t id_o = umma::idesc_f16(128, NV, true, false, true);
+        // K of tile t is unit 2 t, V unit 2 t + 1: two walks over the ring
+        int ks = slot, vs = slot;
+        uint32_t kph = phase, vph = phase;
+        next(vs, vph);
+        wait(&b_q, piece & 1);
+        auto scores = [&](int i) {
+          const uint32_t gt = tile0 + i;
+          wait(&b_full[ks], kph);
+          wait(&b_sfree[gt & 1], ((gt >> 1) & 1) ^ 1);
+          umma::fence_after_sync();
+          const uint32_t kd = ring + ks * C::UNIT;
+#pragma unroll
+          for (int k = 0; k < D; k += 16)
+            umma::mma_f16(tmem + (gt & 1) * TK, umma::desc_kmajor(qd, 128, k), umma::desc_kmajor(kd, TK, k), id_s, k > 0);
+          umma::mma_commit(&b_empty[ks]);
+          umma::mma_commit(&b_s[gt & 1]);
+          mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
+          next(ks, kph);
+          next(ks, kph);
+        };
+        if (tiles > 0) scores(0);
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t gt = tile0 + i;
+          if (i + 1 < tiles) scores(i + 1);
+          wait(&b_p, gt & 1);
+          wait(&b_full[vs], vph);
+          umma::fence_after_sync();
+          const uint32_t vd = ring + vs * C::UNIT;
+#pragma unroll
+          for (int part = PT - 1; part >= 0; --part)
+#pragma unroll
+            for (int n = 0; n < D; n += NV)
+#pragma unroll
+              for (int k = 0; k < TK; k += 16)
+                umma::mma_f16(t_o + n, umma::desc_kmajor(pd + part * C::PB, 128, k),
+                              umma::desc_mnmajor(vd + (n / 64) * (TK * 128), TK, k), id_o, 1);
+          umma::mma_commit(&b_empty[vs]);
+          umma::mma_commit(&b_pfree);
+          next(vs, vph);
+          next(vs, vph);
+        }
+        slot = ks, phase = kph;
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+    if (s_dead) {
+      // a wait ran out: let copies and products in flight finish, then leave
+      if (warp == 8 && lane == 0) {
+        umma::mma_commit(&b_drain);
+        umma::mbar_wait(&b_drain, 0, kUmmaWaitTries);
+      }
+      w.split.x = -1;
+      break;
+    }
+    finish_piece<D, C::COPIES, RP, NT, C::PITCH>(p, w, t1, merge, merge_ml, s_bad);
+    tile0 += tiles;
+    ++piece;
+    if (!walk_next(p, w, t1)) break;
+    umma::fence_smem_to_async();
+    __syncthreads();  // the join is read before the ring is filled again
+  }
+  __syncthreads();
+  if (warp == 8) umma::tmem_dealloc(tmem, C::TMEM);
+  if (tid == 0) p.split[blockIdx.x] = w.split;
+}
+
+template <class C>
+cudaError_t launch_umma(const Plan& p, int grid, cudaStream_t s) {
+  auto kern = attn_umma_kernel<C>;
+  static bool ready[kMaxDevices];  // set twice at worst, to the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_umma_rows(const Plan& p, int grid, cudaStream_t s) {
+  const bool f32 = p.a.out_dtype == LIN_F32;
+  switch (p.block_rows) {
+    case 32: return f32 ? launch_umma<UCfg<D, 32, 3>>(p, grid, s) : launch_umma<UCfg<D, 32, 2>>(p, grid, s);
+    case 64: return f32 ? launch_umma<UCfg<D, 64, 3>>(p, grid, s) : launch_umma<UCfg<D, 64, 2>>(p, grid, s);
+    default: return f32 ? launch_umma<UCfg<D, 128, 3>>(p, grid, s) : launch_umma<UCfg<D, 128, 2>>(p, grid, s);
+  }
+}
+
+}  // namespace attn
+}  // namespace lin

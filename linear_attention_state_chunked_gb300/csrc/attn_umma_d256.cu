@@ -1,0 +1,11 @@
+// Tensor-memory decode attention kernels for heads of 256 channels (attn_umma.cuh).
+
+#include "attn_umma.cuh"
+
+namespace lin {
+namespace attn {
+
+cudaError_t launch_umma_d256(const Plan& p, int grid, cudaStream_t s) { return launch_umma_rows<256>(p, grid, s); }
+
+}  // namespace attn
+}  // namespace lin
