@@ -15,11 +15,13 @@
 // between threads, and the four softmax warps share the tile's tokens evenly.
 // The copies are joined as the pieces of a split are.
 //
-// Roles: warps 0-3 softmax (thread = TMEM lane), 4-7 load, 8 issues the MMAs.
+// Roles: warps 0-3 softmax (thread = TMEM lane), 4-7 load, 8 issues Q K^T, 9
+// issues P V (one warp for both would make each wait for the other's operands).
 // K and V tiles pass through a ring of U units (16-byte asynchronous copies, as
-// pages may end anywhere); S has two buffers, so S of tile t + 1 is made while
-// the weights of tile t are. The weights go in PT bf16 parts (2^-16, 2^-24), each
-// a product of its own.
+// pages may end anywhere). S, and P as the A operand, lie in tensor memory, S in
+// two buffers and P in NB, so scores, weights and value sums of successive tiles
+// overlap. The weights go in PT bf16 parts (2^-16, 2^-24), each a product of its
+// own.
 #pragma once
 
 #include "attn_common.cuh"
@@ -35,15 +37,17 @@ struct UCfg {
   static constexpr int COPIES = 128 / RP;
   static constexpr int KW = TK / COPIES;         // a copy's tokens
   static constexpr int QB = 128 * D * 2;
-  static constexpr int PB = 128 * TK * 2;        // one part of the weights
-  static constexpr int FREE = 224 * 1024 - QB - PT * PB;
+  static constexpr int FREE = 224 * 1024 - QB;
   static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
-  static constexpr int AHEAD = U >= 7 ? U - 4 : U - 2;  // units in flight
-  static constexpr int SMEM = U * UNIT + QB + PT * PB;
+  static constexpr int SMEM = U * UNIT + QB;
   static constexpr int PITCH = D + 4;            // of the joined sums, for the banks
-  static constexpr int TMEM = 2 * TK + D <= 256 ? 256 : 512;
-  static constexpr int THREADS = 288;
-  static_assert(U >= 3 && U * UNIT + QB >= 128 * (PITCH + 2) * 4, "");
+  // tensor memory columns: 2 buffers of S, NB of P (two tokens to a column), O
+  static constexpr int PCOLS = PT * TK / 2;
+  static constexpr int NB = 2 * TK + 2 * PCOLS + D <= 512 ? 2 : 1;
+  static constexpr int COLS = 2 * TK + NB * PCOLS + D;
+  static constexpr int TMEM = COLS <= 256 ? 256 : 512;
+  static constexpr int THREADS = 320;
+  static_assert(COLS <= 512 && U >= 4 && SMEM >= 128 * (PITCH + 2) * 4, "");
 };
 
 constexpr uint32_t kUmmaWaitTries = 1u << 26;
@@ -52,12 +56,28 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
 
+// D += A B with A in tensor memory: row i in lane i, two bf16 of a row to a column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 1, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :
+      : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+// 8 columns of this thread's lane.
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) {
-  constexpr int D = C::D, RP = C::RP, PT = C::PT, TK = C::TK, KW = C::KW, U = C::U, NT = C::THREADS;
+  constexpr int D = C::D, RP = C::RP, PT = C::PT, TK = C::TK, KW = C::KW, U = C::U, NB = C::NB, NT = C::THREADS;
   constexpr int CH = KW < 32 ? KW : 32;  // tokens a thread looks at together
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ uint64_t b_full[U], b_empty[U], b_s[2], b_sfree[2], b_p, b_pfree, b_q, b_drain;
+  __shared__ uint64_t b_full[U], b_empty[U], b_s[2], b_sfree[2], b_p[NB], b_pfree[NB], b_q, b_drain;
   __shared__ uint16_t s_valid[16][8];  // live tokens of a tile, 16 to a word; a ring of tiles
   __shared__ uint32_t s_see[32];
   __shared__ int64_t s_scan[NT / 32], s_first[2];
@@ -69,12 +89,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
   const lin_kv_cache_t& c = p.c;
   const lin_attn_args_t& a = p.a;
   if (tid == 0) {
-    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 4), umma::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 128 + 4), umma::mbar_init(&b_empty[i], 1);
     for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_sfree[i], 4);
-    umma::mbar_init(&b_p, 4);
-    umma::mbar_init(&b_pfree, 1);
+    for (int i = 0; i < NB; ++i) umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_pfree[i], 1);
     umma::mbar_init(&b_q, 4);
-    umma::mbar_init(&b_drain, 1);
+    umma::mbar_init(&b_drain, 2);
     umma::mbar_fence_init();
     s_dead = 0;
   }
@@ -82,18 +101,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
   if (!walk_begin<NT>(p, w, s_scan, s_first)) return;
   if (warp == 8) umma::tmem_alloc(&s_tmem, C::TMEM);
   unsigned char* const qbuf = smem + U * C::UNIT;
-  unsigned char* const pbuf = qbuf + C::QB;
-  if (warp < 4)
-    for (int x = tid; x < PT * C::PB / 16; x += 128) reinterpret_cast<uint4*>(pbuf)[x] = make_uint4(0, 0, 0, 0);
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  const uint32_t tmem = s_tmem, t_o = tmem + 2 * TK;
+  const uint32_t tmem = s_tmem, t_p = tmem + 2 * TK, t_o = t_p + NB * C::PCOLS;
   float* merge = reinterpret_cast<float*>(smem);
   float2* merge_ml = reinterpret_cast<float2*>(merge + 128 * C::PITCH);
 
   // the next unit of the ring and its phase, and tiles and pieces so far
-  int slot = 0, done_slot = 0;
+  int slot = 0;
   uint32_t phase = 0, piece = 0, tile0 = 0;
   auto next = [](int& s, uint32_t& ph) {
     if (++s == U) s = 0, ph ^= 1;
@@ -117,17 +133,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 
     if (warp < 4) {
       // ---- softmax ---------------------------------------------------------------
-      constexpr int CPR = D / 8;
-      const char* qb = static_cast<const char*>(a.q) + r * a.req_stride;
-      for (int x = tid; x < 128 * CPR; x += 128) {
-        const int row = x / CPR, ch = x % CPR, q = row0 + row % RP;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (q < p.rows) {
-          v = *reinterpret_cast<const uint4*>(qb + (q / p.group) * a.token_stride +
-                                              (hk * p.group + q % p.group) * (D * 2) + ch * 16);
+      // every thread brings its lane's row of queries
+      {
+        const int q = row0 + tid % RP;
+        const bool live = q < p.rows;
+        const int j = live ? q / p.group : 0;
+        const char* src = static_cast<const char*>(a.q) + r * a.req_stride + j * a.token_stride +
+                          (live ? hk * p.group + q - j * p.group : 0) * (D * 2);
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ++ch) {
+          uint4 v = reinterpret_cast<const uint4*>(src)[ch];
+          if (!live) v = make_uint4(0, 0, 0, 0);
           v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
+          *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(tid, ch * 8, 128)) = v;
         }
-        *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(row, ch * 8, 128)) = v;
       }
       if (warp == 0) draft_sets(p, r, s_see, s_bad);
       const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
@@ -137,6 +156,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
         for (int i = 0; i < 32; ++i) z[i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < D; i += 32) umma::tmem_st32(t_o + t_lane + i, z);
+        if (piece == 0) {  // other copies' tokens keep weight 0
+#pragma unroll
+          for (int i = 0; i < NB * C::PCOLS; i += 32) umma::tmem_st32(t_p + t_lane + i, z);
+        }
       }
       umma::fence_smem_to_async();
       umma::fence_before_sync();
@@ -186,10 +209,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
           f = cut == -INFINITY ? 0.0f : exp2_fast(y - z);
           z = y, cut = mx + p.slack, l *= f;
         }
-        // the product before this one has read the weights and written O
-        if (i > 0) wait(&b_pfree, (gt - 1) & 1);
+        const bool rescale = i > 0 && __any_sync(~0u, f != 1.0f);
+        const bool drafts = key_begin + (i + 1) * TK > base && a.n_q > 1;
+        // the buffer's last product has read it; where O is touched, all have ended
+        if (gt >= NB) wait(&b_pfree[gt % NB], (gt / NB - 1) & 1);
+        if (NB > 1 && i > 0 && (rescale || drafts)) wait(&b_pfree[(gt - 1) % NB], ((gt - 1) / NB) & 1);
         umma::fence_after_sync();
-        if (i > 0 && __any_sync(~0u, f != 1.0f)) {
+        if (rescale) {
 #pragma unroll
           for (int x = 0; x < D; x += 32) {
             float o[32];
@@ -203,7 +229,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
         // rows that see them (only drafts can be hidden from some rows)
         bool wild = false;
         unsigned char* vbuf = nullptr;
-        if (key_begin + (i + 1) * TK > base && a.n_q > 1) {
+        if (drafts) {
           // this tile's V is the unit after its K
           int sl = slot;
           uint32_t ph = phase;
@@ -265,15 +291,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 #pragma unroll
           for (int part = 0; part < PT; ++part)
 #pragma unroll
-            for (int k = 0; k < CH; k += 8) {
-              uint4 v;
-              v.x = take_bf16(s[k], s[k + 1]);
-              v.y = take_bf16(s[k + 2], s[k + 3]);
-              v.z = take_bf16(s[k + 4], s[k + 5]);
-              v.w = take_bf16(s[k + 6], s[k + 7]);
-              *reinterpret_cast<uint4*>(pbuf + part * C::PB + umma::rp_offset(tid, copy * KW + x + k, 128)) = v;
+            for (int k = 0; k < CH; k += 16) {
+              uint32_t v[8];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) v[y] = take_bf16(s[k + 2 * y], s[k + 2 * y + 1]);
+              tmem_st8(t_p + t_lane + (gt % NB) * C::PCOLS + part * (TK / 2) + (copy * KW + x + k) / 2, v);
             }
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         if (wild) {
           asm volatile("bar.sync 1, 128;" ::: "memory");  // every row has read V
           for (int x = tid; x < C::UNIT / 4; x += 128) {
@@ -281,15 +306,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
             if ((v & 0x7f80u) == 0x7f80u) v &= 0xffff0000u;
             if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
           }
+          umma::fence_smem_to_async();
         }
-        umma::fence_smem_to_async();
         umma::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b_sfree[gt & 1]), mbar_arrive(&b_p);
+        if (lane == 0) mbar_arrive(&b_sfree[gt & 1]), mbar_arrive(&b_p[gt % NB]);
         next(slot, phase);
         next(slot, phase);
       }
-      if (tiles > 0) wait(&b_pfree, (tile0 + tiles - 1) & 1);
+      if (tiles > 0) wait(&b_pfree[(tile0 + tiles - 1) % NB], ((tile0 + tiles - 1) / NB) & 1);
       umma::fence_after_sync();
       asm volatile("bar.sync 1, 128;" ::: "memory");  // every lane's products are done
 #pragma unroll
@@ -311,14 +336,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
       const int32_t* table = a.page_table + r * a.page_table_stride;
       int key = key_begin + lw * RW + (lane & (RW - 1));
       int id = key < key_end ? table[page_of(p, key)] : -1;
-      int flying = 0;
-      auto land = [&]() {  // the oldest unit in flight has landed
-        umma::fence_smem_to_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_full[done_slot]);
-        if (++done_slot == U) done_slot = 0;
-        --flying;
-      };
+      // Lane's place in a unit: row lane / CPR + x (32 / CPR) of its warp's rows, so
+      // that the swizzle of step x is an exclusive-or with a constant.
+      constexpr int STEP = 32 / CPR;
+      const uint32_t place = umma::smem_u32(smem) + umma::rp_offset(lw * RW + lane / CPR, (lane % CPR) * 8, TK);
       for (int i = 0; i < tiles; ++i) {
         const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
         if (key < key_end && !live && lane < RW) report(a.status, LIN_ST_BAD_PAGE);
@@ -334,80 +355,82 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           wait(&b_empty[slot], phase ^ 1);
-          const uint32_t dst = umma::smem_u32(smem) + slot * C::UNIT;
-          const char* src = kv ? vb : kb;
-#pragma unroll 8
-          for (int x = 0; x < RW * CPR / 32; ++x) {
-            const int y = x * 32 + lane, row = y / CPR, ch = y % CPR;
+          const uint32_t dst = place + slot * C::UNIT;
+          const char* src = (kv ? vb : kb) + (lane % CPR) * 16;
+#pragma unroll
+          for (int x = 0; x < RW / STEP; ++x) {
+            const int row = x * STEP + lane / CPR;
             const int64_t o = __shfl_sync(~0u, off, row);
-            cp16(dst + umma::rp_offset(lw * RW + row, ch * 8, TK), src + o + ch * 16, (valid >> row) & 1u);
+            cp16((dst ^ ((x * STEP & 7) << 4)) + x * STEP * 128, src + o, (valid >> row) & 1u);
           }
-          cp_commit();
+          // The unit is full when every lane's copies have landed: nobody waits
+          // here. (A proxy fence here would wait for all copies in flight; the
+          // thread that issues the products has one.)
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(&b_full[slot])) : "memory");
+          if (lane == 0) mbar_arrive(&b_full[slot]);  // and passes on s_valid
           next(slot, phase);
-          if (++flying == C::AHEAD) {
-            cp_wait<C::AHEAD - 1>();
-            land();
-          }
         }
       }
-      cp_wait<0>();
-      while (flying > 0) land();
     } else {
-      // ---- MMA issue ----------------------------------------------------------------
-      if (lane == 0) {
-        const uint32_t ring = umma::smem_u32(smem), qd = umma::smem_u32(qbuf), pd = umma::smem_u32(pbuf);
+      // ---- MMA issue: S = Q K^T by warp 8, O += P V by warp 9 -----------------------
+      // Descriptors of the buffers' starts; a step within one is a sum to the
+      // address field, which holds 18-bit shared-memory addresses / 16.
+      const bool scores = warp == 8;
+      if (piece == 0 && !scores) next(slot, phase);  // K of tile t is unit 2 t, V unit 2 t + 1
+      if (lane == 0 && scores) {
         constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
-        constexpr int NV = D < 128 ? D : 128;
-        constexpr uint32_t id_o = umma::idesc_f16(128, NV, true, false, true);
-        // K of tile t is unit 2 t, V unit 2 t + 1: two walks over the ring
-        int ks = slot, vs = slot;
-        uint32_t kph = phase, vph = phase;
-        next(vs, vph);
+        const uint64_t q_desc = umma::desc_kmajor(umma::smem_u32(qbuf), 128, 0);
+        const uint64_t k_desc = umma::desc_kmajor(umma::smem_u32(smem), TK, 0);
+        auto step = [](int rows, int k) { return uint64_t(((k >> 6) * rows * 128 + (k & 63) * 2) >> 4); };
         wait(&b_q, piece & 1);
-        auto scores = [&](int i) {
-          const uint32_t gt = tile0 + i;
-          wait(&b_full[ks], kph);
-          wait(&b_sfree[gt & 1], ((gt >> 1) & 1) ^ 1);
-          umma::fence_after_sync();
-          const uint32_t kd = ring + ks * C::UNIT;
-#pragma unroll
-          for (int k = 0; k < D; k += 16)
-            umma::mma_f16(tmem + (gt & 1) * TK, umma::desc_kmajor(qd, 128, k), umma::desc_kmajor(kd, TK, k), id_s, k > 0);
-          umma::mma_commit(&b_empty[ks]);
-          umma::mma_commit(&b_s[gt & 1]);
-          mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
-          next(ks, kph);
-          next(ks, kph);
-        };
-        if (tiles > 0) scores(0);
         for (int i = 0; i < tiles; ++i) {
           const uint32_t gt = tile0 + i;
-          if (i + 1 < tiles) scores(i + 1);
-          wait(&b_p, gt & 1);
-          wait(&b_full[vs], vph);
+          wait(&b_full[slot], phase);
+          wait(&b_sfree[gt & 1], ((gt >> 1) & 1) ^ 1);
           umma::fence_after_sync();
-          const uint32_t vd = ring + vs * C::UNIT;
+          umma::fence_smem_to_async();
+          const uint64_t kd = k_desc + slot * (C::UNIT >> 4);
+#pragma unroll
+          for (int k = 0; k < D; k += 16)
+            umma::mma_f16(tmem + (gt & 1) * TK, q_desc + step(128, k), kd + step(TK, k), id_s, k > 0);
+          umma::mma_commit(&b_s[gt & 1]);
+          umma::mma_commit(&b_empty[slot]);
+          mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
+          next(slot, phase);
+          next(slot, phase);
+        }
+      } else if (lane == 0) {
+        constexpr int NV = D < 128 ? D : 128;
+        constexpr uint32_t id_o = umma::idesc_f16(128, NV, true, false, true);
+        const uint64_t v_desc = umma::desc_mnmajor(umma::smem_u32(smem), TK, 0);
+        for (int i = 0; i < tiles; ++i) {
+          const uint32_t gt = tile0 + i;
+          wait(&b_full[slot], phase);
+          umma::fence_smem_to_async();
+          wait(&b_p[gt % NB], (gt / NB) & 1);
+          umma::fence_after_sync();
+          const uint64_t vd = v_desc + slot * (C::UNIT >> 4);
+          const uint32_t pa = t_p + (gt % NB) * C::PCOLS;
 #pragma unroll
           for (int part = PT - 1; part >= 0; --part)
 #pragma unroll
             for (int n = 0; n < D; n += NV)
 #pragma unroll
               for (int k = 0; k < TK; k += 16)
-                umma::mma_f16(t_o + n, umma::desc_kmajor(pd + part * C::PB, 128, k),
-                              umma::desc_mnmajor(vd + (n / 64) * (TK * 128), TK, k), id_o, 1);
-          umma::mma_commit(&b_empty[vs]);
-          umma::mma_commit(&b_pfree);
-          next(vs, vph);
-          next(vs, vph);
+                mma_ts(t_o + n, pa + part * (TK / 2) + k / 2, vd + (((n / 64) * (TK * 128) + k * 128) >> 4), id_o);
+          umma::mma_commit(&b_pfree[gt % NB]);
+          umma::mma_commit(&b_empty[slot]);
+          next(slot, phase);
+          next(slot, phase);
         }
-        slot = ks, phase = kph;
       }
       __syncwarp();
     }
     __syncthreads();
     if (s_dead) {
       // a wait ran out: let copies and products in flight finish, then leave
-      if (warp == 8 && lane == 0) {
+      cp_wait_all();
+      if (warp >= 8 && lane == 0) {
         umma::mma_commit(&b_drain);
         umma::mbar_wait(&b_drain, 0, kUmmaWaitTries);
       }
