@@ -196,38 +196,46 @@ __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t
   const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * ROWS;
   const bool whole = w.t0 == 0 && t1 == w.u;
   const int64_t part = 2 * int64_t(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
-  for (int x = threadIdx.x; x < ROWS * (D / 4); x += NT) {
-    const int row = x / (D / 4), d = (x % (D / 4)) * 4, q = row0 + row;
-    if (q >= p.rows) continue;
-    float top = -INFINITY, sum = 0.0f;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int LANES = D / 4 < 32 ? D / 4 : 32;  // threads of a row, so many steps of 4 channels
+  for (int row = threadIdx.x / LANES; row < ROWS; row += NT / LANES) {
+    const int q = row0 + row, lane = threadIdx.x % LANES;
+    if (q >= p.rows) break;
+    float top = -INFINITY, sum = 0.0f, f[KG];
 #pragma unroll
     for (int k = 0; k < KG; ++k) top = fmaxf(top, merge_ml[k * ROWS + row].x);
 #pragma unroll
     for (int k = 0; k < KG; ++k) {
       const float2 ml = merge_ml[k * ROWS + row];
-      if (ml.y == 0.0f) continue;  // saw nothing (a NaN sum goes on)
-      const float f = ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-      const float4 y = *reinterpret_cast<const float4*>(merge + (k * ROWS + row) * PITCH + d);
-      sum = fmaf(f, ml.y, sum);
-      v.x = fmaf(f, y.x, v.x), v.y = fmaf(f, y.y, v.y);
-      v.z = fmaf(f, y.z, v.z), v.w = fmaf(f, y.w, v.w);
+      // 0 where a copy saw nothing (a NaN sum goes on)
+      f[k] = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+      sum = fmaf(f[k], ml.y, sum);
     }
-    if (whole) {
-      if (bad) continue;
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t at = ((int64_t(w.r) * a.n_q + q / p.group) * a.num_q_heads + hk * p.group + q % p.group) * D + d;
-      if (a.out_dtype == LIN_F32) {
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int j = q / p.group;
+    const int64_t out = ((int64_t(w.r) * a.n_q + j) * a.num_q_heads + hk * p.group + q - j * p.group) * D;
+#pragma unroll
+    for (int d = lane * 4; d < D; d += LANES * 4) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int k = 0; k < KG; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(merge + (k * ROWS + row) * PITCH + d);
+        v.x = fmaf(f[k], y.x, v.x), v.y = fmaf(f[k], y.y, v.y);
+        v.z = fmaf(f[k], y.z, v.z), v.w = fmaf(f[k], y.w, v.w);
+      }
+      if (!whole) {
+        *reinterpret_cast<float4*>(p.part + (part * ROWS + row) * D + d) = v;
+      } else if (bad) {
+      } else if (a.out_dtype == LIN_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out + d) =
+            make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
       } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * f, v.y * f), hi = __floats2bfloat162_rn(v.z * f, v.w * f);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * scale, v.y * scale);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * scale, v.w * scale);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out + d) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
-    } else {
-      *reinterpret_cast<float4*>(p.part + (part * ROWS + row) * D + d) = v;
-      if (d == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? -1.0f : sum);
     }
+    if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? -1.0f : sum);
   }
 }
 

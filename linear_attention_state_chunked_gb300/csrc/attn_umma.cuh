@@ -32,19 +32,24 @@ namespace attn {
 template <int D_, int RP_, int PT_>
 struct UCfg {
   static constexpr int D = D_, RP = RP_, PT = PT_;
-  static constexpr int TK = D == 64 ? 128 : 64;  // tokens of a tile
+  static constexpr int TK = D == 64 && PT == 2 ? 128 : 64;  // tokens of a tile
   static constexpr int UNIT = TK * D * 2;        // its K, or its V
   static constexpr int COPIES = 128 / RP;
   static constexpr int KW = TK / COPIES;         // a copy's tokens
-  static constexpr int QB = 128 * D * 2;
+  // q is the A operand: in tensor memory for heads of up to 128 channels (from
+  // shared memory every product reads all 128 lanes of it again, and takes 74
+  // cycles for its 16; tensor memory has no room beside O of 256 channels)
+  static constexpr bool QT = D <= 128;
+  static constexpr int QCOLS = QT ? D / 2 : 0;
+  static constexpr int QB = QT ? 0 : 128 * D * 2;
   static constexpr int FREE = 224 * 1024 - QB;
   static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
   static constexpr int SMEM = U * UNIT + QB;
   static constexpr int PITCH = D + 4;            // of the joined sums, for the banks
-  // tensor memory columns: 2 buffers of S, NB of P (two tokens to a column), O
+  // tensor memory columns: 2 buffers of S, NB of P (two tokens to a column), O, q
   static constexpr int PCOLS = PT * TK / 2;
-  static constexpr int NB = 2 * TK + 2 * PCOLS + D <= 512 ? 2 : 1;
-  static constexpr int COLS = 2 * TK + NB * PCOLS + D;
+  static constexpr int NB = 2 * TK + 2 * PCOLS + D + QCOLS <= 512 ? 2 : 1;
+  static constexpr int COLS = 2 * TK + NB * PCOLS + D + QCOLS;
   static constexpr int TMEM = COLS <= 256 ? 256 : 512;
   static constexpr int THREADS = 320;
   static_assert(COLS <= 512 && U >= 4 && SMEM >= 128 * (PITCH + 2) * 4, "");
@@ -57,12 +62,13 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // D += A B with A in tensor memory: row i in lane i, two bf16 of a row to a column.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 1, 0;\n\t"
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       :
-      : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc)
+      : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // 8 columns of this thread's lane.
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  const uint32_t tmem = s_tmem, t_p = tmem + 2 * TK, t_o = t_p + NB * C::PCOLS;
+  const uint32_t tmem = s_tmem, t_p = tmem + 2 * TK, t_o = t_p + NB * C::PCOLS, t_q = t_o + D;
   float* merge = reinterpret_cast<float*>(smem);
   float2* merge_ml = reinterpret_cast<float2*>(merge + 128 * C::PITCH);
 
@@ -134,6 +140,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
     if (warp < 4) {
       // ---- softmax ---------------------------------------------------------------
       // every thread brings its lane's row of queries
+      const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
+      uint4 qrow[D / 8];
       {
         const int q = row0 + tid % RP;
         const bool live = q < p.rows;
@@ -142,14 +150,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
                           (live ? hk * p.group + q - j * p.group : 0) * (D * 2);
 #pragma unroll
         for (int ch = 0; ch < D / 8; ++ch) {
-          uint4 v = reinterpret_cast<const uint4*>(src)[ch];
-          if (!live) v = make_uint4(0, 0, 0, 0);
-          v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
-          *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(tid, ch * 8, 128)) = v;
+          qrow[ch] = live ? reinterpret_cast<const uint4*>(src)[ch] : make_uint4(0, 0, 0, 0);
         }
       }
       if (warp == 0) draft_sets(p, r, s_see, s_bad);
-      const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
       {
         float z[32];
 #pragma unroll
@@ -160,6 +164,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 #pragma unroll
           for (int i = 0; i < NB * C::PCOLS; i += 32) umma::tmem_st32(t_p + t_lane + i, z);
         }
+      }
+#pragma unroll
+      for (int ch = 0; ch < D / 8; ++ch) {
+        uint4& v = qrow[ch];
+        v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
+        if constexpr (!C::QT) *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(tid, ch * 8, 128)) = v;
+      }
+      if constexpr (C::QT) {
+#pragma unroll
+        for (int ch = 0; ch < D / 8; ch += 2) {
+          const uint32_t v[8] = {qrow[ch].x, qrow[ch].y, qrow[ch].z, qrow[ch].w,
+                                 qrow[ch + 1].x, qrow[ch + 1].y, qrow[ch + 1].z, qrow[ch + 1].w};
+          tmem_st8(t_q + t_lane + ch * 4, v);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
       umma::fence_smem_to_async();
       umma::fence_before_sync();
@@ -392,7 +411,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
           const uint64_t kd = k_desc + slot * (C::UNIT >> 4);
 #pragma unroll
           for (int k = 0; k < D; k += 16)
-            umma::mma_f16(tmem + (gt & 1) * TK, q_desc + step(128, k), kd + step(TK, k), id_s, k > 0);
+            if constexpr (C::QT)
+              mma_ts(tmem + (gt & 1) * TK, t_q + k / 2, kd + step(TK, k), id_s, k > 0);
+            else
+              umma::mma_f16(tmem + (gt & 1) * TK, q_desc + step(128, k), kd + step(TK, k), id_s, k > 0);
           umma::mma_commit(&b_s[gt & 1]);
           umma::mma_commit(&b_empty[slot]);
           mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
@@ -417,7 +439,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
             for (int n = 0; n < D; n += NV)
 #pragma unroll
               for (int k = 0; k < TK; k += 16)
-                mma_ts(t_o + n, pa + part * (TK / 2) + k / 2, vd + (((n / 64) * (TK * 128) + k * 128) >> 4), id_o);
+                mma_ts(t_o + n, pa + part * (TK / 2) + k / 2, vd + (((n / 64) * (TK * 128) + k * 128) >> 4), id_o, 1);
           umma::mma_commit(&b_pfree[gt % NB]);
           umma::mma_commit(&b_empty[slot]);
           next(slot, phase);
