@@ -78,6 +78,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&v)[8]) {
                : "memory");
 }
 
+// True in one lane of the warp, always the same: issues the products and their
+// commits. (The compiler keeps what this lane does in uniform registers, which
+// the instructions take, where a test of the lane's number leaves moves around
+// each of them.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) {
   constexpr int D = C::D, RP = C::RP, PT = C::PT, TK = C::TK, KW = C::KW, U = C::U, NB = C::NB, NT = C::THREADS;
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
       // address field, which holds 18-bit shared-memory addresses / 16.
       const bool scores = warp == 8;
       if (piece == 0 && !scores) next(slot, phase);  // K of tile t is unit 2 t, V unit 2 t + 1
-      if (lane == 0 && scores) {
+      if (scores) {
         constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
         const uint64_t q_desc = umma::desc_kmajor(umma::smem_u32(qbuf), 128, 0);
         const uint64_t k_desc = umma::desc_kmajor(umma::smem_u32(smem), TK, 0);
@@ -408,20 +418,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
           wait(&b_sfree[gt & 1], ((gt >> 1) & 1) ^ 1);
           umma::fence_after_sync();
           umma::fence_smem_to_async();
-          const uint64_t kd = k_desc + slot * (C::UNIT >> 4);
+          if (elect_one()) {
+            const uint64_t kd = k_desc + slot * (C::UNIT >> 4);
 #pragma unroll
-          for (int k = 0; k < D; k += 16)
-            if constexpr (C::QT)
-              mma_ts(tmem + (gt & 1) * TK, t_q + k / 2, kd + step(TK, k), id_s, k > 0);
-            else
-              umma::mma_f16(tmem + (gt & 1) * TK, q_desc + step(128, k), kd + step(TK, k), id_s, k > 0);
-          umma::mma_commit(&b_s[gt & 1]);
-          umma::mma_commit(&b_empty[slot]);
-          mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
+            for (int k = 0; k < D; k += 16)
+              if constexpr (C::QT)
+                mma_ts(tmem + (gt & 1) * TK, t_q + k / 2, kd + step(TK, k), id_s, k > 0);
+              else
+                umma::mma_f16(tmem + (gt & 1) * TK, q_desc + step(128, k), kd + step(TK, k), id_s, k > 0);
+            umma::mma_commit(&b_s[gt & 1]);
+            umma::mma_commit(&b_empty[slot]);
+            mbar_arrive(&b_s[gt & 1]);  // passes on what the loaders wrote besides the tile
+          }
+          __syncwarp();
           next(slot, phase);
           next(slot, phase);
         }
-      } else if (lane == 0) {
+      } else {
         constexpr int NV = D < 128 ? D : 128;
         constexpr uint32_t id_o = umma::idesc_f16(128, NV, true, false, true);
         const uint64_t v_desc = umma::desc_mnmajor(umma::smem_u32(smem), TK, 0);
@@ -431,28 +444,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
           umma::fence_smem_to_async();
           wait(&b_p[gt % NB], (gt / NB) & 1);
           umma::fence_after_sync();
-          const uint64_t vd = v_desc + slot * (C::UNIT >> 4);
-          const uint32_t pa = t_p + (gt % NB) * C::PCOLS;
+          if (elect_one()) {
+            const uint64_t vd = v_desc + slot * (C::UNIT >> 4);
+            const uint32_t pa = t_p + (gt % NB) * C::PCOLS;
 #pragma unroll
-          for (int part = PT - 1; part >= 0; --part)
+            for (int part = PT - 1; part >= 0; --part)
 #pragma unroll
-            for (int n = 0; n < D; n += NV)
+              for (int n = 0; n < D; n += NV)
 #pragma unroll
-              for (int k = 0; k < TK; k += 16)
-                mma_ts(t_o + n, pa + part * (TK / 2) + k / 2, vd + (((n / 64) * (TK * 128) + k * 128) >> 4), id_o, 1);
-          umma::mma_commit(&b_pfree[gt % NB]);
-          umma::mma_commit(&b_empty[slot]);
+                for (int k = 0; k < TK; k += 16)
+                  mma_ts(t_o + n, pa + part * (TK / 2) + k / 2, vd + (((n / 64) * (TK * 128) + k * 128) >> 4), id_o, 1);
+            umma::mma_commit(&b_pfree[gt % NB]);
+            umma::mma_commit(&b_empty[slot]);
+          }
+          __syncwarp();
           next(slot, phase);
           next(slot, phase);
         }
       }
-      __syncwarp();
     }
     __syncthreads();
     if (s_dead) {
       // a wait ran out: let copies and products in flight finish, then leave
       cp_wait_all();
-      if (warp >= 8 && lane == 0) {
+      if (warp >= 8 && elect_one()) {
         umma::mma_commit(&b_drain);
         umma::mbar_wait(&b_drain, 0, kUmmaWaitTries);
       }
