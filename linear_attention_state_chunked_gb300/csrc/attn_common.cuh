@@ -32,7 +32,9 @@ struct Plan {
   float scale_log2;   // |scale| log2(e); q is negated where scale < 0
   uint32_t negate;
   float slack;        // kSlack in units of q.k
-  uint32_t page_mul, page_shift;  // t / page_size = (mulhi(t, mul) + t) >> shift, t < 2^31
+  uint32_t page_mul, page_shift;    // t / page_size = (mulhi(t, mul) + t) >> shift, t < 2^31
+  uint32_t group_mul, group_shift;  // the same for row / group
+  uint32_t block_mul, block_shift;  // and for item / row_blocks
   float* part;        // [2 grid][block_rows][D] value sums of unfinished pieces
   float2* part_ml;    // [2 grid][block_rows] their (maximum, sum); sum -1: left out
   longlong2* split;   // [grid] the item that begins in range c and goes on past
@@ -61,6 +63,11 @@ __device__ __forceinline__ uint32_t take_bf16(float& a, float& b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// t / page_size, the query token of a row, the kv head of an item
+__device__ __forceinline__ int page_of(const Plan& p, int t) { return (__umulhi(t, p.page_mul) + t) >> p.page_shift; }
+__device__ __forceinline__ int query_of(const Plan& p, int q) { return (__umulhi(q, p.group_mul) + q) >> p.group_shift; }
+__device__ __forceinline__ int head_of(const Plan& p, int it) { return (__umulhi(it, p.block_mul) + it) >> p.block_shift; }
+
 // Units of a request: at least one where it has an output to write.
 __device__ __forceinline__ int units_of(int len, int64_t most) {
   return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
@@ -72,6 +79,7 @@ struct Walk {
   int64_t most;   // longest request allowed
   int per_req;    // items of a request
   int r, len, u;  // the request, its length and units
+  int next_len;   // the next request's length, loaded a piece early
   int it, t0;     // its item, and the item's first unit here
   longlong2 split;
 };
@@ -130,6 +138,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_s
   __syncthreads();
   w.r = static_cast<int>(s_first[0]);
   w.len = a.kv_len[w.r];
+  w.next_len = w.r + 1 < a.batch ? a.kv_len[w.r + 1] : -1;
   w.u = units_of(w.len, w.most);
   w.it = static_cast<int>(s_first[1] / w.u);
   w.t0 = static_cast<int>(s_first[1] % w.u);
@@ -155,7 +164,9 @@ __device__ __forceinline__ bool walk_next(const Plan& p, Walk& w, int t1) {
   if (++w.it == w.per_req) {
     w.it = 0;
     do {
-      w.len = p.a.kv_len[++w.r];
+      ++w.r;
+      w.len = w.next_len;
+      w.next_len = w.r + 1 < p.a.batch ? p.a.kv_len[w.r + 1] : -1;
       w.u = units_of(w.len, w.most);
     } while (w.u == 0);
   }
@@ -193,44 +204,57 @@ template <int D, int KG, int ROWS, int NT, int PITCH = D>
 __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t1, const float* merge,
                                              const float2* merge_ml, bool bad) {
   const lin_attn_args_t& a = p.a;
-  const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * ROWS;
+  const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * ROWS;
   const bool whole = w.t0 == 0 && t1 == w.u;
   const int64_t part = 2 * int64_t(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
   constexpr int LANES = D / 4 < 32 ? D / 4 : 32;  // threads of a row, so many steps of 4 channels
-  for (int row = threadIdx.x / LANES; row < ROWS; row += NT / LANES) {
-    const int q = row0 + row, lane = threadIdx.x % LANES;
-    if (q >= p.rows) break;
-    float top = -INFINITY, sum = 0.0f, f[KG];
-#pragma unroll
-    for (int k = 0; k < KG; ++k) top = fmaxf(top, merge_ml[k * ROWS + row].x);
+  constexpr int STEPS = D / 4 / LANES, AT = NT / LANES;
+  const int lane = threadIdx.x % LANES;
+#pragma unroll 1  // once per piece: what counts is how much code it brings in
+  for (int i = 0; i < (ROWS + AT - 1) / AT; ++i) {
+    const int row = threadIdx.x / LANES + i * AT, q = row0 + row;
+    if (row >= ROWS || q >= p.rows) continue;
+    float2 ml[KG];
+    float4 y[KG][STEPS];
 #pragma unroll
     for (int k = 0; k < KG; ++k) {
-      const float2 ml = merge_ml[k * ROWS + row];
+      ml[k] = merge_ml[k * ROWS + row];
+#pragma unroll
+      for (int x = 0; x < STEPS; ++x)
+        y[k][x] = *reinterpret_cast<const float4*>(merge + (k * ROWS + row) * PITCH + (x * LANES + lane) * 4);
+    }
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < KG; ++k) top = fmaxf(top, ml[k].x);
+    float4 v[STEPS];
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
       // 0 where a copy saw nothing (a NaN sum goes on)
-      f[k] = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-      sum = fmaf(f[k], ml.y, sum);
+      const float f = ml[k].y == 0.0f ? 0.0f : ml[k].x == top ? 1.0f : exp2_fast(ml[k].x - top);
+      sum = fmaf(f, ml[k].y, sum);
+#pragma unroll
+      for (int x = 0; x < STEPS; ++x) {
+        v[x].x = fmaf(f, y[k][x].x, v[x].x), v[x].y = fmaf(f, y[k][x].y, v[x].y);
+        v[x].z = fmaf(f, y[k][x].z, v[x].z), v[x].w = fmaf(f, y[k][x].w, v[x].w);
+      }
     }
     const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int j = q / p.group;
+    const int j = query_of(p, q);
     const int64_t out = ((int64_t(w.r) * a.n_q + j) * a.num_q_heads + hk * p.group + q - j * p.group) * D;
 #pragma unroll
-    for (int d = lane * 4; d < D; d += LANES * 4) {
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int k = 0; k < KG; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(merge + (k * ROWS + row) * PITCH + d);
-        v.x = fmaf(f[k], y.x, v.x), v.y = fmaf(f[k], y.y, v.y);
-        v.z = fmaf(f[k], y.z, v.z), v.w = fmaf(f[k], y.w, v.w);
-      }
+    for (int x = 0; x < STEPS; ++x) {
+      const int d = (x * LANES + lane) * 4;
       if (!whole) {
-        *reinterpret_cast<float4*>(p.part + (part * ROWS + row) * D + d) = v;
+        *reinterpret_cast<float4*>(p.part + (part * ROWS + row) * D + d) = v[x];
       } else if (bad) {
       } else if (a.out_dtype == LIN_F32) {
         *reinterpret_cast<float4*>(static_cast<float*>(a.out) + out + d) =
-            make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+            make_float4(v[x].x * scale, v[x].y * scale, v[x].z * scale, v[x].w * scale);
       } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * scale, v.y * scale);
-        const __nv_bfloat162 hi = __floats2bfloat162_rn(v.z * scale, v.w * scale);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[x].x * scale, v[x].y * scale);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(v[x].z * scale, v[x].w * scale);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + out + d) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
@@ -238,9 +262,6 @@ __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t
     if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? -1.0f : sum);
   }
 }
-
-// t / page_size
-__device__ __forceinline__ int page_of(const Plan& p, int t) { return (__umulhi(t, p.page_mul) + t) >> p.page_shift; }
 
 // One translation unit per head_dim and kind of kernel.
 cudaError_t launch_d64(const Plan& p, int row_tiles, int grid, cudaStream_t s);

@@ -74,7 +74,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = ((r * p.a.n_q + q / p.group) * p.a.num_q_heads + hk * p.group + q % p.group) * D;
+    const int j = query_of(p, q);
+    const int64_t at = ((r * p.a.n_q + j) * p.a.num_q_heads + hk * p.group + q - j * p.group) * D;
     for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
       float x = 0.0f;
 #pragma unroll
@@ -123,6 +124,14 @@ int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a, const Shape& f) {
   return static_cast<int>(most < int64_t(sms) * f.ctas && most > 0 ? most : int64_t(sms) * f.ctas);
 }
 
+// Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
+// mul = floor(2^32 (2^s - d) / d) + 1
+void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
+  shift = 0;
+  while ((int64_t(1) << shift) < d) ++shift;
+  mul = static_cast<uint32_t>((((uint64_t(1) << shift) - d) << 32) / d + 1);
+}
+
 }  // namespace
 }  // namespace attn
 
@@ -145,11 +154,9 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;  // log2(e)
   p.slack = attn::kSlack / p.scale_log2;  // infinite where scale is 0: one reference does
   p.negate = !(a.scale < 0.0f) ? 0u : c.dtype == LIN_BF16 ? 0x80008000u : 0x80000000u;
-  // Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
-  // mul = floor(2^32 (2^s - d) / d) + 1
-  p.page_shift = 0;
-  while ((int64_t(1) << p.page_shift) < c.page_size) ++p.page_shift;
-  p.page_mul = static_cast<uint32_t>((((uint64_t(1) << p.page_shift) - c.page_size) << 32) / c.page_size + 1);
+  attn::divide_by(c.page_size, p.page_mul, p.page_shift);
+  attn::divide_by(p.group, p.group_mul, p.group_shift);
+  attn::divide_by(p.row_blocks, p.block_mul, p.block_shift);
   char* w = static_cast<char*>(ws);
   p.part = reinterpret_cast<float*>(w);
   w += size_t(2) * grid * f.block_rows * c.head_dim * sizeof(float);

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
 
   while (true) {
     const int t1 = walk_until(w), r = w.r;
-    const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * 16 * RT;
+    const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * 16 * RT;
     const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
     const int base = w.len - a.n_q;  // tokens that every query sees
     const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         const int row = x / CPR, ch = x % CPR, q = row0 + row;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (q < p.rows) {
-          const int j = q / p.group, h = hk * p.group + q % p.group;
+          const int j = query_of(p, q), h = hk * p.group + q - j * p.group;
           v = *reinterpret_cast<const uint4*>(qb + j * a.token_stride + h * ROWB + ch * 16);
           v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
         }
@@ -216,8 +216,8 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     __syncthreads();
     const bool bad = s_bad;
     const int qa = row0 + rt * 16 + g, qb2 = qa + 8;
-    const uint32_t see0 = qa < p.rows ? s_see[qa / p.group] : 0u;
-    const uint32_t see1 = qb2 < p.rows ? s_see[qb2 / p.group] : 0u;
+    const uint32_t see0 = qa < p.rows ? s_see[query_of(p, qa)] : 0u;
+    const uint32_t see1 = qb2 < p.rows ? s_see[query_of(p, qb2)] : 0u;
 
     constexpr bool QREG = C::QREG;
     const uint32_t qat = qs + (BF ? chunk_at<ROWB>(rt * 16 + (lane & 15), lane >> 4)

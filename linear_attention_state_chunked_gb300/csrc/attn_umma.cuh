@@ -41,7 +41,7 @@ struct UCfg {
   // cycles for its 16; tensor memory has no room beside O of 256 channels)
   static constexpr bool QT = D <= 128;
   static constexpr int QCOLS = QT ? D / 2 : 0;
-  static constexpr int QB = QT ? 0 : 128 * D * 2;
+  static constexpr int QB = (QT ? RP : 128) * D * 2;
   static constexpr int FREE = 224 * 1024 - QB;
   static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
   static constexpr int SMEM = U * UNIT + QB;
@@ -142,26 +142,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 
   while (true) {
     const int t1 = walk_until(w), r = w.r;
-    const int hk = w.it / p.row_blocks, row0 = (w.it % p.row_blocks) * RP;
+    const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * RP;
     const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
     const int base = w.len - a.n_q;  // tokens that every query sees
     const int tiles = (key_end - key_begin + TK - 1) / TK;
 
     if (warp < 4) {
       // ---- softmax ---------------------------------------------------------------
-      // every thread brings its lane's row of queries
+      // The queries, row by row, to shared memory: q there (every copy of it), or
+      // once, for the lanes to take their rows to tensor memory
+      constexpr int CPR = D / 8;
       const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
-      uint4 qrow[D / 8];
-      {
-        const int q = row0 + tid % RP;
-        const bool live = q < p.rows;
-        const int j = live ? q / p.group : 0;
-        const char* src = static_cast<const char*>(a.q) + r * a.req_stride + j * a.token_stride +
-                          (live ? hk * p.group + q - j * p.group : 0) * (D * 2);
-#pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) {
-          qrow[ch] = live ? reinterpret_cast<const uint4*>(src)[ch] : make_uint4(0, 0, 0, 0);
+      const char* const qsrc = static_cast<const char*>(a.q) + r * a.req_stride + hk * p.group * (D * 2);
+#pragma unroll 8
+      for (int x = tid; x < RP * CPR; x += 128) {
+        const int row = x / CPR, ch = x % CPR, q = row0 + row;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q < p.rows) {
+          const int j = query_of(p, q);
+          v = *reinterpret_cast<const uint4*>(qsrc + j * a.token_stride + (q - j * p.group) * (D * 2) + ch * 16);
+          v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
         }
+#pragma unroll
+        for (int k = 0; k < (C::QT ? 1 : C::COPIES); ++k)
+          *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(k * RP + row, ch * 8, C::QT ? RP : 128)) = v;
       }
       if (warp == 0) draft_sets(p, r, s_see, s_bad);
       {
@@ -171,31 +175,27 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
 #pragma unroll
         for (int i = 0; i < D; i += 32) umma::tmem_st32(t_o + t_lane + i, z);
         if (piece == 0) {  // other copies' tokens keep weight 0
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < NB * C::PCOLS; i += 32) umma::tmem_st32(t_p + t_lane + i, z);
         }
       }
-#pragma unroll
-      for (int ch = 0; ch < D / 8; ++ch) {
-        uint4& v = qrow[ch];
-        v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
-        if constexpr (!C::QT) *reinterpret_cast<uint4*>(qbuf + umma::rp_offset(tid, ch * 8, 128)) = v;
-      }
       if constexpr (C::QT) {
+        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-        for (int ch = 0; ch < D / 8; ch += 2) {
-          const uint32_t v[8] = {qrow[ch].x, qrow[ch].y, qrow[ch].z, qrow[ch].w,
-                                 qrow[ch + 1].x, qrow[ch + 1].y, qrow[ch + 1].z, qrow[ch + 1].w};
+        for (int ch = 0; ch < CPR; ch += 2) {
+          const uint4 y0 = *reinterpret_cast<const uint4*>(qbuf + umma::rp_offset(tid % RP, ch * 8, RP));
+          const uint4 y1 = *reinterpret_cast<const uint4*>(qbuf + umma::rp_offset(tid % RP, ch * 8 + 8, RP));
+          const uint32_t v[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
           tmem_st8(t_q + t_lane + ch * 4, v);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       }
-      umma::fence_smem_to_async();
+      if (!C::QT) umma::fence_smem_to_async();
       umma::fence_before_sync();
       asm volatile("bar.sync 1, 128;" ::: "memory");
       if (lane == 0) mbar_arrive(&b_q);
       const int copy = tid / RP, q = row0 + tid % RP;
-      const uint32_t see = q < p.rows ? s_see[q / p.group] : 0u;
+      const uint32_t see = q < p.rows ? s_see[query_of(p, q)] : 0u;
       float cut = -INFINITY, z = 0.0f, l = 0.0f;  // as in attn_kernel.cuh
       for (int i = 0; i < tiles; ++i) {
         const uint32_t gt = tile0 + i;
@@ -265,8 +265,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
           next(sl, ph);
           vbuf = smem + sl * C::UNIT;
           wait(&b_full[sl], ph);
-          for (int x = tid; x < C::UNIT / 16; x += 128) {
-            const uint4 v = reinterpret_cast<const uint4*>(vbuf)[x];
+          const int tile_key = key_begin + i * TK;
+          const int from = max(0, base - tile_key), many = min(TK, key_end - tile_key) - from;
+          for (int x = tid; x < many * CPR; x += 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vbuf + umma::rp_offset(from + x / CPR, x % CPR * 8, TK));
             const uint32_t y[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
