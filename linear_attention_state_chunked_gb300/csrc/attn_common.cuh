@@ -1,10 +1,12 @@
 // What the kernels of decode attention share: the plan of a call, the split of
 // a batch's work over the CTAs, and the end of a piece of work.
 //
-// A unit is kUnit tokens of one item = (request, kv head, block of rows). The
+// A unit is kUnit tokens of one item = (request, kv head, block of rows), and an
+// item counts as item_cost units more, for what its start and end take. The
 // units of the whole batch, laid end to end, are cut into one equal range per
 // CTA (lengths are read on the device), so a batch of ragged lengths and a
-// single long request load the SMs alike. An item inside one range is finished
+// single long request load the SMs alike. A border among an item's first
+// item_cost units moves to the item's start. An item inside one range is finished
 // there; one that crosses a border leaves (value sums, m, sum) of each piece in
 // the workspace, and a second kernel joins them in range order, so results do
 // not depend on timing.
@@ -29,6 +31,7 @@ struct Plan {
   int rows;           // n_q * group
   int block_rows;     // rows of an item
   int row_blocks;     // items of one (request, kv head)
+  int item_cost;      // of an item besides its tokens, in units
   float scale_log2;   // |scale| log2(e); q is negated where scale < 0
   uint32_t negate;
   float slack;        // kSlack in units of q.k
@@ -75,7 +78,7 @@ __device__ __forceinline__ int units_of(int len, int64_t most) {
 
 // Where a CTA is in its range.
 struct Walk {
-  int64_t cur, end, total, ranges;
+  int64_t base, end, total, ranges;  // where the item and the range lie among all units
   int64_t most;   // longest request allowed
   int per_req;    // items of a request
   int r, len, u;  // the request, its length and units
@@ -83,6 +86,12 @@ struct Walk {
   int it, t0;     // its item, and the item's first unit here
   longlong2 split;
 };
+
+// The piece's end: the first of the item's units past it.
+__device__ __forceinline__ int walk_until(const Plan& p, const Walk& w) {
+  const int64_t upto = w.end - w.base - p.item_cost;
+  return static_cast<int>(upto >= w.u ? w.u : upto > 0 ? upto : 0);
+}
 
 // The CTA's range, from a scan over the requests' lengths by all NT threads.
 // False where there is no work for it.
@@ -100,9 +109,9 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_s
   for (int r = r0; r < r1; ++r) {
     const int len = a.kv_len[r];
     if (len > w.most && blockIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
-    mine += units_of(len, w.most);
+    const int u = units_of(len, w.most);
+    if (u > 0) mine += int64_t(u + p.item_cost) * w.per_req;
   }
-  mine *= w.per_req;
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -122,44 +131,46 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_s
     if (tid == 0) p.split[blockIdx.x].x = -1;
     return false;
   }
-  w.cur = w.total * blockIdx.x / w.ranges;
+  const int64_t cur = w.total * blockIdx.x / w.ranges;
   w.end = w.total * (blockIdx.x + 1) / w.ranges;
-  if (w.cur >= upto - mine && w.cur < upto) {
+  if (cur >= upto - mine && cur < upto) {
     int64_t at = upto - mine;
     int r = r0;
     for (;; ++r) {
-      const int64_t n = int64_t(units_of(a.kv_len[r], w.most)) * w.per_req;
-      if (w.cur < at + n) break;
+      const int u = units_of(a.kv_len[r], w.most);
+      const int64_t n = u > 0 ? int64_t(u + p.item_cost) * w.per_req : 0;
+      if (cur < at + n) break;
       at += n;
     }
     s_first[0] = r;
-    s_first[1] = w.cur - at;
+    s_first[1] = at;
   }
   __syncthreads();
   w.r = static_cast<int>(s_first[0]);
   w.len = a.kv_len[w.r];
   w.next_len = w.r + 1 < a.batch ? a.kv_len[w.r + 1] : -1;
   w.u = units_of(w.len, w.most);
-  w.it = static_cast<int>(s_first[1] / w.u);
-  w.t0 = static_cast<int>(s_first[1] % w.u);
-  return true;
-}
-
-// The piece's end: the first unit past it.
-__device__ __forceinline__ int walk_until(const Walk& w) {
-  return static_cast<int>(min(int64_t(w.u), w.t0 + (w.end - w.cur)));
+  w.it = static_cast<int>((cur - s_first[1]) / (w.u + p.item_cost));
+  w.base = s_first[1] + int64_t(w.it) * (w.u + p.item_cost);
+  w.t0 = max(0, static_cast<int>(cur - w.base) - p.item_cost);
+  if (walk_until(p, w) > w.t0) return true;
+  if (tid == 0) p.split[blockIdx.x].x = -1;
+  return false;
 }
 
 // On to the next piece; false at the range's end.
 __device__ __forceinline__ bool walk_next(const Plan& p, Walk& w, int t1) {
-  if (w.t0 == 0 && t1 < w.u) {
-    // the item goes on: its last unit lies in the range whose end is the first past it
-    const int64_t last = w.cur + w.u - 1;
-    w.split.x = int64_t(w.r) * w.per_req + w.it;
-    w.split.y = ((last + 1) * w.ranges - 1) / w.total - blockIdx.x + 1;
+  if (t1 < w.u) {
+    if (w.t0 == 0) {
+      // the item goes on: its last unit lies in the range whose end is the first past it
+      const int64_t last = w.base + w.u + p.item_cost - 1;
+      w.split.x = int64_t(w.r) * w.per_req + w.it;
+      w.split.y = ((last + 1) * w.ranges - 1) / w.total - blockIdx.x + 1;
+    }
+    return false;
   }
-  w.cur += t1 - w.t0;
-  if (w.cur >= w.end) return false;
+  w.base += w.u + p.item_cost;
+  if (w.base >= w.end) return false;
   w.t0 = 0;
   if (++w.it == w.per_req) {
     w.it = 0;
@@ -170,7 +181,7 @@ __device__ __forceinline__ bool walk_next(const Plan& p, Walk& w, int t1) {
       w.u = units_of(w.len, w.most);
     } while (w.u == 0);
   }
-  return true;
+  return walk_until(p, w) > 0;
 }
 
 // What each draft sees of the drafts, by one warp: lane j's set goes to see[j].

@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   float2* merge_ml = reinterpret_cast<float2*>(merge + KG * 16 * RT * D);  // [KG][16 RT]
 
   while (true) {
-    const int t1 = walk_until(w), r = w.r;
+    const int t1 = walk_until(p, w), r = w.r;
     const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * 16 * RT;
     const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
     const int base = w.len - a.n_q;  // tokens that every query sees

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
   };
 
   while (true) {
-    const int t1 = walk_until(w), r = w.r;
+    const int t1 = walk_until(p, w), r = w.r;
     const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * RP;
     const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
     const int base = w.len - a.n_q;  // tokens that every query sees
