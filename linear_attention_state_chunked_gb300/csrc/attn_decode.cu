@@ -110,7 +110,7 @@ Shape shape_of(const lin_kv_cache_t& c, int rows) {
   const bool b = c.dtype == LIN_BF16;
   if (b && rows > 16) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7};
   const int rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), 2};
+  return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), b ? 3 : 2};
 }
 
 // CTAs of the main kernel: what is resident at once, or one per unit where the

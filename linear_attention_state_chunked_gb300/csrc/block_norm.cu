@@ -7,8 +7,11 @@
 // between its two norms. A row belongs to a set of whole warps (several rows
 // share a CTA where rows are short), a thread to vectors of 8 consecutive
 // channels, so group sums of 8 .. 256 channels are butterflies inside a warp
-// and row sums add one barrier. Where 8-element vectors do not fit (an odd
-// width or row start) a thread owns single channels instead.
+// and row sums add one barrier. Rows of an odd width start anywhere in a vector
+// of 8, but all arrays of one call alike: there the vectors are shifted (channel
+// c0 - shift on), and only a row's first and last are taken by elements. Where
+// the arrays differ in that, or groups do not end with vectors, a thread owns
+// single channels instead.
 
 #include "common.cuh"
 #include "step_internal.h"
@@ -18,6 +21,7 @@ namespace {
 
 constexpr int kNormThreads = 512;   // most threads of one row
 constexpr int kNormBlock = 256;     // rows shorter than this share a CTA
+constexpr int kManyRows = 2048;     // rows that fill the GPU several times over
 
 template <int DT, int VEC>
 struct Raw;  // VEC elements as loaded
@@ -58,6 +62,21 @@ template <> struct Raw<LIN_BF16, 1> {
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = bf16_bits_to_f32(a); }
 };
 
+// The elements c0 .. c0 + 7 of a row at `p` + `row` that lie in [0, C), 0 elsewhere.
+template <int DT>
+__device__ __forceinline__ void load_part(Raw<DT, 8>& r, const void* p, int64_t row, int c0, int C) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = c0 + i >= 0 && c0 + i < C ? load_elem(p, row + c0 + i, DT) : 0.0f;
+  Vec8<DT>::store(&r, v);  // exact: the values are of that type
+}
+template <int DT>
+__device__ __forceinline__ void put_part(void* p, int64_t row, int c0, int C, const float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + i >= 0 && c0 + i < C) store_elem(p, row + c0 + i, DT, v[i]);
+}
+
 template <int DT>
 __device__ __forceinline__ void put(void* p, int64_t i, const float (&v)[8]) {
   Vec8<DT>::store(static_cast<char*>(p) + i * (DT == LIN_BF16 ? 2 : 4), v);
@@ -86,12 +105,24 @@ __device__ __forceinline__ float row_sum(float v, float* part, int tpr, int tx) 
   return v;
 }
 
+// 1 / (1 + 2^(-x log2 e)) in four instructions (the gate alone would else bound a
+// long prompt's call by its instructions): off by about (|x| + 4) 2^-24 of itself,
+// from the exponent's product; 0 where the power overflows.
+__device__ __forceinline__ float sigmoid(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
+}
+
 // How the first norm's sums are taken: over the row, over aligned sets of
 // lanes, or through shared memory.
 enum GroupMode { kGroupNone = 0, kGroupRow = 1, kGroupLanes = 2, kGroupShared = 3 };
 
-template <int XT, int IOT, int HT, int VEC, int NV>
-__global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024) block_norm_kernel(const lin_norm_args_t a, int mode, int shared_floats) {
+// VEC 8 with SH: shifted vectors (the group is the row, if any).
+template <int XT, int IOT, int HT, int VEC, int NV, bool SH>
+__global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024)
+block_norm_kernel(const lin_norm_args_t a, int mode, int shared_floats) {
   extern __shared__ float sm[];
   const int tpr = blockDim.x, tx = threadIdx.x;
   float* part = sm + threadIdx.y * 32;
@@ -99,29 +130,38 @@ __global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024) block_norm_ker
   const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   const int C = a.channels;
   const bool live = row < a.rows;
+  const int shift = SH ? static_cast<int>((row * a.x_stride) & 7) : 0;
+  auto chan = [&](int v) { return (v * tpr + tx) * VEC - shift; };
+  auto in = [&](int c) { return live && c < C && (!SH || c > -VEC); };
+  auto whole = [&](int c) { return !SH || (c >= 0 && c + VEC <= C); };
   Raw<XT, VEC> rx[NV];
   Raw<IOT, VEC> rg[NV];
   Raw<HT, VEC> rr[NV];
   // every load of the row is in flight before the first sum
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + tx) * VEC;
-    if (live && c < C) {
+    const int c = chan(v);
+    if (!in(c)) continue;
+    if (whole(c)) {
       rx[v].load(a.x, row * a.x_stride + c);
       if (a.gate) rg[v].load(a.gate, row * a.gate_stride + c);
       if (a.residual) rr[v].load(a.residual, row * a.residual_stride + c);
+    } else if constexpr (SH) {
+      load_part(rx[v], a.x, row * a.x_stride, c, C);
+      if (a.gate) load_part(rg[v], a.gate, row * a.gate_stride, c, C);
+      if (a.residual) load_part(rr[v], a.residual, row * a.residual_stride, c, C);
     }
   }
   float t[NV][VEC];
   float ss[NV], all = 0.0f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const bool in = live && (v * tpr + tx) * VEC < C;
-    if (in) rx[v].get(t[v]);
+    const bool mine = in(chan(v));
+    if (mine) rx[v].get(t[v]);
     ss[v] = 0.0f;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
-      if (!in) t[v][i] = 0.0f;
+      if (!mine) t[v][i] = 0.0f;
       ss[v] = fmaf(t[v][i], t[v][i], ss[v]);
     }
     all += ss[v];
@@ -157,16 +197,26 @@ __global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024) block_norm_ker
       }
     }
   }
+  // VEC weights from channel c on
+  auto weights = [&](const void* w, int c, float (&out)[VEC]) {
+    if constexpr (SH) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) out[i] = c + i >= 0 && c + i < C ? load_elem(w, c + i, IOT) : 0.0f;
+    } else {
+      Raw<IOT, VEC> rw;
+      rw.load(w, c);
+      rw.get(out);
+    }
+  };
   all = 0.0f;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + tx) * VEC;
-    if (!live || c >= C) continue;
+    const int c = chan(v);
+    if (!in(c)) continue;
     float w[VEC];
     if (mode != kGroupNone) {
-      Raw<IOT, VEC> rw;
-      rw.load(a.w_post, c % a.group);
-      rw.get(w);
+      // groups of whole lanes are powers of two wide
+      weights(a.w_post, mode == kGroupRow ? c : mode == kGroupLanes ? c & (a.group - 1) : c % a.group, w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) t[v][i] *= ss[v] * w[i];
     }
@@ -174,14 +224,12 @@ __global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024) block_norm_ker
       rg[v].get(w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float sig = __fdividef(1.0f, 1.0f + expf(-w[i]));  // 0 where expf overflows
+        const float sig = sigmoid(w[i]);
         t[v][i] *= a.gate_act == LIN_ACT_SILU ? w[i] * sig : sig;
       }
     }
     if (a.scale_w) {
-      Raw<IOT, VEC> rw;
-      rw.load(a.scale_w, c);
-      rw.get(w);
+      weights(a.scale_w, c, w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) t[v][i] *= w[i];
     }
@@ -189,39 +237,52 @@ __global__ void __launch_bounds__(VEC == 8 ? kNormThreads : 1024) block_norm_ker
       rr[v].get(w);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) t[v][i] = fmaf(a.scale, t[v][i], w[i]);
-    } else {
+    } else if (a.scale != 1.0f) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) t[v][i] *= a.scale;
     }
-    if (a.h_out) put<HT>(a.h_out, row * a.h_stride + c, t[v]);
+    if (a.h_out) {
+      if (whole(c))
+        put<HT>(a.h_out, row * a.h_stride + c, t[v]);
+      else if constexpr (SH)
+        put_part<HT>(a.h_out, row * a.h_stride, c, C, t[v]);
+    }
+    if (a.w_pre) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) all = fmaf(t[v][i], t[v][i], all);
+      for (int i = 0; i < VEC; ++i) all = fmaf(t[v][i], t[v][i], all);
+    }
   }
   if (!a.w_pre) return;
   const float s = rsqrtf(row_sum(all, part, tpr, tx) / static_cast<float>(C) + a.eps);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int c = (v * tpr + tx) * VEC;
-    if (!live || c >= C) continue;
-    Raw<IOT, VEC> rw;
+    const int c = chan(v);
+    if (!in(c)) continue;
     float w[VEC];
-    rw.load(a.w_pre, c);
-    rw.get(w);
+    weights(a.w_pre, c, w);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) t[v][i] *= s * w[i];
-    put<IOT>(a.y, row * a.y_stride + c, t[v]);
+    if (whole(c))
+      put<IOT>(a.y, row * a.y_stride + c, t[v]);
+    else if constexpr (SH)
+      put_part<IOT>(a.y, row * a.y_stride, c, C, t[v]);
   }
 }
 
 bool vec_ok(const void* p, int64_t stride) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0);
 }
+// the row starts at the same place of a vector of 8 as x's
+bool shift_ok(const void* p, int64_t stride, int dt, int64_t x_stride) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (8 * dtype_size(dt)) == 0 && (stride - x_stride) % 8 == 0);
+}
 
-template <int XT, int IOT, int HT, int VEC, int NV>
-cudaError_t run(const lin_norm_args_t& a, int tpr, int rows, int mode, cudaStream_t s) {
+template <int XT, int IOT, int HT, int VEC, int NV, bool SH = false>
+cudaError_t run(const lin_norm_args_t& a, int tpr, int mode, cudaStream_t s) {
+  const int rows = tpr >= kNormBlock ? 1 : kNormBlock / tpr;
   const int shared = mode == kGroupShared ? (a.channels + VEC - 1) / VEC : 0;
   const size_t smem = sizeof(float) * rows * (32 + shared);
-  auto kern = block_norm_kernel<XT, IOT, HT, VEC, NV>;
+  auto kern = block_norm_kernel<XT, IOT, HT, VEC, NV, SH>;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
@@ -237,31 +298,38 @@ cudaError_t pick(const lin_norm_args_t& a, cudaStream_t s) {
                    vec_ok(a.gate, a.gate_stride) && vec_ok(a.residual, a.residual_stride) &&
                    vec_ok(a.h_out, a.h_stride) && vec_ok(a.y, a.y_stride) && vec_ok(a.w_post, 0) &&
                    vec_ok(a.scale_w, 0) && vec_ok(a.w_pre, 0);
-  const int per = vec ? 8 : 1;
-  const int vecs = (a.channels + per - 1) / per;
-  const int most = vec ? kNormThreads : 1024;
-  // the fewest vectors per thread, of 1, 2, 4, 8 (and 32 single channels)
-  int nv = 1;
-  while (vecs > most * nv) nv *= 2;
-  const int tpr = ((vecs + nv - 1) / nv + 31) / 32 * 32;
-  const int rows = tpr >= kNormBlock ? 1 : kNormBlock / tpr;
+  const bool shift = !vec && (!a.w_post || a.group == a.channels) && shift_ok(a.x, a.x_stride, XT, a.x_stride) &&
+                     shift_ok(a.gate, a.gate_stride, IOT, a.x_stride) &&
+                     shift_ok(a.residual, a.residual_stride, HT, a.x_stride) &&
+                     shift_ok(a.h_out, a.h_stride, HT, a.x_stride) && shift_ok(a.y, a.y_stride, IOT, a.x_stride);
   int mode = kGroupNone;
   if (a.w_post) {
-    const int lanes = a.group / per;
+    const int lanes = vec ? a.group / 8 : a.group;
     mode = a.group == a.channels ? kGroupRow
            : lanes <= 32 && (lanes & (lanes - 1)) == 0 ? kGroupLanes : kGroupShared;
   }
-  if (vec) {
-    if (nv == 1) return run<XT, IOT, HT, 8, 1>(a, tpr, rows, mode, s);
-    if (nv == 2) return run<XT, IOT, HT, 8, 2>(a, tpr, rows, mode, s);
-    if (nv == 4) return run<XT, IOT, HT, 8, 4>(a, tpr, rows, mode, s);
-    return run<XT, IOT, HT, 8, 8>(a, tpr, rows, mode, s);
+  if (vec || shift) {
+    const int vecs = vec ? a.channels / 8 : (a.channels + 14) / 8;
+    // Vectors per thread: one, or two where many long rows let bytes in flight
+    // count for more than threads (8192 rows of 4096 channels 60.9 to 53.4 us; rows
+    // of 512, 41.4 against 42.4; shifted rows of 1533, 15.4 against 17.8), and more
+    // where kNormThreads demand it.
+    int nv = vec && a.rows >= kManyRows && vecs >= 256 ? 2 : 1;
+    while (vecs > kNormThreads * nv) nv *= 2;
+    const int tpr = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+    if (vec) {
+      if (nv == 1) return run<XT, IOT, HT, 8, 1>(a, tpr, mode, s);
+      if (nv == 2) return run<XT, IOT, HT, 8, 2>(a, tpr, mode, s);
+      if (nv == 4) return run<XT, IOT, HT, 8, 4>(a, tpr, mode, s);
+      return run<XT, IOT, HT, 8, 8>(a, tpr, mode, s);
+    }
+    if (nv == 1) return run<XT, IOT, HT, 8, 1, true>(a, tpr, mode, s);
+    if (nv == 2) return run<XT, IOT, HT, 8, 2, true>(a, tpr, mode, s);
+    if (nv == 4) return run<XT, IOT, HT, 8, 4, true>(a, tpr, mode, s);
+    if (a.channels <= 4096 * 8 - 8) return run<XT, IOT, HT, 8, 8, true>(a, tpr, mode, s);
   }
-  if (nv <= 4) {
-    const int t4 = ((vecs + 3) / 4 + 31) / 32 * 32;
-    return run<XT, IOT, HT, 1, 4>(a, t4, t4 >= kNormBlock ? 1 : kNormBlock / t4, mode, s);
-  }
-  return run<XT, IOT, HT, 1, 32>(a, 1024, 1, mode, s);
+  if (a.channels <= 4096) return run<XT, IOT, HT, 1, 4>(a, ((a.channels + 3) / 4 + 31) / 32 * 32, mode, s);
+  return run<XT, IOT, HT, 1, 32>(a, 1024, mode, s);
 }
 
 }  // namespace
