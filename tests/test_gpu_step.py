@@ -190,6 +190,27 @@ def test_attn_many_short_requests():
     check_attn(cache, table, queries(700, 1, 4, 1, 64, BF, gen), lens, BF)
 
 
+@pytest.mark.parametrize("D,n", [(64, 1), (128, 3), (256, 8)])
+def test_attn_fp32_error_does_not_grow_with_the_length(D, n):
+    """fp32 sums over 64 times the tokens: every rounding is to nearest, so errors
+    grow as the outputs' own random sum does. A bias of one cut-off place per
+    addition would show: 16,384 tokens are 1,024 additions, 2^-14 of the outputs
+    at the most. The bound is 2^-20, four places above the products' 2^-22."""
+    gen = torch.Generator().manual_seed(D)
+    for length in (256, 16384):
+        cache, table, _ = make_cache([length], 64, 1, D, F32, seed=length)
+        q = queries(1, n, 4, 1, D, F32, gen)
+        out = torch.empty((1, n, 4, D), device="cuda")
+        L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table.cuda(),
+                                kv_len=torch.tensor([length], dtype=torch.int32).cuda())
+        at = table[0, :length // 64].long().cuda()
+        k, v = (t[0, at].reshape(length, D).double() for t in (cache.k, cache.v))
+        s = torch.einsum("jhd,td->jht", q[0].double(), k) * D ** -0.5
+        hidden = torch.arange(length, device="cuda") > length - n + torch.arange(n, device="cuda")[:, None]
+        want = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1) @ v
+        assert float((out[0] - want).norm() / want.norm()) < 2.0 ** -20
+
+
 def test_attn_repeats_bit_for_bit():
     lens = [4000, 77, 1500]
     cache, table, gen = make_cache(lens, 16, 2, 128, BF, seed=8)
