@@ -90,15 +90,15 @@ def _entry(name, *argtypes):
 _call_append = _entry("lin_state_kv_append", _vp, ctypes.c_char_p, _vp)
 _call_attn = _entry("lin_state_attn_decode", _vp, ctypes.c_char_p, _vp, ctypes.c_size_t, _vp)
 _call_norm = _entry("lin_state_block_norm", ctypes.c_char_p, _vp)
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+# the current stream's handle without the object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _stream_of(stream, t: torch.Tensor):
     """The given stream's handle, or that of the current stream of t's device."""
     if stream is None:
-        if t.is_cuda and _raw_stream is not None:
-            return _raw_stream(t.get_device())
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -156,13 +156,19 @@ def _raise(rc: int, where: str):
     raise LinStateError(rc, where)
 
 
+def _addr(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name}: want a CUDA tensor, got one on {t.device}")
+    return t.data_ptr()
+
+
 def _ptr32(t: Optional[torch.Tensor], name: str, shape) -> int:
     """Address of a contiguous int32 tensor of this shape, or 0 for None."""
     if t is None:
         return 0
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous int32 tensor {shape}, got {tuple(t.shape)} of {t.dtype}")
-    return t.data_ptr()
+    return _addr(t, name)
 
 
 def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype):
@@ -181,7 +187,7 @@ def _table(t: torch.Tensor, batch: int):
     if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and s[1] != 1):
         raise ValueError(f"page_table: want int32 [{batch}][max_pages] with contiguous rows, got "
                          f"{tuple(shape)} of {t.dtype}")
-    return shape[1], t.data_ptr(), s[0]
+    return shape[1], _addr(t, "page_table"), s[0]
 
 
 def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_tok=None,
@@ -198,7 +204,7 @@ def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_
     B, n = shape[0], shape[1]
     es = 2 if cache.dtype is torch.bfloat16 else 4
     pages, table, pstride = _table(page_table, B)
-    a = _pack_append(layer, B, n, pages, k.data_ptr(), v.data_ptr(), s[0] * es, s[1] * es, table, pstride,
+    a = _pack_append(layer, B, n, pages, _addr(k, "k"), _addr(v, "v"), s[0] * es, s[1] * es, table, pstride,
                      _ptr32(pos, "pos", (B,)), _ptr32(n_tok, "n_tok", (B,)),
                      _ptr32(parent, "parent", (B, n)), _ptr32(accept_node, "accept_node", (B,)),
                      0 if status is None else status.data_ptr())
@@ -235,16 +241,18 @@ def lin_state_attn_decode(cache: KVCache, *, layer: int, q, out, page_table, kv_
     es = 2 if cache.dtype is torch.bfloat16 else 4
     pages, table, pstride = _table(page_table, B)
     a = _pack_attn(layer, B, n, Hq, _dt(out.dtype), pages, D ** -0.5 if scale is None else scale,
-                   q.data_ptr(), s[0] * es, s[1] * es, out.data_ptr(), table, pstride,
+                   _addr(q, "q"), s[0] * es, s[1] * es, _addr(out, "out"), table, pstride,
                    _ptr32(kv_len, "kv_len", (B,)), _ptr32(parent, "parent", (B, n)),
                    0 if status is None else status.data_ptr())
     if workspace is None:
         need = lin_state_attn_workspace(cache, batch=B, n_q=n, num_q_heads=Hq, max_pages=pages,
                                         out_dtype=out.dtype)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None and need:  # freed here while the launch on `stream` may still run
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream)))
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        else:  # from that stream's own memory: it is used there, and freed before it ends
+            with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                   else torch.cuda.ExternalStream(int(stream))):
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     rc = _call_attn(cache._addr, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                     _stream_of(stream, q))
     if rc:
@@ -261,7 +269,7 @@ def _norm_row(t, name: str, shape, dtype):
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: gate, the weights and y must have one dtype, and residual and h_out "
                          f"one: got {t.dtype} beside {dtype}")
-    return t.data_ptr(), s[0], t.dtype
+    return _addr(t, name), s[0], t.dtype
 
 
 def _norm_weight(w, name: str, channels: Optional[int], dtype):
@@ -272,7 +280,7 @@ def _norm_weight(w, name: str, channels: Optional[int], dtype):
                          f"got {tuple(w.shape)}")
     if dtype is not None and w.dtype is not dtype:
         raise ValueError(f"{name}: gate, the weights and y must have one dtype, got {w.dtype} beside {dtype}")
-    return w.data_ptr(), w.dtype
+    return _addr(w, name), w.dtype
 
 
 def lin_state_block_norm(*, x, gate=None, gate_act: Optional[str] = None, w_post=None,

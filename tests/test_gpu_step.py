@@ -479,3 +479,27 @@ def test_norm_extreme_rows():
     x[1, 5] = float("inf")
     L.lin_state_block_norm(x=x, w_post=w, h_out=h)
     assert torch.equal(h[0], ref[0]) and torch.equal(h[2], ref[2]) and h[1].isnan().any()
+
+
+def test_binding_refuses_wrong_device_tensors():
+    c = L.KVCache(1, 4, 8, 2, 64)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new = torch.zeros((3, 2, 2, 64), dtype=BF, device="cuda")
+    table, pos = torch.zeros((3, 4), **i32), torch.zeros(3, **i32)
+    with pytest.raises(ValueError, match="pos: want a contiguous int32"):
+        L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table, pos=pos.long())
+    with pytest.raises(ValueError, match="n_tok: want a contiguous int32"):
+        L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table, pos=pos, n_tok=pos[:2])
+    with pytest.raises(ValueError, match="pos: want a CUDA tensor"):
+        L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table, pos=pos.cpu())
+    q = torch.zeros((3, 2, 8, 64), dtype=BF, device="cuda")
+    with pytest.raises(L.LinStateError, match="workspace"):
+        L.lin_state_attn_decode(c, layer=0, q=q, out=q.clone(), page_table=table, kv_len=pos,
+                                workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(L.LinStateError, match="multiple"):
+        L.lin_state_attn_decode(c, layer=0, q=q[:, :, :3], out=q[:, :, :3].contiguous(), page_table=table, kv_len=pos)
+    x = torch.zeros((3, 64), dtype=BF, device="cuda")
+    with pytest.raises(ValueError, match="one dtype"):
+        L.lin_state_block_norm(x=x, gate=x, gate_act="silu", w_post=torch.ones(64, device="cuda"), h_out=x)
+    with pytest.raises(ValueError, match="h_out: want"):
+        L.lin_state_block_norm(x=x, h_out=x[:, :32])

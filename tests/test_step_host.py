@@ -188,10 +188,10 @@ def test_binding_refuses_wrong_tensors():
         L.lin_state_kv_append(c, layer=0, k=new.float(), v=new, page_table=table, pos=pos)
     with pytest.raises(ValueError, match="same shape"):
         L.lin_state_kv_append(c, layer=0, k=new, v=new[:, :1], page_table=table, pos=pos)
-    with pytest.raises(ValueError, match="pos"):
-        L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table, pos=pos.long())
-    with pytest.raises(ValueError, match="page_table"):
+    with pytest.raises(ValueError, match="page_table: want int32"):
         L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table[:2], pos=pos)
+    with pytest.raises(ValueError, match="want a CUDA tensor"):
+        L.lin_state_kv_append(c, layer=0, k=new, v=new, page_table=table, pos=pos)
     q = torch.zeros((3, 2, 8, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="out"):
         L.lin_state_attn_decode(c, layer=0, q=q, out=q[:, :1], page_table=table, kv_len=pos)
@@ -199,12 +199,10 @@ def test_binding_refuses_wrong_tensors():
         L.lin_state_attn_decode(c, layer=0, q=q.transpose(2, 3).contiguous().transpose(2, 3), out=q,
                                 page_table=table, kv_len=pos)
     x = torch.zeros((3, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="one dtype"):
-        L.lin_state_block_norm(x=x, gate=x, gate_act="silu", w_post=torch.ones(64), h_out=x)
     with pytest.raises(ValueError, match="gate_act"):
         L.lin_state_block_norm(x=x, gate=x, gate_act="relu", h_out=x)
-    with pytest.raises(ValueError, match="h_out: want"):
-        L.lin_state_block_norm(x=x, h_out=x[:, :32])
+    with pytest.raises(ValueError, match="want a CUDA tensor"):
+        L.lin_state_block_norm(x=x, h_out=x)
 
 
 # ---- the oracle's own pins ---------------------------------------------------
