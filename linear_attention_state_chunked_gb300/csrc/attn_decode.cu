@@ -8,16 +8,20 @@ namespace attn {
 namespace {
 
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 16;  // most rows side by side in the grid
+constexpr int kJoinRows = 16;  // most rows of an item side by side in the grid
 
-// Block (c, y): rows y, y + gridDim.y, ... of the item that begins in range c
-// and goes on past it. Its parts, in token order: 2c + 1, then 2c' of the ranges
-// c' = c + 1, ... The warps take every eighth part and are joined in shared
-// memory, always in the same order.
-template <int D>
+// Block (c, y): rows of the item that begins in range c and goes on past it. Its
+// parts, in token order: 2c + 1, then 2c' of the ranges c' = c + 1, ... Each row is
+// joined by RW warps, which take every RW-th part and meet in shared memory,
+// always in the same order; a block has 8 / RW rows at a time.
+//
+// Bound by the latency of its loads (split, then sums, then values) and by the
+// launch of blocks that find no split: many items (few parts each) take one warp
+// per row, so eight rows to a block; few items (many parts) take a block per row.
+template <int D, int RW>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
-  constexpr int V = D / 32;
-  __shared__ float s_v[kJoinWarps][D], s_sum[kJoinWarps];
+  constexpr int V = D / 32, ROWS = kJoinWarps / RW;
+  __shared__ float s_v[RW > 1 ? RW : 1][RW > 1 ? D : 1], s_sum[RW];
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const longlong2 split = p.split[c];
@@ -28,7 +32,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   const int64_t head = item / p.row_blocks;
   const int hk = static_cast<int>(head % p.c.num_kv_heads);
   const int64_t r = head / p.c.num_kv_heads;
-  for (int row = blockIdx.y; row < p.block_rows; row += gridDim.y) {
+  for (int row = blockIdx.y * ROWS + warp / RW; row < p.block_rows; row += gridDim.y * ROWS) {
     const int q = rb * p.block_rows + row;
     if (q >= p.rows) return;
     auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * p.block_rows + row; };
@@ -46,7 +50,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
 #pragma unroll
     for (int x = 0; x < V; ++x) v[x] = 0.0f;
 #pragma unroll 4
-    for (int i = warp; i < parts; i += kJoinWarps) {
+    for (int i = warp % RW; i < parts; i += RW) {
       const int64_t at = index(i);
       const float2 ml = p.part_ml[at];
       const float* src = p.part + at * D + lane * V;
@@ -66,24 +70,47 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
 #pragma unroll
       for (int k = 0; k < V; ++k) v[k] = fmaf(f, x[k], v[k]);
     }
-#pragma unroll
-    for (int k = 0; k < V; ++k) s_v[warp][lane * V + k] = v[k];
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-    sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += s_sum[w];
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int j = query_of(p, q);
     const int64_t at = ((r * p.a.n_q + j) * p.a.num_q_heads + hk * p.group + q - j * p.group) * D;
-    for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
-      float x = 0.0f;
+    if constexpr (RW == 1) {
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int w = 0; w < kJoinWarps; ++w) x += s_v[w][d];
-      store_elem(p.a.out, at + d, p.a.out_dtype, x * f);
+      for (int k = 0; k < V; k += 2) {
+        const int64_t d = at + lane * V + k;
+        if (p.a.out_dtype == LIN_F32)
+          *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + d) = make_float2(v[k] * f, v[k + 1] * f);
+        else
+          *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + d) = __floats2bfloat162_rn(v[k] * f, v[k + 1] * f);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k) s_v[warp][lane * V + k] = v[k];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < RW; ++w) sum += s_sum[w];
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+        float x = 0.0f;
+#pragma unroll
+        for (int w = 0; w < RW; ++w) x += s_v[w][d];
+        store_elem(p.a.out, at + d, p.a.out_dtype, x * f);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
+}
+
+template <int D>
+cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int grid, int64_t items) {
+  const int rows = p.rows < p.block_rows ? p.rows : p.block_rows;
+  if (items * 4 >= grid) {
+    cfg.gridDim = dim3(grid, (rows + kJoinWarps - 1) / kJoinWarps);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p);
+  }
+  cfg.gridDim = dim3(grid, rows < kJoinRows ? rows : kJoinRows);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, kJoinWarps>, p);
 }
 
 // Which kernel a call takes, the rows of its items and its CTAs per SM.
@@ -183,14 +210,14 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, p.rows < attn::kJoinRows ? p.rows : attn::kJoinRows);
   cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return c.head_dim == 64    ? cudaLaunchKernelEx(&cfg, attn::join_kernel<64>, p)
-         : c.head_dim == 128 ? cudaLaunchKernelEx(&cfg, attn::join_kernel<128>, p)
-                             : cudaLaunchKernelEx(&cfg, attn::join_kernel<256>, p);
+  const int64_t items = int64_t(a.batch) * c.num_kv_heads * p.row_blocks;
+  return c.head_dim == 64    ? attn::launch_join<64>(cfg, p, grid, items)
+         : c.head_dim == 128 ? attn::launch_join<128>(cfg, p, grid, items)
+                             : attn::launch_join<256>(cfg, p, grid, items);
 }
 
 }  // namespace lin
