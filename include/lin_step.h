@@ -89,10 +89,16 @@ LIN_API int lin_state_kv_append(const lin_kv_cache_t* cache, const lin_kv_append
  * Precision: scores, the softmax and the sums over values are fp32. bf16
  * caches multiply on tensor cores with exact bf16 operands and the weights in
  * two bf16 parts (three for fp32 outputs); fp32 caches multiply with every
- * operand in two tf32 parts.
+ * operand in two tf32 parts and add the products of 16 tokens, and of 32
+ * channels of a score, with rounding. Visible infinities may give NaN.
+ * Results do not depend on timing: the same call gives the same bits.
+ * Any batch of lengths loads the SMs evenly: the lengths are read on the device,
+ * the batch's tokens are cut into equal ranges, and items that cross a border
+ * are joined by a second launch.
  * Workspace: lin_state_attn_workspace() bytes of device memory, 16-byte
- * aligned, not shared by calls that may overlap. It grows with the GPU, not
- * with the cache. */
+ * aligned, not shared by calls that may overlap. It grows with the GPU and
+ * with n_q * num_q_heads / num_kv_heads, not with the cache. Its contents
+ * before the call do not matter. Longest request: 2^31 - 65536 tokens. */
 typedef struct {
   int32_t layer, batch, n_q, num_q_heads;
   int32_t out_dtype;         /* lin_dtype_t */

@@ -1,32 +1,30 @@
-// Decode attention over a paged key-value cache: the main kernel (lin_step.h).
+// Decode attention over a paged key-value cache (lin_step.h): bf16 caches with up
+// to 16 rows per (request, kv head), and fp32 caches.
 //
 //   out[r][j][h] = sum_t p_t v_t / sum_t p_t,  p_t = 2^(s_t - m),
 //   s_t = scale log2(e) q.k_t over the tokens that query j sees,
 //
-// one pass over the cache with a running maximum m, sum and value sum per row.
+// one pass over the cache with a reference m, the sum and the value sum per row.
 // The rows of one (request, key-value head) are its n_q x G queries (G query
 // heads share the head's keys), so every key is read once for all of them.
 //
-// Bound by HBM: 2 head_dim elements per token and key-value head are read for
-// 4 head_dim flops a row, a few tens of flops per byte. The tensor work
-// is warp-level MMA on 16 rows: a tile of 16 rows is what a decode step has,
-// and each warp keeps its rows' whole softmax state in registers, with no
-// barrier between warps of a step.
+// Bound by HBM with one row tile in bf16: 2 head_dim elements per token and
+// key-value head are read for 4 head_dim flops a row. The tensor work is
+// warp-level MMA on 16 rows, which is what a decode step has, and each warp keeps
+// its rows' whole softmax state in registers. 256 requests of 1k-16k tokens, 8
+// query heads to a kv head of 128: 334 us, 0.98 of the measured copy bandwidth.
+// fp32 is bound by the tensor unit from two row tiles on: three tf32 products to
+// an fp32 one, 8 cycles each per scheduler (trees of 8 drafts, 24 rows: 60 us for
+// a floor of 20).
 //
-// Work split. A unit is 64 tokens of one item = (request, kv head, row block).
-// The units of the whole batch, laid end to end, are cut into one equal range
-// per CTA (lengths are read on the device), so a batch of ragged lengths and a
-// single long request load the SMs alike. An item inside one range is finished
-// there; one that crosses a border leaves (value sums, m, sum) of each piece in
-// the workspace and a second kernel joins them in range order, so results do
-// not depend on timing.
-//
-// Inside a CTA a group of RT warps (one per 16 rows) shares a ring of S slots of
-// SUB tokens' K and V, filled by 16-byte asynchronous copies of its own threads;
-// NW / RT groups take every KG-th slot of a piece and are joined in shared
-// memory at its end. Rows of a slot are swizzled (16-byte chunk c of row r at
-// c ^ (r % 8)), so every fragment load is free of bank conflicts. Tokens past
-// the length, or in a bad page, are filled with zeros and masked.
+// Inside a CTA a group of RT x DS warps (one per 16 rows, and per part of the
+// values) shares a ring of S slots of 16 tokens' K and V, filled by 16-byte
+// asynchronous copies of its own threads (one bulk copy per row was three times
+// slower: a warp issues them one by one). The KG groups take every KG-th slot of
+// a piece and are joined in shared memory at its end. Rows of a slot are swizzled
+// (16-byte chunk c of row r at c ^ (r % 8)), so every fragment load is free of
+// bank conflicts. Tokens past the length, or in a bad page, are filled with zeros
+// and masked.
 #pragma once
 
 #include "attn_common.cuh"
@@ -34,17 +32,20 @@
 namespace lin {
 namespace attn {
 
-// Warps of one CTA: KG groups x RT row tiles x DS parts of head_dim. DS 2 halves
-// a warp's value sums (it computes the scores twice) where rows of 256 channels
-// would otherwise leave one warp per scheduler.
+constexpr int kSub = 16;  // tokens of a ring slot
+
+// Warps of one CTA: KG groups x RT row tiles (bf16: 1) x DS parts of head_dim. DS
+// 2 halves a warp's value sums (it computes the scores twice) where rows of 256
+// channels would otherwise leave one warp per scheduler (heads of 256, 4 drafts:
+// 206 to 152 us). As many CTAs as leave room for two slots a group and registers
+// for the value sums.
 template <int D_, int DT_, int RT_>
 struct Cfg {
   static constexpr int D = D_, DT = DT_, RT = RT_;
   static constexpr bool BF = DT == LIN_BF16;
   static constexpr int ES = BF ? 2 : 4;
   static constexpr int ROWB = D * ES;                 // bytes of one key or value
-  static constexpr int SUB = 16;                      // tokens of a ring slot
-  static constexpr int SLOT = 2 * SUB * ROWB;         // their K and V
+  static constexpr int SLOT = 2 * kSub * ROWB;        // K and V of a slot's tokens
   static constexpr int QP = BF ? 1 : 2;               // planes of q: fp32 as two tf32 parts
   static constexpr int QBYTES = QP * 16 * RT * ROWB;
   static constexpr bool MANY = RT >= 2;
@@ -52,7 +53,7 @@ struct Cfg {
   static constexpr int DS = ROWB <= 256 ? 1 : ROWB == 512 ? 2 : RT == 4 ? 2 : 4;
   static constexpr int NW = ROWB <= 256 ? (MANY ? 8 : 4) : ROWB == 512 ? (MANY ? 16 : 8) : 8;
   // a warp keeps its queries' operands in registers where that costs no occupancy
-  static constexpr bool QREG = BF && (D == 64 || (D == 128 && !MANY));
+  static constexpr bool QREG = BF && D <= 128;
   static constexpr int KG = NW / (RT * DS);
   static constexpr int GT = RT * DS * 32;             // threads of a group
   static constexpr int BUDGET = (CTAS == 4 ? 55 : CTAS == 3 ? 73 : CTAS == 2 ? 110 : 222) * 1024;
@@ -123,7 +124,7 @@ __device__ __forceinline__ uint32_t chunk_from(uint32_t at, int c) {
 template <class C, int PT>
 __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p) {
   constexpr int D = C::D, RT = C::RT, DS = C::DS, KG = C::KG, S = C::S, NT = C::NW * 32, ROWB = C::ROWB;
-  constexpr int SUB = C::SUB, GT = C::GT, DW = D / DS;  // a warp sums DW channels of the values
+  constexpr int GT = C::GT, DW = D / DS;  // a warp sums DW channels of the values
   constexpr bool BF = C::BF;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_valid[KG][S];  // live tokens of each slot
@@ -154,10 +155,10 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
     const int32_t* table = a.page_table + r * a.page_table_stride;
 
-    // ---- slots: lane l of every warp looks up token l % SUB of the slot --------
-    const int subs = (key_end - key_begin + SUB - 1) / SUB;
+    // ---- slots: lane l of every warp looks up token l % 16 of the slot --------
+    const int subs = (key_end - key_begin + kSub - 1) / kSub;
     const int count = subs > kg ? (subs - kg + KG - 1) / KG : 0;  // this group's
-    int key = key_begin + kg * SUB + (lane & (SUB - 1));
+    int key = key_begin + kg * kSub + (lane & (kSub - 1));
     int in_page = 0, id = -1;
     auto look = [&]() {  // page id of the next slot's token
       const int page = page_of(p, key);
@@ -166,21 +167,21 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
     };
     auto fill = [&](int slot) {
       const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
-      if (key < key_end && !live && gtid == (lane & (SUB - 1))) report(a.status, LIN_ST_BAD_PAGE);
+      if (key < key_end && !live && gtid == (lane & (kSub - 1))) report(a.status, LIN_ST_BAD_PAGE);
       const int64_t off = live ? id * c.page_stride + in_page * c.token_stride : 0;
-      const uint32_t valid = __ballot_sync(~0u, live) & (SUB == 32 ? ~0u : (1u << (SUB & 31)) - 1u);
+      const uint32_t valid = __ballot_sync(~0u, live) & 0xffffu;
       if (gtid == 0) s_valid[kg][slot] = valid;
       constexpr int CPR = ROWB / 16;
       const uint32_t dst = ring + slot * C::SLOT;
 #pragma unroll
-      for (int i = 0; i < SUB * CPR / GT; ++i) {
+      for (int i = 0; i < kSub * CPR / GT; ++i) {
         const int x = i * GT + gtid, row = x / CPR, ch = x % CPR;
         const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
         const bool ok = (valid >> row) & 1u;
         cp16(dst + chunk_at<ROWB>(row, ch), kb + o, ok);
-        cp16(dst + SUB * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
+        cp16(dst + kSub * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
       }
-      key += KG * SUB;
+      key += KG * kSub;
       look();
     };
     look();
@@ -243,36 +244,29 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       group_sync<GT>(kg);  // slot i has landed; slot i - 1 is free
       if (i + S - 1 < count) fill(slot == 0 ? S - 1 : slot - 1);
       cp_commit();
-      const uint32_t ks = ring + slot * C::SLOT, vs = ks + SUB * ROWB;
-      constexpr int NT8 = SUB / 8;  // tiles of 8 tokens
-      float s[NT8][4], s2[2][4];
+      const uint32_t ks = ring + slot * C::SLOT, vs = ks + kSub * ROWB;
+      float s[2][4];  // two column tiles of 8 tokens
 #pragma unroll
-      for (int n = 0; n < NT8; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
       if constexpr (BF) {
-        // tokens 0-7 | 8-15 of 16 are two column tiles; with one such pair the
         // even and odd steps sum apart, for chains half as long
+        float s2[2][4];
         const uint32_t kat = ks + chunk_at<ROWB>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-        if constexpr (NT8 == 2)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s2[0][x] = s2[1][x] = 0.0f;
+        for (int x = 0; x < 4; ++x) s2[0][x] = s2[1][x] = 0.0f;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t q[4];
           if constexpr (!QREG) ldsm4(q, chunk_from(qat, 2 * k));
-#pragma unroll
-          for (int n = 0; n < NT8; n += 2) {
-            uint32_t b[4];
-            ldsm4(b, chunk_from(kat + n * 8 * ROWB, 2 * k));
-            const bool odd = NT8 == 2 && (k & 1);
-            mma_bf16(odd ? s2[0] : s[n], QREG ? qf[QREG ? k : 0] : q, b[0], b[1]);
-            mma_bf16(odd ? s2[1] : s[n + 1], QREG ? qf[QREG ? k : 0] : q, b[2], b[3]);
-          }
+          uint32_t b[4];
+          ldsm4(b, chunk_from(kat, 2 * k));
+          mma_bf16(k & 1 ? s2[0] : s[0], QREG ? qf[QREG ? k : 0] : q, b[0], b[1]);
+          mma_bf16(k & 1 ? s2[1] : s[1], QREG ? qf[QREG ? k : 0] : q, b[2], b[3]);
         }
-        if constexpr (NT8 == 2)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) s[0][x] += s2[0][x], s[1][x] += s2[1][x];
+        for (int x = 0; x < 4; ++x) s[0][x] += s2[0][x], s[1][x] += s2[1][x];
       } else {
         const uint32_t kat = ks + chunk_at<ROWB>(g, 0) + t4 * 4;
         // 32 channels to a chain of products, chains joined by rounded additions
@@ -308,9 +302,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       // which of the slot's tokens the two rows see; token n * 8 + 2 t4 + e is
       // bit 8 n + e of the shifted masks
       const uint32_t valid = s_valid[kg][slot];
-      const int sh = key_begin + (i * KG + kg) * SUB - base;
-      const bool drafts = sh + SUB > 0;
-      const bool masked = drafts || valid != (SUB == 32 ? ~0u : (1u << (SUB & 31)) - 1u);
+      const int sh = key_begin + (i * KG + kg) * kSub - base;
+      const bool drafts = sh + kSub > 0;
+      const bool masked = drafts || valid != 0xffffu;
       uint32_t vis0 = valid, vis1 = valid;
       if (masked) {
         if (drafts) {
@@ -321,7 +315,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         vis0 >>= 2 * t4;
         vis1 >>= 2 * t4;
 #pragma unroll
-        for (int n = 0; n < NT8; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (!((vis0 >> (8 * n + e)) & 1u)) s[n][e] = -INFINITY;
@@ -330,7 +324,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       }
       float mx0 = s[0][0], mx1 = s[0][2];
 #pragma unroll
-      for (int n = 0; n < NT8; ++n) {
+      for (int n = 0; n < 2; ++n) {
         mx0 = fmaxf(mx0, fmaxf(s[n][0], s[n][1]));
         mx1 = fmaxf(mx1, fmaxf(s[n][2], s[n][3]));
       }
@@ -358,7 +352,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         }
       }
 #pragma unroll
-      for (int n = 0; n < NT8; ++n)
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           s[n][e] = exp2_fast(fmaf(s[n][e], p.scale_log2, z0));
@@ -371,14 +365,14 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       bool wild = false;
       if (masked) {
 #pragma unroll
-        for (int n = 0; n < NT8; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {  // scale 0 makes NaN of a hidden score
             if (!((vis0 >> (8 * n + e)) & 1u)) s[n][e] = 0.0f;
             if (!((vis1 >> (8 * n + e)) & 1u)) s[n][2 + e] = 0.0f;
           }
         if (drafts && a.n_q > 1) {
-          for (int x = lane; x < SUB * ROWB / 16; x += 32) {
+          for (int x = lane; x < kSub * ROWB / 16; x += 32) {
             uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(vs + x * 16) : "memory");
@@ -392,7 +386,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         }
         if (wild) {
 #pragma unroll
-          for (int n = 0; n < NT8; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll 1
@@ -423,7 +417,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         }
       }
 #pragma unroll
-      for (int n = 0; n < NT8; ++n) {
+      for (int n = 0; n < 2; ++n) {
         l0 += s[n][0] + s[n][1];
         l1 += s[n][2] + s[n][3];
       }
@@ -432,33 +426,27 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       // fp32 outputs add a slot's sums by rounded additions.
       if constexpr (BF) {
         const uint32_t vat = vs + chunk_at<ROWB>(lane & 15, lane >> 4);
-        uint32_t pf[NT8 / 2][PT][4];
+        uint32_t pf[PT][4];
 #pragma unroll
-        for (int k = 0; k < NT8 / 2; ++k)
-#pragma unroll
-          for (int x = 0; x < PT; ++x) {
-            pf[k][x][0] = take_bf16(s[2 * k][0], s[2 * k][1]);
-            pf[k][x][1] = take_bf16(s[2 * k][2], s[2 * k][3]);
-            pf[k][x][2] = take_bf16(s[2 * k + 1][0], s[2 * k + 1][1]);
-            pf[k][x][3] = take_bf16(s[2 * k + 1][2], s[2 * k + 1][3]);
-          }
+        for (int x = 0; x < PT; ++x) {
+          pf[x][0] = take_bf16(s[0][0], s[0][1]);
+          pf[x][1] = take_bf16(s[0][2], s[0][3]);
+          pf[x][2] = take_bf16(s[1][0], s[1][1]);
+          pf[x][3] = take_bf16(s[1][2], s[1][3]);
+        }
 #pragma unroll
         for (int n = 0; n < DW / 16; ++n) {
           float f0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, f1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          uint32_t b[4];
+          ldsm4t(b, chunk_from(vat + ds * (DW * C::ES), 2 * n));
+          if (wild) {
 #pragma unroll
-          for (int k = 0; k < NT8 / 2; ++k) {
-            uint32_t b[4];
-            ldsm4t(b, DS == 1 ? chunk_from(vat + k * 16 * ROWB, 2 * n)
-                              : chunk_from(vat + k * 16 * ROWB + ds * (DW * C::ES), 2 * n));
-            if (wild) {
+            for (int x = 0; x < 4; ++x) b[x] = finite_bf16(b[x]);
+          }
 #pragma unroll
-              for (int x = 0; x < 4; ++x) b[x] = finite_bf16(b[x]);
-            }
-#pragma unroll
-            for (int x = PT - 1; x >= 0; --x) {
-              mma_bf16(PT == 3 ? f0 : o[2 * n], pf[k][x], b[0], b[1]);
-              mma_bf16(PT == 3 ? f1 : o[2 * n + 1], pf[k][x], b[2], b[3]);
-            }
+          for (int x = PT - 1; x >= 0; --x) {
+            mma_bf16(PT == 3 ? f0 : o[2 * n], pf[x], b[0], b[1]);
+            mma_bf16(PT == 3 ? f1 : o[2 * n + 1], pf[x], b[2], b[3]);
           }
           if constexpr (PT == 3) {
 #pragma unroll

@@ -4,7 +4,9 @@
 //
 // What bounds it is HBM, as for few rows (attn_kernel.cuh); but warp-level MMA
 // of 16 rows, one m16n8k16 in 8 cycles per scheduler, takes as long as the loads
-// at about 24 rows, and tcgen05 some twentieth of that. So its M = 128 need not
+// at about 24 rows (64 requests, 4 drafts of a group of 8: 81 us against 71 us
+// here; 8 drafts 132 against 86; heads of 256, 4 drafts 161 against 105), and
+// tcgen05 some twentieth of that. So its M = 128 need not
 // be filled with work: the RP (32, 64 or 128) rows are repeated 128 / RP times
 // along M, and copy c only ever looks at the c-th share of a tile's tokens:
 //   S  = Q K^T      [128 lanes][TK tokens], every lane against every token;
@@ -14,6 +16,11 @@
 // A thread owns a lane: its row's maximum, sum and weights need no exchange
 // between threads, and the four softmax warps share the tile's tokens evenly.
 // The copies are joined as the pieces of a split are.
+//
+// Per 64 tokens and SM: 0.80 us for 32 rows of 128 (floor 0.735), 1.40 for 32 rows
+// of 256 (1.47); 1.0 and 1.5 us for 64 and 128 rows of 128, where a thread's 32 and
+// 64 weights of a tile take longer than its loads. An item's start and end take 5-6
+// us, which the split counts (Plan::item_cost).
 //
 // Roles: warps 0-3 softmax (thread = TMEM lane), 4-7 load, 8 issues Q K^T, 9
 // issues P V (one warp for both would make each wait for the other's operands).

@@ -9,6 +9,8 @@
 // a step. One warp moves one token: it owns whole rows, so tokens may land in
 // any order of pages, and it looks the page up once for all heads of K and V.
 // The rows' loads are issued before the page lookup, whose latency they hide.
+// 8 prompts of 2k-4k tokens, 8 heads of 128 in bf16: 33.5 us, 0.89 of the measured
+// copy bandwidth; one token of each of 256 requests: 3.0 us, the launch.
 
 #include "common.cuh"
 #include "step_internal.h"
