@@ -35,9 +35,9 @@ namespace attn {
 constexpr int kSub = 16;  // tokens of a ring slot
 
 // Warps of one CTA: KG groups x RT row tiles (bf16: 1) x DS parts of head_dim. DS
-// 2 halves a warp's value sums (it computes the scores twice) where rows of 256
-// channels would otherwise leave one warp per scheduler (heads of 256, 4 drafts:
-// 206 to 152 us). As many CTAs as leave room for two slots a group and registers
+// warps share a row tile where rows of 512 bytes and more would otherwise leave
+// one warp per scheduler: each makes its channels' part of the scores, which are
+// added in shared memory, and its channels' value sums. As many CTAs as leave room for two slots a group and registers
 // for the value sums.
 template <int D_, int DT_, int RT_>
 struct Cfg {
@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr bool QREG = BF && D <= 128;
   static constexpr int KG = NW / (RT * DS);
   static constexpr int GT = RT * DS * 32;             // threads of a group
-  static constexpr int BUDGET = (CTAS == 4 ? 55 : CTAS == 3 ? 73 : CTAS == 2 ? 110 : 222) * 1024;
+  static constexpr int BUDGET = (CTAS == 4 ? 55 : CTAS == 3 ? 73 : CTAS == 2 ? 110 : 216) * 1024;
   static constexpr int SLOTS = (BUDGET - QBYTES) / SLOT / KG;
   static constexpr int S = SLOTS < 12 ? SLOTS : 12;
   static constexpr int RING = KG * S * SLOT;
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
   constexpr bool BF = C::BF;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint32_t s_valid[KG][S];  // live tokens of each slot
+  __shared__ float4 s_score[DS > 1 ? C::NW : 1][2][DS > 1 ? 32 : 1];  // a warp's share of the scores
   __shared__ uint32_t s_see[32];       // drafts that each query sees
   __shared__ int64_t s_scan[C::NW], s_first[2];
   __shared__ int s_bad;
@@ -246,6 +247,7 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       cp_commit();
       const uint32_t ks = ring + slot * C::SLOT, vs = ks + kSub * ROWB;
       float s[2][4];  // two column tiles of 8 tokens
+      const uint32_t dsb = DS > 1 ? ds * (DW * C::ES) : 0;  // this warp's channels
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -257,11 +259,11 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s2[0][x] = s2[1][x] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+        for (int k = 0; k < DW / 16; ++k) {
           uint32_t q[4];
-          if constexpr (!QREG) ldsm4(q, chunk_from(qat, 2 * k));
+          if constexpr (!QREG) ldsm4(q, chunk_from(qat + dsb, 2 * k));
           uint32_t b[4];
-          ldsm4(b, chunk_from(kat, 2 * k));
+          ldsm4(b, chunk_from(kat + dsb, 2 * k));
           mma_bf16(k & 1 ? s2[0] : s[0], QREG ? qf[QREG ? k : 0] : q, b[0], b[1]);
           mma_bf16(k & 1 ? s2[1] : s[1], QREG ? qf[QREG ? k : 0] : q, b[2], b[3]);
         }
@@ -270,14 +272,14 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
       } else {
         const uint32_t kat = ks + chunk_at<ROWB>(g, 0) + t4 * 4;
         // 32 channels to a chain of products, chains joined by rounded additions
-#pragma unroll(D == 64 ? 2 : 1)
-        for (int k0 = 0; k0 < D / 8; k0 += 4) {
+#pragma unroll
+        for (int k0 = 0; k0 < DW / 8; k0 += 4) {
           float c0[2][4], c1[2][4];
 #pragma unroll
           for (int x = 0; x < 4; ++x) c0[0][x] = c0[1][x] = c1[0][x] = c1[1][x] = 0.0f;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const uint32_t ko = (k0 >> 2) * 128;  // 4 steps are one turn of the swizzle
+            const uint32_t ko = (k0 >> 2) * 128 + dsb;  // 4 steps are one turn of the swizzle
             uint32_t qh[4], ql[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -297,6 +299,23 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x) s[0][x] += c0[0][x] + c1[0][x], s[1][x] += c0[1][x] + c1[1][x];
+        }
+      }
+      if constexpr (DS > 1) {
+        // each of the DS warps has the products of its own channels: add them up,
+        // in one order, so that all go on with the same scores
+        s_score[warp][0][lane] = make_float4(s[0][0], s[0][1], s[0][2], s[0][3]);
+        s_score[warp][1][lane] = make_float4(s[1][0], s[1][1], s[1][2], s[1][3]);
+        group_sync<GT>(kg);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          float4 sum = s_score[warp - ds][n][lane];
+#pragma unroll
+          for (int x = 1; x < DS; ++x) {
+            const float4 y = s_score[warp - ds + x][n][lane];
+            sum.x += y.x, sum.y += y.y, sum.z += y.z, sum.w += y.w;
+          }
+          s[n][0] = sum.x, s[n][1] = sum.y, s[n][2] = sum.z, s[n][3] = sum.w;
         }
       }
       // which of the slot's tokens the two rows see; token n * 8 + 2 t4 + e is
