@@ -32,6 +32,7 @@ struct Plan {
   int block_rows;     // rows of an item
   int row_blocks;     // items of one (request, kv head)
   int item_cost;      // of an item besides its tokens, in units
+  int whole;          // items are short and stay whole: every border moves to an item's start
   float scale_log2;   // |scale| log2(e); q is negated where scale < 0
   uint32_t negate;
   float slack;        // kSlack in units of q.k
@@ -90,7 +91,7 @@ struct Walk {
 // The piece's end: the first of the item's units past it.
 __device__ __forceinline__ int walk_until(const Plan& p, const Walk& w) {
   const int64_t upto = w.end - w.base - p.item_cost;
-  return static_cast<int>(upto >= w.u ? w.u : upto > 0 ? upto : 0);
+  return static_cast<int>(upto >= w.u ? w.u : upto > 0 && !p.whole ? upto : 0);
 }
 
 // The CTA's range, from a scan over the requests' lengths by all NT threads.
@@ -152,7 +153,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_s
   w.u = units_of(w.len, w.most);
   w.it = static_cast<int>((cur - s_first[1]) / (w.u + p.item_cost));
   w.base = s_first[1] + int64_t(w.it) * (w.u + p.item_cost);
-  w.t0 = max(0, static_cast<int>(cur - w.base) - p.item_cost);
+  w.t0 = p.whole ? 0 : max(0, static_cast<int>(cur - w.base) - p.item_cost);
   if (walk_until(p, w) > w.t0) return true;
   if (tid == 0) p.split[blockIdx.x].x = -1;
   return false;
