@@ -136,12 +136,17 @@ int ctas_of(bool bf16, int rt) {
 }
 
 // bf16 caches: up to 16 rows per (request, kv head) on warp-level MMA, more on
-// tcgen05 in blocks of 32, 64 or 128. fp32 caches: warp-level MMA in blocks of 16,
+// tcgen05 in blocks of 32, 64 or 128; but 17 to 32 rows of requests of up to 256
+// tokens as two blocks of 16, for an item's start and end take longer there than
+// reading it twice (4 drafts of a group of 8: 1 request
+// of 64 tokens 8.6 to 6.3 us, 256 requests of up to 256 tokens 41 to 38 us). fp32 caches: warp-level MMA in blocks of 16,
 // 32 or 64.
-Shape shape_of(const lin_kv_cache_t& c, int rows) {
+Shape shape_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads);
+  const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
   const bool b = c.dtype == LIN_BF16;
-  if (b && rows > 16) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
-  const int rt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  if (b && rows > 16 && (rows > 32 || units > 4)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
+  const int rt = rows <= 16 || b ? 1 : rows <= 32 ? 2 : 4;
   return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), b ? 3 : 2, b ? 4 : 2};
 }
 
@@ -171,7 +176,7 @@ void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
 }  // namespace attn
 
 size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
-  const attn::Shape f = attn::shape_of(c, a.n_q * (a.num_q_heads / c.num_kv_heads));
+  const attn::Shape f = attn::shape_of(c, a);
   const size_t grid = attn::grid_of(c, a, f);
   return 2 * grid * f.block_rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
 }
@@ -182,7 +187,7 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.a = a;
   p.group = a.num_q_heads / c.num_kv_heads;
   p.rows = a.n_q * p.group;
-  const attn::Shape f = attn::shape_of(c, p.rows);
+  const attn::Shape f = attn::shape_of(c, a);
   const int grid = attn::grid_of(c, a, f);
   p.block_rows = f.block_rows;
   p.item_cost = f.item_cost;

@@ -126,6 +126,52 @@ def test_attn_chain_of_drafts(n, dtype, D):
     assert not out[0].any() and not out[1, :n - 1].any()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(17, 1), (8, 3), (4, 8), (3, 11), (8, 8), (13, 5), (32, 4), (3, 43)])
+@pytest.mark.parametrize("out_dtype,tree", [(BF, False), (F32, True)])
+def test_attn_rows_and_tiles(D, n, G, out_dtype, tree):
+    """17 to 129 rows per key-value head over lengths around the tiles' ends,
+    from none to some that are split, in one batch."""
+    lens = [0, 1, n, 62 + n, 64, 127, 128, 129, 900, 1300, -1, 2600]
+    rng = np.random.default_rng(n * G)
+    parent = [[int(rng.integers(max(-1, j - 4), j)) if j else -1 for j in range(n)] for _ in lens] if tree else None
+    cache, table, gen = make_cache(lens, 20, 1, D, BF, seed=n + G)
+    check_attn(cache, table, queries(len(lens), n, G, 1, D, BF, gen), lens, out_dtype, parent=parent)
+
+
+@pytest.mark.parametrize("G", [2, 8, 16, 32])
+def test_attn_hidden_drafts_of_many_rows(G):
+    """As below, over a longer cache and up to 128 rows, with the bad drafts on
+    both sides of a tile's border."""
+    lens, n = [258, 700], 4
+    parent = [[-1, -1, 0, 1]] * 2
+    cache, table, gen = make_cache(lens, 16, 1, 128, BF, seed=G)
+    q = queries(2, n, G, 1, 128, BF, gen)
+    before = check_attn(cache, table, q, lens, BF, parent=parent).clone()
+    for r, t in ((0, 255), (0, 257), (1, 697), (1, 699)):  # drafts 1 and 3
+        at = O.locate(table[r], t, 16, cache.num_pages)
+        cache.k[0, at[0], at[1]] = float("nan")
+        cache.v[0, at[0], at[1], :, ::2] = float("nan")
+        cache.v[0, at[0], at[1], :, 1::2] = float("-inf")
+    out = torch.zeros_like(before)
+    L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table.cuda(),
+                            kv_len=torch.tensor(lens, dtype=torch.int32).cuda(),
+                            parent=torch.tensor(parent, dtype=torch.int32).cuda())
+    for j in (0, 2):
+        assert torch.equal(out[:, j], before[:, j])
+    for j in (1, 3):
+        assert out[:, j].isnan().all()
+
+
+def test_attn_repeats_bit_for_bit_with_many_rows():
+    lens = [4000, 77, 1500]
+    cache, table, gen = make_cache(lens, 16, 2, 128, BF, seed=18)
+    q = queries(3, 4, 16, 2, 128, BF, gen)
+    first = check_attn(cache, table, q, lens, BF)
+    for _ in range(3):
+        assert torch.equal(check_attn(cache, table, q, lens, BF), first)
+
+
 @pytest.mark.parametrize("n", [2, 8, 32])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_draft_trees(n, dtype):
