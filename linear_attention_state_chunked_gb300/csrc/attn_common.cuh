@@ -29,6 +29,7 @@ struct Plan {
   lin_attn_args_t a;
   int group;          // query heads per key-value head
   int rows;           // n_q * group
+  int grid;           // CTAs of the main kernel
   int block_rows;     // rows of an item
   int row_blocks;     // items of one (request, kv head)
   int item_cost;      // of an item besides its tokens, in units
@@ -77,6 +78,11 @@ __device__ __forceinline__ int units_of(int len, int64_t most) {
   return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
 }
 
+// The longest request allowed: token indices stay clear of the 32-bit end.
+__device__ __forceinline__ int64_t longest(const Plan& p) {
+  return min(int64_t(p.a.max_pages) * p.c.page_size, int64_t(INT32_MAX - 65536));
+}
+
 // Where a CTA is in its range.
 struct Walk {
   int64_t base, end, total, ranges;  // where the item and the range lie among all units
@@ -100,8 +106,7 @@ template <int NT>
 __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_scan)[NT / 32], int64_t (&s_first)[2]) {
   const lin_attn_args_t& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // token indices stay clear of the 32-bit end
-  w.most = min(int64_t(a.max_pages) * p.c.page_size, int64_t(INT32_MAX - 65536));
+  w.most = longest(p);
   w.per_req = p.c.num_kv_heads * p.row_blocks;
   w.split = make_longlong2(-1, 0);
   const int span = (a.batch + NT - 1) / NT;

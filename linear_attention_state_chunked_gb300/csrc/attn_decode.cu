@@ -7,98 +7,204 @@ namespace lin {
 namespace attn {
 namespace {
 
-constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 16;  // most rows of an item side by side in the grid
+constexpr int kJoinWarps = 8, kRowWarps = 16;
+constexpr int kJoinRows = 16;    // most rows of an item side by side in the grid
+constexpr int kMaxRanges = 1024;
 
-// Block (c, y): rows of the item that begins in range c and goes on past it. Its
-// parts, in token order: 2c + 1, then 2c' of the ranges c' = c + 1, ... Each row is
-// joined by RW warps, which take every RW-th part and meet in shared memory,
-// always in the same order; a block has 8 / RW rows at a time.
+// The item that begins in range c and goes on past it has the parts, in token
+// order, 2c + 1 and then 2c' of the ranges c' = c + 1, ... They are joined in that
+// order (RW warps of a row each take every RW-th), so the result does not depend
+// on timing.
 //
-// Bound by the latency of its loads (split, then sums, then values) and by the
-// launch of blocks that find no split: many items (few parts each) take one warp
-// per row, so eight rows to a block; few items (many parts) take a block per row.
-template <int D, int RW>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
-  constexpr int V = D / 32, ROWS = kJoinWarps / RW;
-  __shared__ float s_v[RW > 1 ? RW : 1][RW > 1 ? D : 1], s_sum[RW];
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Bound by the latency of dependent loads (split, sums, values). Many items, few
+// parts each: a block for every range, a warp per row, and most find no split. Few
+// items, many parts: a block for every item's row, which works out from the lengths
+// (while the main kernel runs) which ranges hold it, loads all sums at once and
+// the values by 16 warps (one request of 60,000 tokens, one kv head, 304 parts:
+// 24 us in all with a block for every range's row, 17 so).
+struct Split {
+  int parts, hk, rb;
+  int64_t r;
+};
+__device__ __forceinline__ bool split_of(const Plan& p, int c, Split& s) {
   const longlong2 split = p.split[c];
-  const int64_t item = split.x;
-  if (item < 0) return;
-  const int parts = static_cast<int>(split.y);
-  const int rb = static_cast<int>(item % p.row_blocks);
-  const int64_t head = item / p.row_blocks;
-  const int hk = static_cast<int>(head % p.c.num_kv_heads);
-  const int64_t r = head / p.c.num_kv_heads;
-  for (int row = blockIdx.y * ROWS + warp / RW; row < p.block_rows; row += gridDim.y * ROWS) {
-    const int q = rb * p.block_rows + row;
+  if (split.x < 0) return false;
+  const int64_t head = split.x / p.row_blocks;
+  s.rb = static_cast<int>(split.x - head * p.row_blocks);
+  s.r = head / p.c.num_kv_heads;
+  s.hk = static_cast<int>(head - s.r * p.c.num_kv_heads);
+  s.parts = static_cast<int>(split.y);
+  return true;
+}
+// Index of part i's row, and of a row's first output.
+__device__ __forceinline__ int64_t part_row(const Plan& p, int c, int i, int row) {
+  return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * p.block_rows + row;
+}
+template <int D>
+__device__ __forceinline__ int64_t out_row(const Plan& p, const Split& s, int q) {
+  const int j = query_of(p, q);
+  return ((s.r * p.a.n_q + j) * p.a.num_q_heads + s.hk * p.group + q - j * p.group) * D;
+}
+// a part's share of the joined sums (0 where it saw nothing; a NaN sum goes on)
+__device__ __forceinline__ float share_of(float2 ml, float top) {
+  return ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
+}
+template <int V>
+__device__ __forceinline__ void load_values(const float* src, float (&x)[V]) {
+  if constexpr (V == 2) {
+    const float2 y = *reinterpret_cast<const float2*>(src);
+    x[0] = y.x, x[1] = y.y;
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(src + k);
+      x[k] = y.x, x[k + 1] = y.y, x[k + 2] = y.z, x[k + 3] = y.w;
+    }
+  }
+}
+
+// A warp per row.
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
+  constexpr int V = D / 32;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Split s;
+  if (!split_of(p, c, s)) return;
+  const int q = s.rb * p.block_rows + row;
+  if (row >= p.block_rows || q >= p.rows) return;
+  float top = -INFINITY;
+  bool out = false;
+  for (int i = lane; i < s.parts; i += 32) {
+    const float2 ml = p.part_ml[part_row(p, c, i, row)];
+    top = fmaxf(top, ml.x);
+    out |= ml.y == -1.0f;
+  }
+  if (__any_sync(~0u, out)) return;  // a request left out
+#pragma unroll
+  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+  float sum = 0.0f, v[V];
+#pragma unroll
+  for (int x = 0; x < V; ++x) v[x] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < s.parts; ++i) {
+    const int64_t at = part_row(p, c, i, row);
+    const float2 ml = p.part_ml[at];
+    float x[V];
+    load_values<V>(p.part + at * D + lane * V, x);
+    const float f = share_of(ml, top);
+    sum = fmaf(f, ml.y, sum);
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = fmaf(f, x[k], v[k]);
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = out_row<D>(p, s, q) + lane * V;
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    if (p.a.out_dtype == LIN_F32)
+      *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at + k) = make_float2(v[k] * f, v[k + 1] * f);
+    else
+      *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + at + k) =
+          __floats2bfloat162_rn(v[k] * f, v[k + 1] * f);
+  }
+}
+
+// A block per row of an item: block (item, y).
+template <int D>
+__global__ void __launch_bounds__(kRowWarps * 32) join_row_kernel(const Plan p) {
+  constexpr int V = D / 32, NT = kRowWarps * 32;
+  __shared__ float s_f[kMaxRanges], s_v[kRowWarps][D], s_top[kRowWarps], s_sum[kRowWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per_req = p.c.num_kv_heads * p.row_blocks, it = blockIdx.x % per_req;
+  Split s;
+  s.r = blockIdx.x / per_req;
+  s.hk = head_of(p, it);
+  s.rb = it - s.hk * p.row_blocks;
+  // where the item lies among all units, as in walk_begin (every warp by itself)
+  const int64_t most = longest(p);
+  int64_t before = 0, total = 0;
+  for (int r = lane; r < p.a.batch; r += 32) {
+    const int u = units_of(p.a.kv_len[r], most);
+    const int64_t n = u > 0 ? int64_t(u + p.item_cost) * per_req : 0;
+    total += n;
+    if (r < s.r) before += n;
+  }
+#pragma unroll
+  for (int w = 16; w; w >>= 1) {
+    before += __shfl_xor_sync(~0u, before, w);
+    total += __shfl_xor_sync(~0u, total, w);
+  }
+  const int u = units_of(p.a.kv_len[s.r], most);
+  if (u == 0) return;
+  const int64_t ranges = total < p.grid ? total : p.grid, base = before + int64_t(it) * (u + p.item_cost);
+  auto range_of = [&](int64_t unit) { return static_cast<int>(((unit + 1) * ranges - 1) / total); };
+  // borders among the first item_cost units have moved to the item's start
+  const int c = range_of(base + p.item_cost);
+  s.parts = range_of(base + u + p.item_cost - 1) - c + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (s.parts == 1) return;
+  for (int row = blockIdx.y; row < p.block_rows; row += gridDim.y) {
+    const int q = s.rb * p.block_rows + row;
     if (q >= p.rows) return;
-    auto index = [&](int i) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * p.block_rows + row; };
+    constexpr int MOST = kMaxRanges / NT;
+    float2 ml[MOST];
     float top = -INFINITY;
     bool out = false;
-    for (int i = lane; i < parts; i += 32) {
-      const float2 ml = p.part_ml[index(i)];
-      top = fmaxf(top, ml.x);
-      out |= ml.y == -1.0f;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      const int i = tid + k * NT;
+      ml[k] = i < s.parts ? p.part_ml[part_row(p, c, i, row)] : make_float2(-INFINITY, 0.0f);
     }
-    if (__any_sync(~0u, out)) return;  // a request left out
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      top = fmaxf(top, ml[k].x);
+      out |= ml[k].y == -1.0f;
+    }
 #pragma unroll
     for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-    float sum = 0.0f, v[V];
+    if (lane == 0) s_top[warp] = top;
+    if (__syncthreads_or(out)) return;  // a request left out
+#pragma unroll
+    for (int w = 0; w < kRowWarps; ++w) top = fmaxf(top, s_top[w]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < MOST; ++k) {
+      const int i = tid + k * NT;
+      const float f = share_of(ml[k], top);
+      if (i < s.parts) s_f[i] = f;
+      sum = fmaf(f, ml[k].y, sum);
+    }
+#pragma unroll
+    for (int w = 16; w; w >>= 1) sum += __shfl_xor_sync(~0u, sum, w);
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    float v[V];
 #pragma unroll
     for (int x = 0; x < V; ++x) v[x] = 0.0f;
-#pragma unroll 4
-    for (int i = warp % RW; i < parts; i += RW) {
-      const int64_t at = index(i);
-      const float2 ml = p.part_ml[at];
-      const float* src = p.part + at * D + lane * V;
+#pragma unroll(D <= 128 ? 10 : 8)
+    for (int i = warp; i < s.parts; i += kRowWarps) {
       float x[V];
-      if constexpr (V == 2) {
-        const float2 y = *reinterpret_cast<const float2*>(src);
-        x[0] = y.x, x[1] = y.y;
-      } else {
-#pragma unroll
-        for (int k = 0; k < V; k += 4) {
-          const float4 y = *reinterpret_cast<const float4*>(src + k);
-          x[k] = y.x, x[k + 1] = y.y, x[k + 2] = y.z, x[k + 3] = y.w;
-        }
-      }
-      const float f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : exp2_fast(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
+      load_values<V>(p.part + part_row(p, c, i, row) * D + lane * V, x);
+      const float f = s_f[i];
 #pragma unroll
       for (int k = 0; k < V; ++k) v[k] = fmaf(f, x[k], v[k]);
     }
-    const int j = query_of(p, q);
-    const int64_t at = ((r * p.a.n_q + j) * p.a.num_q_heads + hk * p.group + q - j * p.group) * D;
-    if constexpr (RW == 1) {
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
-      for (int k = 0; k < V; k += 2) {
-        const int64_t d = at + lane * V + k;
-        if (p.a.out_dtype == LIN_F32)
-          *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + d) = make_float2(v[k] * f, v[k + 1] * f);
-        else
-          *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + d) = __floats2bfloat162_rn(v[k] * f, v[k + 1] * f);
-      }
-    } else {
+    for (int k = 0; k < V; ++k) s_v[warp][lane * V + k] = v[k];
+    __syncthreads();
+    sum = 0.0f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) s_v[warp][lane * V + k] = v[k];
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();
-      sum = 0.0f;
+    for (int w = 0; w < kRowWarps; ++w) sum += s_sum[w];
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int64_t at = out_row<D>(p, s, q);
+    for (int d = tid; d < D; d += NT) {
+      float x = 0.0f;
 #pragma unroll
-      for (int w = 0; w < RW; ++w) sum += s_sum[w];
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-      for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < RW; ++w) x += s_v[w][d];
-        store_elem(p.a.out, at + d, p.a.out_dtype, x * f);
-      }
-      __syncthreads();
+      for (int w = 0; w < kRowWarps; ++w) x += s_v[w][d];
+      store_elem(p.a.out, at + d, p.a.out_dtype, x * f);
     }
+    __syncthreads();
   }
 }
 
@@ -107,10 +213,12 @@ cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int grid, int64_
   const int rows = p.rows < p.block_rows ? p.rows : p.block_rows;
   if (items * 4 >= grid) {
     cfg.gridDim = dim3(grid, (rows + kJoinWarps - 1) / kJoinWarps);
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
   }
-  cfg.gridDim = dim3(grid, rows < kJoinRows ? rows : kJoinRows);
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, kJoinWarps>, p);
+  cfg.gridDim = dim3(static_cast<unsigned>(items), rows < kJoinRows ? rows : kJoinRows);
+  cfg.blockDim = dim3(kRowWarps * 32);
+  return cudaLaunchKernelEx(&cfg, join_row_kernel<D>, p);
 }
 
 // Which kernel a call takes, the rows of its items and its CTAs per SM.
@@ -161,7 +269,8 @@ int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a, const Shape& f) {
   const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
   const int64_t items = int64_t(a.batch) * c.num_kv_heads * blocks;
   const int64_t most = units > 1 && items < INT32_MAX ? items * units : items;
-  return static_cast<int>(most < int64_t(sms) * f.ctas && most > 0 ? most : int64_t(sms) * f.ctas);
+  const int64_t full = int64_t(sms) * f.ctas < kMaxRanges ? int64_t(sms) * f.ctas : kMaxRanges;
+  return static_cast<int>(most < full && most > 0 ? most : full);
 }
 
 // Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
@@ -189,6 +298,7 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.rows = a.n_q * p.group;
   const attn::Shape f = attn::shape_of(c, a);
   const int grid = attn::grid_of(c, a, f);
+  p.grid = grid;
   p.block_rows = f.block_rows;
   p.item_cost = f.item_cost;
   p.whole = int64_t(a.max_pages) * c.page_size <= int64_t(f.whole_units) * attn::kUnit;
@@ -221,7 +331,6 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(attn::kJoinWarps * 32);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
