@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) join_row_kernel(const Plan p) 
 template <int D>
 cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int grid, int64_t items) {
   const int rows = p.rows < p.block_rows ? p.rows : p.block_rows;
-  if (items * 4 >= grid) {
+  if (items * 8 > grid) {  // fewer than 8 parts to an item
     cfg.gridDim = dim3(grid, (rows + kJoinWarps - 1) / kJoinWarps);
     cfg.blockDim = dim3(kJoinWarps * 32);
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
