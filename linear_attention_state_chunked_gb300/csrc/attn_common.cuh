@@ -112,6 +112,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, int64_t (&s_s
   const int span = (a.batch + NT - 1) / NT;
   const int r0 = min(a.batch, tid * span), r1 = min(a.batch, r0 + span);
   int64_t mine = 0;
+#pragma unroll 4
   for (int r = r0; r < r1; ++r) {
     const int len = a.kv_len[r];
     if (len > w.most && blockIdx.x == 0) report(a.status, LIN_ST_BAD_SEQLEN);
