@@ -63,6 +63,11 @@ __device__ __forceinline__ void load_values(const float* src, float (&x)[V]) {
   }
 }
 
+// The range that holds this unit.
+__device__ __forceinline__ int range_of(int64_t unit, int64_t ranges, int64_t total) {
+  return static_cast<int>(((unit + 1) * ranges - 1) / total);
+}
+
 // A warp per row.
 template <int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
@@ -136,12 +141,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) join_row_kernel(const Plan p) 
     total += __shfl_xor_sync(~0u, total, w);
   }
   const int u = units_of(p.a.kv_len[s.r], most);
-  if (u == 0) return;
-  const int64_t ranges = total < p.grid ? total : p.grid, base = before + int64_t(it) * (u + p.item_cost);
-  auto range_of = [&](int64_t unit) { return static_cast<int>(((unit + 1) * ranges - 1) / total); };
-  // borders among the first item_cost units have moved to the item's start
-  const int c = range_of(base + p.item_cost);
-  s.parts = range_of(base + u + p.item_cost - 1) - c + 1;
+  int c = 0;
+  s.parts = 1;
+  if (u > 0) {
+    const int64_t ranges = total < p.grid ? total : p.grid, base = before + int64_t(it) * (u + p.item_cost);
+    // borders among the first item_cost units have moved to the item's start
+    c = range_of(base + p.item_cost, ranges, total);
+    s.parts = range_of(base + u + p.item_cost - 1, ranges, total) - c + 1;
+  }
+  // Every block waits, those of a request without units too: the stream's next
+  // launch is ordered behind this grid alone, which therefore must not end
+  // before the main kernel, the last reader of the lengths and writer of `split`.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (s.parts == 1) return;
   for (int row = blockIdx.y; row < p.block_rows; row += gridDim.y) {
