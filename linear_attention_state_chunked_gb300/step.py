@@ -93,12 +93,13 @@ _call_norm = _entry("lin_state_block_norm", ctypes.c_char_p, _vp)
 # the current stream's handle without the object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = torch.cuda.current_device
 
 
-def _stream_of(stream, t: torch.Tensor):
-    """The given stream's handle, or that of the current stream of t's device."""
+def _stream_of(stream, device: int):
+    """The given stream's handle, or that of the device's current stream."""
     if stream is None:
-        return _raw_stream(t.get_device())
+        return _raw_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -122,6 +123,8 @@ class KVCache:
                                  f"got {tuple(t.shape)} of {t.dtype}, strides {t.stride()}")
         if k.stride() != v.stride():
             raise ValueError(f"cache: k and v must have the same strides, got {k.stride()} and {v.stride()}")
+        if k.device != v.device:
+            raise ValueError(f"cache: k and v must lie on one device, got {k.device} and {v.device}")
         self._k, self._v, self.dtype = k, v, dtype
         self.num_layers, self.num_pages, self.page_size = num_layers, num_pages, page_size
         self.num_kv_heads, self.head_dim = num_kv_heads, head_dim
@@ -156,19 +159,39 @@ def _raise(rc: int, where: str):
     raise LinStateError(rc, where)
 
 
-def _addr(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
+def _launch_device(t: torch.Tensor, name: str) -> int:
+    """The GPU of t, on which the call's other tensors have to lie too. Kernels
+    are launched on the current device, which it therefore has to be."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name}: want a CUDA tensor, got one on {t.device}")
+    if device != _current_device():
+        raise ValueError(f"{name}: lies on cuda:{device}, which is not the current device (cuda:{_current_device()})")
+    return device
+
+
+def _addr(t: torch.Tensor, name: str, device: int) -> int:
+    if t.get_device() != device:
+        raise ValueError(f"{name}: want a CUDA tensor on cuda:{device}, got one on {t.device}")
     return t.data_ptr()
 
 
-def _ptr32(t: Optional[torch.Tensor], name: str, shape) -> int:
+def _ptr32(t: Optional[torch.Tensor], name: str, shape, device: int) -> int:
     """Address of a contiguous int32 tensor of this shape, or 0 for None."""
     if t is None:
         return 0
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: want a contiguous int32 tensor {shape}, got {tuple(t.shape)} of {t.dtype}")
-    return _addr(t, name)
+    return _addr(t, name, device)
+
+
+def _status(t: Optional[torch.Tensor], device: int) -> int:
+    """Address of the status word, or 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError(f"status: want an int32 tensor of one word, got {tuple(t.shape)} of {t.dtype}")
+    return _addr(t, "status", device)
 
 
 def _rows(t: torch.Tensor, name: str, heads: int, dim: int, dtype):
@@ -187,7 +210,7 @@ def _table(t: torch.Tensor, batch: int):
     if t.dtype is not torch.int32 or len(shape) != 2 or shape[0] != batch or (shape[1] > 1 and s[1] != 1):
         raise ValueError(f"page_table: want int32 [{batch}][max_pages] with contiguous rows, got "
                          f"{tuple(shape)} of {t.dtype}")
-    return shape[1], _addr(t, "page_table"), s[0]
+    return shape[1], s[0]
 
 
 def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_tok=None,
@@ -203,12 +226,14 @@ def lin_state_kv_append(cache: KVCache, *, layer: int, k, v, page_table, pos, n_
         raise ValueError("k and v must have the same shape and strides")
     B, n = shape[0], shape[1]
     es = 2 if cache.dtype is torch.bfloat16 else 4
-    pages, table, pstride = _table(page_table, B)
-    a = _pack_append(layer, B, n, pages, _addr(k, "k"), _addr(v, "v"), s[0] * es, s[1] * es, table, pstride,
-                     _ptr32(pos, "pos", (B,)), _ptr32(n_tok, "n_tok", (B,)),
-                     _ptr32(parent, "parent", (B, n)), _ptr32(accept_node, "accept_node", (B,)),
-                     0 if status is None else status.data_ptr())
-    rc = _call_append(cache._addr, a, _stream_of(stream, k))
+    pages, pstride = _table(page_table, B)
+    dev = _launch_device(cache._k, "cache")
+    a = _pack_append(layer, B, n, pages, _addr(k, "k", dev), _addr(v, "v", dev), s[0] * es, s[1] * es,
+                     _addr(page_table, "page_table", dev), pstride,
+                     _ptr32(pos, "pos", (B,), dev), _ptr32(n_tok, "n_tok", (B,), dev),
+                     _ptr32(parent, "parent", (B, n), dev), _ptr32(accept_node, "accept_node", (B,), dev),
+                     _status(status, dev))
+    rc = _call_append(cache._addr, a, _stream_of(stream, dev))
     if rc:
         _raise(rc, "lin_state_kv_append")
 
@@ -239,11 +264,12 @@ def lin_state_attn_decode(cache: KVCache, *, layer: int, q, out, page_table, kv_
     if out.shape != shape or not out.is_contiguous():
         raise ValueError(f"out: want a contiguous tensor {tuple(shape)}, got {tuple(out.shape)}")
     es = 2 if cache.dtype is torch.bfloat16 else 4
-    pages, table, pstride = _table(page_table, B)
+    pages, pstride = _table(page_table, B)
+    dev = _launch_device(cache._k, "cache")
     a = _pack_attn(layer, B, n, Hq, _dt(out.dtype), pages, D ** -0.5 if scale is None else scale,
-                   _addr(q, "q"), s[0] * es, s[1] * es, _addr(out, "out"), table, pstride,
-                   _ptr32(kv_len, "kv_len", (B,)), _ptr32(parent, "parent", (B, n)),
-                   0 if status is None else status.data_ptr())
+                   _addr(q, "q", dev), s[0] * es, s[1] * es, _addr(out, "out", dev),
+                   _addr(page_table, "page_table", dev), pstride,
+                   _ptr32(kv_len, "kv_len", (B,), dev), _ptr32(parent, "parent", (B, n), dev), _status(status, dev))
     if workspace is None:
         need = lin_state_attn_workspace(cache, batch=B, n_q=n, num_q_heads=Hq, max_pages=pages,
                                         out_dtype=out.dtype)
@@ -253,13 +279,15 @@ def lin_state_attn_decode(cache: KVCache, *, layer: int, q, out, page_table, kv_
             with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
                                    else torch.cuda.ExternalStream(int(stream))):
                 workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    rc = _call_attn(cache._addr, a, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                    _stream_of(stream, q))
+    if not workspace.is_contiguous():
+        raise ValueError(f"workspace: want a contiguous tensor, got strides {workspace.stride()}")
+    rc = _call_attn(cache._addr, a, _addr(workspace, "workspace", dev), workspace.numel() * workspace.element_size(),
+                    _stream_of(stream, dev))
     if rc:
         _raise(rc, "lin_state_attn_decode")
 
 
-def _norm_row(t, name: str, shape, dtype):
+def _norm_row(t, name: str, shape, dtype, device: int):
     """(address, row stride, dtype) of a [T][C] tensor, or of None."""
     if t is None:
         return 0, 0, dtype
@@ -269,10 +297,10 @@ def _norm_row(t, name: str, shape, dtype):
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: gate, the weights and y must have one dtype, and residual and h_out "
                          f"one: got {t.dtype} beside {dtype}")
-    return _addr(t, name), s[0], t.dtype
+    return _addr(t, name, device), s[0], t.dtype
 
 
-def _norm_weight(w, name: str, channels: Optional[int], dtype):
+def _norm_weight(w, name: str, channels: Optional[int], dtype, device: int):
     if w is None:
         return 0, dtype
     if w.dim() != 1 or not w.is_contiguous() or (channels is not None and w.shape[0] != channels):
@@ -280,7 +308,7 @@ def _norm_weight(w, name: str, channels: Optional[int], dtype):
                          f"got {tuple(w.shape)}")
     if dtype is not None and w.dtype is not dtype:
         raise ValueError(f"{name}: gate, the weights and y must have one dtype, got {w.dtype} beside {dtype}")
-    return _addr(w, name), w.dtype
+    return _addr(w, name, device), w.dtype
 
 
 def lin_state_block_norm(*, x, gate=None, gate_act: Optional[str] = None, w_post=None,
@@ -297,16 +325,17 @@ def lin_state_block_norm(*, x, gate=None, gate_act: Optional[str] = None, w_post
     act = _ACTS.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act: want None, 'silu' or 'sigmoid', got {gate_act!r}")
-    px, sx, xd = _norm_row(x, "x", shape, None)
-    pg, sg, io = _norm_row(gate, "gate", shape, None)
-    py, sy, io = _norm_row(y, "y", shape, io)
-    pr, sr, hd = _norm_row(residual, "residual", shape, None)
-    ph, sh, hd = _norm_row(h_out, "h_out", shape, hd)
-    pw, io = _norm_weight(w_post, "w_post", None, io)
-    ps, io = _norm_weight(scale_w, "scale_w", C, io)
-    pp, io = _norm_weight(w_pre, "w_pre", C, io)
+    dev = _launch_device(x, "x")
+    px, sx, xd = _norm_row(x, "x", shape, None, dev)
+    pg, sg, io = _norm_row(gate, "gate", shape, None, dev)
+    py, sy, io = _norm_row(y, "y", shape, io, dev)
+    pr, sr, hd = _norm_row(residual, "residual", shape, None, dev)
+    ph, sh, hd = _norm_row(h_out, "h_out", shape, hd, dev)
+    pw, io = _norm_weight(w_post, "w_post", None, io, dev)
+    ps, io = _norm_weight(scale_w, "scale_w", C, io, dev)
+    pp, io = _norm_weight(w_pre, "w_pre", C, io, dev)
     a = _pack_norm(T, C, w_post.shape[0] if w_post is not None else 0, _dt(xd), _dt(io or xd), _dt(hd or xd),
                    act, eps, scale, px, pg, pw, pr, ps, pp, ph, py, sx, sg, sr, sh, sy)
-    rc = _call_norm(a, _stream_of(stream, x))
+    rc = _call_norm(a, _stream_of(stream, dev))
     if rc:
         _raise(rc, "lin_state_block_norm")
