@@ -95,12 +95,21 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo in two tf32 values of 11 significant bits, each rounded to nearest
-// (the unit reads the upper 19 bits of an operand), so the pair is off by at
-// most 2^-22 of x. Integer additions: the conversion instruction is slower.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+// x = hi + lo in two tf32 values of 11 significant bits (the unit reads the upper
+// 19 bits of an operand): hi rounded to nearest, by an integer addition as the
+// conversion instruction is slower; lo at most 2^12 units of x's last place, so
+// that what the unit cuts off is one of them, 2^-23 of x. A NaN x leaves NaN in
+// lo whatever becomes of hi, and an infinity does as well.
+__device__ __forceinline__ void split_weight(float x, uint32_t& hi, uint32_t& lo) {  // x below kTf32Top
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi)) + 0x1000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// The same for any x: from kTf32Top on hi is cut off, as rounding up would give an
+// infinity, and lo's cut is 2^-21 of x.
+constexpr float kTf32Top = 0x1.ffep127f;
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (fabsf(x) < kTf32Top ? __float_as_uint(x) + 0x1000u : __float_as_uint(x)) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
 }
 // a pair of bf16 values with 0 for infinities and NaN
 __device__ __forceinline__ uint32_t finite_bf16(uint32_t w) {
@@ -478,10 +487,10 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         uint32_t ph[2][4], pl[2][4];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          split_tf32(s[k][0], ph[k][0], pl[k][0]);
-          split_tf32(s[k][2], ph[k][1], pl[k][1]);
-          split_tf32(s[k][1], ph[k][2], pl[k][2]);
-          split_tf32(s[k][3], ph[k][3], pl[k][3]);
+          split_weight(s[k][0], ph[k][0], pl[k][0]);
+          split_weight(s[k][2], ph[k][1], pl[k][1]);
+          split_weight(s[k][1], ph[k][2], pl[k][2]);
+          split_weight(s[k][3], ph[k][3], pl[k][3]);
         }
         const uint32_t va = vs + ds * (DW * C::ES) + chunk_at<ROWB>(2 * t4, g >> 2) + (g & 3) * 4;
         const uint32_t vb1 = vs + ds * (DW * C::ES) + chunk_at<ROWB>(2 * t4 + 1, g >> 2) + (g & 3) * 4;

@@ -38,3 +38,94 @@ def test_a_call_without_work_ends_before_the_next_launch(dtype, n, G, lens, stat
         assert bool((ws == 255).all())
     assert L.lin_state_read_status(status) == status_want
     assert bool((out == 7.0).all())
+
+
+def pattern(bits, dtype):
+    """One value of this bit pattern."""
+    if dtype == F32:
+        return torch.tensor(bits - (1 << 32) if bits >> 31 else bits, dtype=torch.int32).view(F32)
+    return torch.tensor(bits - (1 << 16) if bits >> 15 else bits, dtype=torch.int16).view(BF)
+
+
+NANS = [(F32, 0x7fffffff), (F32, 0xffffffff), (F32, 0x7fc00000), (F32, 0x7f800001), (F32, 0xffbfffff),
+        (BF, 0x7fff), (BF, 0xffff), (BF, 0x7f81)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(1, 4), (2, 12), (4, 12), (2, 40)])
+@pytest.mark.parametrize("dtype,bits", NANS)
+def test_a_visible_nan_reaches_every_output_that_uses_it(dtype, bits, D, n, G):
+    """A NaN of any payload in a query, a key or a value that is seen: NaN in the
+    outputs it has a part in, the others as they were, bit for bit."""
+    lens, ps = [200, 75, 40], 16
+    gen = torch.Generator(device="cuda").manual_seed(D + n + G)
+    pages = [-(-x // ps) for x in lens]
+    table = torch.zeros((3, max(pages)), dtype=torch.int32)
+    for r in range(3):
+        table[r, :pages[r]] = torch.arange(sum(pages[:r]), sum(pages[:r + 1]))
+    k, v = (torch.randn((1, sum(pages), ps, 2, D), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((3, n, 2 * G, D), generator=gen, device="cuda").to(dtype)
+    bad = pattern(bits, dtype).cuda()
+
+    def attend(q, k, v):
+        out = torch.empty((3, n, 2 * G, D), dtype=dtype, device="cuda")
+        L.lin_state_attn_decode(L.KVCache(1, sum(pages), ps, 2, D, dtype=dtype, k=k, v=v), layer=0, q=q, out=out,
+                                page_table=table.cuda(), kv_len=i32(*lens))
+        return out
+
+    plain = attend(q, k, v)
+    assert not plain.isnan().any()
+    q2 = q.clone()
+    q2[1, n - 1, G + 1, 7] = bad
+    hit = torch.zeros(plain.shape, dtype=torch.bool, device="cuda")
+    hit[1, n - 1, G + 1] = True
+    out = attend(q2, k, v)
+    assert bool(out[hit].isnan().all()) and torch.equal(out[~hit], plain[~hit])
+    page, row = int(table[0, 33 // ps]), 33 % ps  # token 33 of request 0, kv head 1
+    for in_value in (False, True):
+        k2, v2 = k.clone(), v.clone()
+        (v2 if in_value else k2)[0, page, row, 1, 9] = bad
+        hit = torch.zeros(plain.shape, dtype=torch.bool, device="cuda")
+        hit[0, :, G:, 9 if in_value else slice(None)] = True
+        out = attend(q, k2, v2)
+        assert bool(out[hit].isnan().all()) and torch.equal(out[~hit], plain[~hit])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(1, 4), (2, 12), (2, 40)])
+@pytest.mark.parametrize("bits", [0x7f7fffff, 0xff7fffff, 0x7f7ff000, 0x7f7fefff])
+def test_fp32_values_next_to_the_largest(n, G, D, bits):
+    """Keys, queries and values at the end of the range stay finite: products of
+    the largest with 2^-125 are 2^3, and one token's weight is 1. Tolerances as
+    for other values (2 S (D + 16 + c) u + (L + 16) u + 12 u of sum p |v|, u =
+    2^-24), with c = 24: three terms of 2^-22, and 2^-21 where the largest value's
+    first part is cut off. A value leaves 2^-12 to the end of the range, as the
+    weight itself may round to more than 1."""
+    big = float(pattern(bits, F32))
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    k, v = (torch.randn((1, 2, 16, 1, D), generator=gen, device="cuda") for _ in range(2))
+    q = torch.randn((1, n, G, D), generator=gen, device="cuda")
+
+    def check(q, k, v, length):
+        out = torch.empty((1, n, G, D), device="cuda")
+        L.lin_state_attn_decode(L.KVCache(1, 2, 16, 1, D, dtype=F32, k=k, v=v), layer=0, q=q, out=out,
+                                page_table=i32(1, 0)[None].contiguous(), kv_len=i32(length))
+        kk, vv = (t[0, [1, 0]].reshape(32, D)[:length].double() for t in (k, v))
+        s = torch.einsum("jhd,td->jht", q[0].double(), kk) * D ** -0.5
+        hidden = torch.arange(length, device="cuda") > length - n + torch.arange(n, device="cuda")[:, None]
+        p = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1)
+        spread = float((q[0].double().abs()[:, :, None] * kk.abs()).sum(-1).max()) * D ** -0.5
+        tol = (p @ vv.abs()) * (2 * spread * (D + 16 + 24) + length + 16 + 12) * 2.0 ** -24
+        assert bool(torch.isfinite(out).all())
+        assert bool(((out[0].double() - p @ vv).abs() <= tol).all())
+
+    q2, k2 = q.clone(), k.clone()
+    q2[..., 5], k2[0, 1, 3, 0, 5] = 2.0 ** -125, big
+    check(q2, k2, v, 30)
+    q2, k2 = q.clone(), k.clone()
+    q2[..., 5], k2[..., 5] = big, 2.0 ** -125
+    check(q2, k2, v, 30)
+    v2 = v.clone()
+    top = float(pattern(0x7f7ff801, F32))
+    v2[0, 1, 0, 0, 5] = max(-top, min(top, big))
+    check(q, k, v2, n)
