@@ -247,24 +247,26 @@ struct Shape {
 
 template <int D>
 int ctas_of(bool bf16, int rt) {
-  return bf16      ? Cfg<D, LIN_BF16, 1>::CTAS
-         : rt == 1 ? Cfg<D, LIN_F32, 1>::CTAS
-         : rt == 2 ? Cfg<D, LIN_F32, 2>::CTAS
-                   : Cfg<D, LIN_F32, 4>::CTAS;
+  if (bf16) return rt == 1 ? Cfg<D, LIN_BF16, 1>::CTAS : rt == 2 ? Cfg<D, LIN_BF16, 2>::CTAS : Cfg<D, LIN_BF16, 4>::CTAS;
+  return rt == 1 ? Cfg<D, LIN_F32, 1>::CTAS : rt == 2 ? Cfg<D, LIN_F32, 2>::CTAS : Cfg<D, LIN_F32, 4>::CTAS;
 }
 
 // bf16 caches: up to 16 rows per (request, kv head) on warp-level MMA, more on
 // tcgen05 in blocks of 32, 64 or 128; but 17 to 32 rows of requests of up to 256
 // tokens as two blocks of 16, for an item's start and end take longer there than
 // reading it twice (4 drafts of a group of 8: 1 request
-// of 64 tokens 8.6 to 6.3 us, 256 requests of up to 256 tokens 41 to 38 us). fp32 caches: warp-level MMA in blocks of 16,
-// 32 or 64.
+// of 64 tokens 8.6 to 6.3 us, 256 requests of up to 256 tokens 41 to 38 us). fp32
+// caches: warp-level MMA in blocks of 16, 32 or 64. So do fp32 outputs of bf16 caches,
+// whose long sums tcgen05 does not round (64 requests of 500-8,000 tokens, heads
+// of 128, 32, 64 and 128 rows: 81, 140 and 260 us, where it took 76, 102 and 170;
+// heads of 64, 32 rows: 86 against 135).
 Shape shape_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
   const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads);
   const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
   const bool b = c.dtype == LIN_BF16;
-  if (b && rows > 16 && (rows > 32 || units > 4)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
-  const int rt = rows <= 16 || b ? 1 : rows <= 32 ? 2 : 4;
+  const bool bb = b && a.out_dtype == LIN_BF16;
+  if (bb && rows > 16 && (rows > 32 || units > 4)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
+  const int rt = rows <= 16 || bb ? 1 : rows <= 32 ? 2 : 4;
   return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), b ? 3 : 2, b ? 4 : 2};
 }
 

@@ -1,5 +1,6 @@
 // Decode attention over a paged key-value cache (lin_step.h): bf16 caches with up
-// to 16 rows per (request, kv head), and fp32 caches.
+// to 16 rows per (request, kv head), 32 of short requests, or with fp32 outputs,
+// and fp32 caches.
 //
 //   out[r][j][h] = sum_t p_t v_t / sum_t p_t,  p_t = 2^(s_t - m),
 //   s_t = scale log2(e) q.k_t over the tokens that query j sees,
@@ -34,7 +35,7 @@ namespace attn {
 
 constexpr int kSub = 16;  // tokens of a ring slot
 
-// Warps of one CTA: KG groups x RT row tiles (bf16: 1) x DS parts of head_dim. DS
+// Warps of one CTA: KG groups x RT row tiles x DS parts of head_dim. DS
 // warps share a row tile where rows of 512 bytes and more would otherwise leave
 // one warp per scheduler: each makes its channels' part of the scores, which are
 // added in shared memory, and its channels' value sums. As many CTAs as leave room for two slots a group and registers
@@ -53,7 +54,7 @@ struct Cfg {
   static constexpr int DS = ROWB <= 256 ? 1 : ROWB == 512 ? 2 : RT == 4 ? 2 : 4;
   static constexpr int NW = ROWB <= 256 ? (MANY ? 8 : 4) : ROWB == 512 ? (MANY ? 16 : 8) : 8;
   // a warp keeps its queries' operands in registers where that costs no occupancy
-  static constexpr bool QREG = BF && D <= 128;
+  static constexpr bool QREG = BF && D <= 128 && !MANY;
   static constexpr int KG = NW / (RT * DS);
   static constexpr int GT = RT * DS * 32;             // threads of a group
   static constexpr int BUDGET = (CTAS == 4 ? 55 : CTAS == 3 ? 73 : CTAS == 2 ? 110 : 216) * 1024;
@@ -450,8 +451,9 @@ __global__ void __launch_bounds__(C::NW * 32, C::CTAS) attn_kernel(const Plan p)
         l1 += s[n][2] + s[n][3];
       }
       // The unit's own accumulation cuts off below the last place of the sum: over a
-      // long cache the loss adds up (4.6e-6 of the outputs at 3,000 tokens), so
-      // fp32 outputs add a slot's sums by rounded additions.
+      // long cache the loss adds up (4.6e-6 of the outputs at 3,000 tokens; tcgen05
+      // does the same, 9.5e-5 at 16,384 tokens of 128 rows), so fp32 outputs add a
+      // slot's sums by rounded additions.
       if constexpr (BF) {
         const uint32_t vat = vs + chunk_at<ROWB>(lane & 15, lane >> 4);
         uint32_t pf[PT][4];
@@ -561,8 +563,11 @@ cudaError_t launch_main(const Plan& p, int grid, cudaStream_t s) {
 
 template <int D, int DT>
 cudaError_t launch_rows(const Plan& p, int row_tiles, int grid, cudaStream_t s) {
-  if constexpr (DT == LIN_BF16) {  // one row tile; more rows take the kernels of attn_umma.cuh
-    return p.a.out_dtype == LIN_F32 ? launch_main<Cfg<D, DT, 1>, 3>(p, grid, s) : launch_main<Cfg<D, DT, 1>, 2>(p, grid, s);
+  if constexpr (DT == LIN_BF16) {  // bf16 outputs of more rows take the kernels of attn_umma.cuh
+    return row_tiles == 4   ? launch_main<Cfg<D, DT, 4>, 3>(p, grid, s)
+           : row_tiles == 2 ? launch_main<Cfg<D, DT, 2>, 3>(p, grid, s)
+           : p.a.out_dtype == LIN_F32 ? launch_main<Cfg<D, DT, 1>, 3>(p, grid, s)
+                                      : launch_main<Cfg<D, DT, 1>, 2>(p, grid, s);
   } else {
     return row_tiles == 1   ? launch_main<Cfg<D, DT, 1>, 1>(p, grid, s)
            : row_tiles == 2 ? launch_main<Cfg<D, DT, 2>, 1>(p, grid, s)

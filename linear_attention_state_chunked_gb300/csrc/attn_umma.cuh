@@ -1,6 +1,6 @@
 // Decode attention for more than 16 rows per (request, kv head) over a bf16
-// cache: a verify of several drafts, or many query heads to a key-value head.
-// The products run on the 5th-generation tensor cores.
+// cache, bf16 outputs: a verify of several drafts, or many query heads to a
+// key-value head. The products run on the 5th-generation tensor cores.
 //
 // What bounds it is HBM, as for few rows (attn_kernel.cuh); but warp-level MMA
 // of 16 rows, one m16n8k16 in 8 cycles per scheduler, takes as long as the loads
@@ -27,8 +27,13 @@
 // K and V tiles pass through a ring of U units (16-byte asynchronous copies, as
 // pages may end anywhere). S, and P as the A operand, lie in tensor memory, S in
 // two buffers and P in NB, so scores, weights and value sums of successive tiles
-// overlap. The weights go in PT bf16 parts (2^-16, 2^-24), each a product of its
-// own.
+// overlap. The weights go in PT = 2 bf16 parts (2^-16 together), each a product of
+// its own.
+//
+// The value sums of a piece stay in the unit, which cuts off below the last place
+// of what it adds to: with 128 rows that takes 1e-4 off the outputs over 16,384
+// tokens of one piece and 8.6e-4 over 131,072, where a bf16 output is rounded by up
+// to 3.9e-3. fp32 outputs take attn_kernel.cuh, which adds with rounding.
 #pragma once
 
 #include "attn_common.cuh"
@@ -36,10 +41,10 @@
 namespace lin {
 namespace attn {
 
-template <int D_, int RP_, int PT_>
+template <int D_, int RP_>
 struct UCfg {
-  static constexpr int D = D_, RP = RP_, PT = PT_;
-  static constexpr int TK = D == 64 && PT == 2 ? 128 : 64;  // tokens of a tile
+  static constexpr int D = D_, RP = RP_, PT = 2;
+  static constexpr int TK = D == 64 ? 128 : 64;  // tokens of a tile
   static constexpr int UNIT = TK * D * 2;        // its K, or its V
   static constexpr int COPIES = 128 / RP;
   static constexpr int KW = TK / COPIES;         // a copy's tokens
@@ -513,11 +518,10 @@ cudaError_t launch_umma(const Plan& p, int grid, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_umma_rows(const Plan& p, int grid, cudaStream_t s) {
-  const bool f32 = p.a.out_dtype == LIN_F32;
   switch (p.block_rows) {
-    case 32: return f32 ? launch_umma<UCfg<D, 32, 3>>(p, grid, s) : launch_umma<UCfg<D, 32, 2>>(p, grid, s);
-    case 64: return f32 ? launch_umma<UCfg<D, 64, 3>>(p, grid, s) : launch_umma<UCfg<D, 64, 2>>(p, grid, s);
-    default: return f32 ? launch_umma<UCfg<D, 128, 3>>(p, grid, s) : launch_umma<UCfg<D, 128, 2>>(p, grid, s);
+    case 32: return launch_umma<UCfg<D, 32>>(p, grid, s);
+    case 64: return launch_umma<UCfg<D, 64>>(p, grid, s);
+    default: return launch_umma<UCfg<D, 128>>(p, grid, s);
   }
 }
 

@@ -129,3 +129,28 @@ def test_fp32_values_next_to_the_largest(n, G, D, bits):
     top = float(pattern(0x7f7ff801, F32))
     v2[0, 1, 0, 0, 5] = max(-top, min(top, big))
     check(q, k, v2, n)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(1, 8), (17, 1), (4, 8), (8, 8), (3, 43)])
+@pytest.mark.parametrize("positive", [False, True])
+def test_fp32_outputs_of_a_bf16_cache_do_not_lose_with_the_length(D, n, G, positive):
+    """304 requests that share one sequence's pages, so that the longer one stays
+    in one piece: 256 and 16,384 tokens to one bound, 2^-20 of the outputs, as for
+    fp32 caches (rounded sums grow as the outputs' own random sum does). Values of
+    one sign would show any bias of the additions."""
+    B = 304
+    for length in (256, 16384):
+        gen = torch.Generator(device="cuda").manual_seed(D + n)
+        k, v = (torch.randn((1, length // 64, 64, 1, D), generator=gen, device="cuda") for _ in range(2))
+        k, v = k.to(BF), (v.abs() + 1 if positive else v).to(BF)
+        q = torch.randn((B, n, G, D), generator=gen, device="cuda").to(BF)
+        out = torch.empty((B, n, G, D), dtype=F32, device="cuda")
+        table = torch.arange(length // 64, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+        L.lin_state_attn_decode(L.KVCache(1, length // 64, 64, 1, D, dtype=BF, k=k, v=v), layer=0, q=q, out=out,
+                                page_table=table, kv_len=torch.full((B,), length, dtype=torch.int32, device="cuda"))
+        hidden = torch.arange(length, device="cuda") > length - n + torch.arange(n, device="cuda")[:, None]
+        for r in (0, 151, 303):
+            s = torch.einsum("jhd,td->jht", q[r].double(), k.reshape(length, D).double()) * D ** -0.5
+            want = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1) @ v.reshape(length, D).double()
+            assert float((out[r] - want).norm() / want.norm()) < 2.0 ** -20, (length, r)
