@@ -99,8 +99,10 @@ LIN_API int lin_state_kv_append(const lin_kv_cache_t* cache, const lin_kv_append
  * the batch's tokens are cut into equal ranges, and items that cross a border
  * are joined by a second launch.
  * Workspace: lin_state_attn_workspace() bytes of device memory, 16-byte
- * aligned, not shared by calls that may overlap. It grows with the GPU and
- * with n_q * num_q_heads / num_kv_heads, not with the cache. Its contents
+ * aligned, not shared by calls that may overlap. The size never shrinks as
+ * batch, n_q, num_q_heads / num_kv_heads or max_pages grow, and covers either
+ * output type: one sized for the largest call serves the smaller ones. A few MB,
+ * it depends on the GPU and not on the cache's size. Its contents
  * before the call do not matter. Longest request: 2^31 - 65536 tokens. */
 typedef struct {
   int32_t layer, batch, n_q, num_q_heads;

@@ -10,6 +10,7 @@ namespace {
 constexpr int kJoinWarps = 8, kRowWarps = 16;
 constexpr int kJoinRows = 16;    // most rows of an item side by side in the grid
 constexpr int kMaxRanges = 1024;
+constexpr int kShortUnits = 4;   // of a request: see shape_of
 
 // The item that begins in range c and goes on past it has the parts, in token
 // order, 2c + 1 and then 2c' of the ranges c' = c + 1, ... They are joined in that
@@ -260,29 +261,33 @@ int ctas_of(bool bf16, int rt) {
 // whose long sums tcgen05 does not round (64 requests of 500-8,000 tokens, heads
 // of 128, 32, 64 and 128 rows: 81, 140 and 260 us, where it took 76, 102 and 170;
 // heads of 64, 32 rows: 86 against 135).
-Shape shape_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
-  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads);
-  const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
+Shape shape_of(const lin_kv_cache_t& c, int rows, int64_t units, int out_dtype) {
   const bool b = c.dtype == LIN_BF16;
-  const bool bb = b && a.out_dtype == LIN_BF16;
-  if (bb && rows > 16 && (rows > 32 || units > 4)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
+  const bool bb = b && out_dtype == LIN_BF16;
+  if (bb && rows > 16 && (rows > 32 || units > kShortUnits)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
   const int rt = rows <= 16 || bb ? 1 : rows <= 32 ? 2 : 4;
   return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), b ? 3 : 2, b ? 4 : 2};
 }
 
 // CTAs of the main kernel: what is resident at once, or one per unit where the
 // longest request allowed would give fewer.
-int grid_of(const lin_kv_cache_t& c, const lin_attn_args_t& a, const Shape& f) {
+int grid_of(const lin_kv_cache_t& c, int batch, int rows, int64_t units, const Shape& f) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
   if (sms <= 0) sms = 152;  // no device: the size of a GB300
-  const int rows = a.n_q * (a.num_q_heads / c.num_kv_heads);
   const int64_t blocks = (rows + f.block_rows - 1) / f.block_rows;
-  const int64_t units = (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
-  const int64_t items = int64_t(a.batch) * c.num_kv_heads * blocks;
+  const int64_t items = int64_t(batch) * c.num_kv_heads * blocks;
   const int64_t most = units > 1 && items < INT32_MAX ? items * units : items;
   const int64_t full = int64_t(sms) * f.ctas < kMaxRanges ? int64_t(sms) * f.ctas : kMaxRanges;
   return static_cast<int>(most < full && most > 0 ? most : full);
+}
+
+int rows_of(const lin_kv_cache_t& c, const lin_attn_args_t& a) { return a.n_q * (a.num_q_heads / c.num_kv_heads); }
+int64_t units_most(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+  return (int64_t(a.max_pages) * c.page_size + kUnit - 1) / kUnit;
+}
+size_t bytes_of(const lin_kv_cache_t& c, const Shape& f, size_t grid) {
+  return 2 * grid * f.block_rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
 }
 
 // Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
@@ -296,10 +301,31 @@ void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
 }  // namespace
 }  // namespace attn
 
+// What this call uses.
+size_t attn_need(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
+  const int rows = attn::rows_of(c, a);
+  const int64_t units = attn::units_most(c, a);
+  const attn::Shape f = attn::shape_of(c, rows, units, a.out_dtype);
+  return attn::bytes_of(c, f, attn::grid_of(c, a.batch, rows, units, f));
+}
+
+// The most that a call uses of up to this batch, so many rows and pages, and either
+// output type. Within one kind of kernel that grows with each of them, so the
+// kinds' largest calls do (shape_of's borders).
 size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
-  const attn::Shape f = attn::shape_of(c, a);
-  const size_t grid = attn::grid_of(c, a, f);
-  return 2 * grid * f.block_rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(longlong2);
+  const int rows = attn::rows_of(c, a);
+  const int64_t units = attn::units_most(c, a);
+  size_t most = 0;
+  for (const int out : {LIN_BF16, LIN_F32})
+    for (const int r : {16, 32, 64, rows})
+      for (const int64_t u : {int64_t(attn::kShortUnits), units}) {
+        const int x = r < rows ? r : rows;
+        const int64_t y = u < units ? u : units;
+        const attn::Shape f = attn::shape_of(c, x, y, out);
+        const size_t n = attn::bytes_of(c, f, attn::grid_of(c, a.batch, x, y, f));
+        if (n > most) most = n;
+      }
+  return most;
 }
 
 cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a, void* ws, cudaStream_t s) {
@@ -307,9 +333,10 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.c = c;
   p.a = a;
   p.group = a.num_q_heads / c.num_kv_heads;
-  p.rows = a.n_q * p.group;
-  const attn::Shape f = attn::shape_of(c, a);
-  const int grid = attn::grid_of(c, a, f);
+  p.rows = attn::rows_of(c, a);
+  const int64_t units = attn::units_most(c, a);
+  const attn::Shape f = attn::shape_of(c, p.rows, units, a.out_dtype);
+  const int grid = attn::grid_of(c, a.batch, p.rows, units, f);
   p.grid = grid;
   p.block_rows = f.block_rows;
   p.item_cost = f.item_cost;

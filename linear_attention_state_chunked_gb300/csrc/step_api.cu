@@ -118,7 +118,7 @@ int lin_state_attn_decode(const lin_kv_cache_t* c, const lin_attn_args_t* a, voi
   if (rc) return rc;
   if (a->page_table_stride < a->max_pages && a->batch > 1)
     return fail(LIN_EINVAL, "attn: page_table_stride smaller than max_pages");
-  const size_t need = lin::attn_workspace(*c, *a);
+  const size_t need = lin::attn_need(*c, *a);
   if (workspace_bytes < need || (need > 0 && !workspace))
     return fail(LIN_EWORKSPACE, "attn: workspace of %zu bytes needed, %zu given", need, workspace_bytes);
   if (!aligned16(workspace)) return fail(LIN_EINVAL, "attn: workspace must be 16-byte aligned");

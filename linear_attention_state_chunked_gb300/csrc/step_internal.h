@@ -12,6 +12,7 @@ cudaError_t launch_kv_append(const lin_kv_cache_t& cache, const lin_kv_append_ar
 
 // attn_decode.cu
 constexpr int kAttnMaxQuery = 32;
+size_t attn_need(const lin_kv_cache_t& cache, const lin_attn_args_t& a);
 size_t attn_workspace(const lin_kv_cache_t& cache, const lin_attn_args_t& a);
 cudaError_t launch_attn_decode(const lin_kv_cache_t& cache, const lin_attn_args_t& a,
                                void* workspace, cudaStream_t stream);

@@ -154,3 +154,24 @@ def test_fp32_outputs_of_a_bf16_cache_do_not_lose_with_the_length(D, n, G, posit
             s = torch.einsum("jhd,td->jht", q[r].double(), k.reshape(length, D).double()) * D ** -0.5
             want = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1) @ v.reshape(length, D).double()
             assert float((out[r] - want).norm() / want.norm()) < 2.0 ** -20, (length, r)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_workspace_of_the_largest_call_serves_the_smaller(D, dtype):
+    """A server keeps one workspace, of its most drafts and its widest table."""
+    B, H, G, ps, wide = 9, 2, 8, 16, 80
+    cache = L.KVCache(1, wide, ps, H, D, dtype=dtype, k=torch.randn((1, wide, ps, H, D), device="cuda").to(dtype),
+                      v=torch.randn((1, wide, ps, H, D), device="cuda").to(dtype))
+    ws = torch.empty(L.lin_state_attn_workspace(cache, batch=B, n_q=16, num_q_heads=H * G, max_pages=wide),
+                     dtype=torch.uint8, device="cuda")
+    for b, n, pages in [(9, 16, 80), (9, 1, 80), (9, 2, 80), (9, 4, 80), (9, 8, 80), (1, 1, 80), (9, 4, 16), (9, 4, 17),
+                        (3, 3, 4), (9, 1, 1)]:
+        q = torch.randn((b, n, H * G, D), device="cuda").to(dtype)
+        table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(b, pages).contiguous()
+        length = torch.full((b,), pages * ps - 3, dtype=torch.int32, device="cuda")
+        for out_dtype in (BF, F32):
+            outs = [torch.empty(q.shape, dtype=out_dtype, device="cuda") for _ in range(2)]
+            for out, w in zip(outs, (ws, None)):
+                L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table, kv_len=length, workspace=w)
+            assert torch.equal(*outs)
