@@ -23,6 +23,8 @@ namespace attn {
 
 constexpr float kSlack = 8.0f;
 constexpr int kUnit = 64;  // tokens of a work unit
+// A part's sum where its item is not to be written: a bad tree, or a wait that ran out
+constexpr float kLeftOut = -1.0f;
 
 struct Plan {
   lin_kv_cache_t c;
@@ -41,7 +43,7 @@ struct Plan {
   uint32_t group_mul, group_shift;  // the same for row / group
   uint32_t block_mul, block_shift;  // and for item / row_blocks
   float* part;        // [2 grid][block_rows][D] value sums of unfinished pieces
-  float2* part_ml;    // [2 grid][block_rows] their (maximum, sum); sum -1: left out
+  float2* part_ml;    // [2 grid][block_rows] their (maximum, sum or kLeftOut)
   longlong2* split;   // [grid] the item that begins in range c and goes on past
                       // it (or -1), and its number of parts
 };
@@ -277,7 +279,7 @@ __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
-    if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? -1.0f : sum);
+    if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? kLeftOut : sum);
   }
 }
 

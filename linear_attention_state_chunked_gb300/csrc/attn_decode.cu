@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   for (int i = lane; i < s.parts; i += 32) {
     const float2 ml = p.part_ml[part_row(p, c, i, row)];
     top = fmaxf(top, ml.x);
-    out |= ml.y == -1.0f;
+    out |= ml.y == kLeftOut;
   }
   if (__any_sync(~0u, out)) return;  // a request left out
 #pragma unroll
@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) join_row_kernel(const Plan p) 
 #pragma unroll
     for (int k = 0; k < MOST; ++k) {
       top = fmaxf(top, ml[k].x);
-      out |= ml[k].y == -1.0f;
+      out |= ml[k].y == kLeftOut;
     }
 #pragma unroll
     for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));

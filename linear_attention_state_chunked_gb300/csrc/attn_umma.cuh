@@ -485,6 +485,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
         umma::mma_commit(&b_drain);
         umma::mbar_wait(&b_drain, 0, kUmmaWaitTries);
       }
+      // The parts that this range now leaves unwritten, of the piece at hand and of an
+      // item that goes on past the range, count as left out, and their items with them.
+      for (int x = tid; x < 2 * RP; x += NT)
+        if (x >= RP || w.t0 > 0)
+          p.part_ml[2 * int64_t(blockIdx.x) * RP + x] = make_float2(-INFINITY, kLeftOut);
       w.split.x = -1;
       break;
     }

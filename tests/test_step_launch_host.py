@@ -39,3 +39,20 @@ def test_no_path_ends_before_the_wait(name, body):
     get the memory that it still writes."""
     before = body[:body.index(WAIT)]
     assert not re.search(r"\b(return|exit)\b", before), name
+
+
+def test_a_wait_that_ran_out_leaves_its_items_out():
+    """The joins skip an item of which any part is marked. (No wait can be made to
+    run out from outside, so this reads the source as well.) A range that gives up
+    has two parts at most to answer for: the piece at hand, which is the first
+    part where it goes on from the range before, and the second one, of an item
+    that goes on past the range."""
+    with open(os.path.join(CSRC, "attn_umma.cuh")) as f:
+        text = f.read()
+    dead = text[text.index("if (s_dead) {"):]
+    dead = dead[:dead.index("break;")]
+    assert re.search(r"if \(x >= RP \|\| w\.t0 > 0\)\s+p\.part_ml\[2 \* int64_t\(blockIdx\.x\) \* RP \+ x\] = "
+                     r"make_float2\(-INFINITY, kLeftOut\)", dead)
+    for name, body in kernels_that_wait():
+        skip = re.search(r"out \|= ml\S*\.y == kLeftOut;.*?return;", body, re.S)
+        assert skip and "p.a.out" not in body[:skip.end()], name
