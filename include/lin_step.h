@@ -24,7 +24,8 @@ extern "C" {
 /* ---- the paged key-value cache -------------------------------------------
  * k, v: bases of [num_layers][num_pages][page_size][num_kv_heads][head_dim]
  * in `dtype`; head_dim is contiguous, the other strides are given in bytes
- * (multiples of 16, the same for k and v), so tokens-first and heads-first
+ * (multiples of 16, the same for k and v; that of an axis of one is not looked
+ * at, here and below), so tokens-first and heads-first
  * pages and views of a combined tensor all do. A request's token t lies in
  * page page_table[r][t / page_size], row t % page_size. page_size is any
  * positive number; head_dim is 64, 128 or 256 (else LIN_EUNSUPPORTED). */

@@ -17,11 +17,11 @@ int check_cache(const lin_kv_cache_t* c) {
   if (!c->k || !c->v) return fail(LIN_EINVAL, "cache: k / v is NULL");
   if (!aligned16(c->k) || !aligned16(c->v)) return fail(LIN_EINVAL, "cache: k / v must be 16-byte aligned");
   // the four axes nest in some order: sorted by stride, each stride covers
-  // the extent of the axes below it
+  // the extent of the axes below it (the stride of an axis of one is not used)
   int64_t stride[4] = {c->head_stride, c->token_stride, c->page_stride, c->layer_stride};
   int64_t count[4] = {c->num_kv_heads, c->page_size, c->num_pages, c->num_layers};
   for (int i = 0; i < 4; ++i)
-    if (stride[i] < 0 || (stride[i] & 15))
+    if (count[i] > 1 && (stride[i] < 0 || (stride[i] & 15)))
       return fail(LIN_EINVAL, "cache: strides must be non-negative multiples of 16 bytes");
   for (int i = 1; i < 4; ++i)
     for (int j = i; j > 0 && stride[j] < stride[j - 1]; --j) {
@@ -39,10 +39,12 @@ int check_cache(const lin_kv_cache_t* c) {
   return LIN_OK;
 }
 
-// Rows of `heads` head vectors, `tokens` to a request.
+// Rows of `heads` head vectors, `tokens` to a request. The stride of a single
+// token or request is not used.
 int check_rows(const char* what, int64_t req_stride, int64_t token_stride, int64_t row_bytes,
                int batch, int tokens) {
-  if (req_stride < 0 || token_stride < 0 || (req_stride & 15) || (token_stride & 15))
+  if ((tokens > 1 && (token_stride < 0 || (token_stride & 15))) ||
+      (batch > 1 && (req_stride < 0 || (req_stride & 15))))
     return fail(LIN_EINVAL, "%s: strides must be non-negative multiples of 16 bytes", what);
   if ((tokens > 1 && token_stride < row_bytes) || (batch > 1 && req_stride < row_bytes))
     return fail(LIN_EINVAL, "%s: strides smaller than one row of %lld bytes", what,

@@ -175,3 +175,23 @@ def test_a_workspace_of_the_largest_call_serves_the_smaller(D, dtype):
             for out, w in zip(outs, (ws, None)):
                 L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table, kv_len=length, workspace=w)
             assert torch.equal(*outs)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hq", [2, 64])
+def test_strides_of_single_requests_and_tokens_are_not_used(dtype, Hq):
+    """One request of one token, a cache of one layer and page: any strides there."""
+    gen = torch.Generator(device="cuda").manual_seed(Hq)
+    k, v = (torch.randn((1, 1, 16, 1, 64), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    q, new = (torch.randn((1, 1, h, 64), generator=gen, device="cuda").to(dtype) for h in (Hq, 1))
+    want = torch.empty_like(q)
+
+    def attend(k, v, q, new, out):
+        cache = L.KVCache(1, 1, 16, 1, 64, dtype=dtype, k=k, v=v)
+        L.lin_state_kv_append(cache, layer=0, k=new, v=new, page_table=i32(0)[None], pos=i32(9))
+        L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=i32(0)[None], kv_len=i32(10))
+        return out
+
+    want = attend(k, v, q, new, torch.empty_like(q))
+    odd = [torch.as_strided(t, t.shape, (3, 5, *t.stride()[2:])) for t in (k, v, q, new)]
+    assert torch.equal(attend(*odd, torch.empty_like(q)), want)
