@@ -130,6 +130,9 @@ class HybridModel:
         return logits
 
     def verify(self, drafts):
+        """Two drafts or more: one would be a step, which moves the linear states."""
+        if drafts.shape[1] < 2:
+            raise ValueError(f"a verify takes 2 drafts or more, got {drafts.shape[1]}: one token is a step")
         return self.forward(drafts, verify=True)
 
     def commit(self, accept_len):
@@ -151,6 +154,8 @@ def main():
     ap.add_argument("--steps", type=int, default=8)
     ap.add_argument("--batch", type=int, default=4)
     args = ap.parse_args()
+    if args.steps < 1:
+        ap.error("--steps: 1 or more, for drafts to verify")
     model = HybridModel(args.batch, 4 * args.steps + 8)
     token = torch.arange(args.batch, device="cuda") % VOCAB
     said = [token]
