@@ -80,9 +80,11 @@ __device__ __forceinline__ int units_of(int len, int64_t most) {
   return len < 0 || len > most ? 0 : len == 0 ? 1 : (len - 1) / kUnit + 1;
 }
 
-// The longest request allowed: token indices stay clear of the 32-bit end.
+// The longest request allowed: token indices, and those that loads run ahead by,
+// stay clear of the 32-bit end.
+constexpr int64_t kLongest = (int64_t(1) << 31) - 65536;
 __device__ __forceinline__ int64_t longest(const Plan& p) {
-  return min(int64_t(p.a.max_pages) * p.c.page_size, int64_t(INT32_MAX - 65536));
+  return min(int64_t(p.a.max_pages) * p.c.page_size, kLongest);
 }
 
 // Where a CTA is in its range.

@@ -195,3 +195,26 @@ def test_strides_of_single_requests_and_tokens_are_not_used(dtype, Hq):
     want = attend(k, v, q, new, torch.empty_like(q))
     odd = [torch.as_strided(t, t.shape, (3, 5, *t.stride()[2:])) for t in (k, v, q, new)]
     assert torch.equal(attend(*odd, torch.empty_like(q)), want)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_the_longest_request_and_one_token_more(n):
+    """2^31 - 65536 tokens, whose table names one page of 65,536 tokens over and
+    over: the output is that page's mean, as all keys are 0, to the 2^31 / 608 / 16
+    additions of a group of warps that rounds each by 2^-24 at most, below 2^-6. One
+    token more is left out."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    k = torch.zeros((1, 1, 65536, 1, 64), dtype=BF, device="cuda")
+    v = torch.randn(k.shape, generator=gen, device="cuda").abs().to(BF)
+    cache = L.KVCache(1, 1, 65536, 1, 64, dtype=BF, k=k, v=v)
+    q = torch.randn((1, n, 8, 64), generator=gen, device="cuda").to(BF)
+    table = torch.zeros((1, 32768), dtype=torch.int32, device="cuda")
+    for length, want in ((2 ** 31 - 65536, v.double().mean((0, 1, 2, 3))), (2 ** 31 - 65535, None)):
+        out = torch.full(q.shape, 7.0, dtype=F32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table, kv_len=i32(length), status=status)
+        assert L.lin_state_read_status(status) == (0 if want is not None else L.LIN_ST_BAD_SEQLEN)
+        if want is None:
+            assert bool((out == 7.0).all())
+        else:
+            assert bool(((out - want).abs() <= want * 2.0 ** -6).all())
