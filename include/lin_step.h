@@ -89,12 +89,13 @@ LIN_API int lin_state_kv_append(const lin_kv_cache_t* cache, const lin_kv_append
  * and that page's tokens count as not seen.
  * Precision: scores, the softmax and the sums over values are fp32. bf16
  * caches multiply on tensor cores with exact bf16 operands and the weights in
- * two bf16 parts; their value sums are the tensor unit's, which cuts off below the
- * last place of fp32 with each 16 tokens it adds. For fp32 outputs the weights go in
- * three parts and the sums of 16 tokens are added with rounding. fp32 caches
- * multiply with every operand in two tf32 parts and add the products of 16 tokens,
- * and of 32 channels of a score, with rounding. Visible NaN, of any payload, gives
- * NaN; visible infinities may give NaN.
+ * two bf16 parts (three for fp32 outputs); fp32 caches multiply with every
+ * operand in two tf32 parts. The sums of 16 tokens, and for fp32 caches of 32
+ * channels of a score, are added with rounding; but bf16 outputs of more than 16
+ * rows (n_q * num_q_heads / num_kv_heads) leave the value sums to the tensor unit,
+ * which cuts off below the last place of fp32: 1e-4 of the outputs over 16,384
+ * tokens, where their own rounding is up to 3.9e-3. Visible NaN, of any payload,
+ * gives NaN; visible infinities may give NaN.
  * Results do not depend on timing: the same call gives the same bits.
  * Any batch of lengths loads the SMs evenly: the lengths are read on the device,
  * the batch's tokens are cut into equal ranges, and items that cross a border

@@ -218,3 +218,37 @@ def test_the_longest_request_and_one_token_more(n):
             assert bool((out == 7.0).all())
         else:
             assert bool(((out - want).abs() <= want * 2.0 ** -6).all())
+
+
+
+def shift_of_bf16_outputs(D, n, G, length):
+    """Mean of (output - correctly rounded output) / output for requests that share
+    one sequence, so that each stays in one piece. Values of one sign, channels of
+    different sizes, so that outputs lie anywhere between two bf16 values: what an
+    accumulation loses shows in full as outputs that round to the neighbour."""
+    B = 304
+    gen = torch.Generator(device="cuda").manual_seed(D + n)
+    k, v = (torch.randn((1, length // 64, 64, 1, D), generator=gen, device="cuda") for _ in range(2))
+    size = 2.0 ** torch.rand(D, generator=gen, device="cuda")
+    k, v = k.to(BF), ((v.abs() + 1) * size).to(BF)
+    q = torch.randn((B, n, G, D), generator=gen, device="cuda").to(BF)
+    out = torch.empty_like(q)
+    table = torch.arange(length // 64, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    L.lin_state_attn_decode(L.KVCache(1, length // 64, 64, 1, D, dtype=BF, k=k, v=v), layer=0, q=q, out=out,
+                            page_table=table, kv_len=torch.full((B,), length, dtype=torch.int32, device="cuda"))
+    hidden = torch.arange(length, device="cuda") > length - n + torch.arange(n, device="cuda")[:, None]
+    off = []
+    for r in range(0, B, 38):
+        s = torch.einsum("jhd,td->jht", q[r].double(), k.reshape(length, D).double()) * D ** -0.5
+        want = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1) @ v.reshape(length, D).double()
+        off.append(((out[r].double() - want.to(BF).double()) / want).mean())
+    return abs(float(torch.stack(off).mean()))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(1, 8), (2, 8)])
+def test_bf16_outputs_lose_nothing_over_a_long_piece(D, n, G):
+    """Up to 16 rows: sums that are rounded to nearest shift nothing, and weights
+    in two parts less than 2^-17; another 2^-17 for chance. (A sum that cut off with every
+    16 tokens took 2^-12 over half as many.)"""
+    assert shift_of_bf16_outputs(D, n, G, 1 << 18) < 2.0 ** -16
