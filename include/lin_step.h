@@ -92,10 +92,10 @@ LIN_API int lin_state_kv_append(const lin_kv_cache_t* cache, const lin_kv_append
  * two bf16 parts (three for fp32 outputs); fp32 caches multiply with every
  * operand in two tf32 parts. The sums of 16 tokens, and for fp32 caches of 32
  * channels of a score, are added with rounding; but bf16 outputs of more than 16
- * rows (n_q * num_q_heads / num_kv_heads) leave the value sums to the tensor unit,
- * which cuts off below the last place of fp32: 1e-4 of the outputs over 16,384
- * tokens, where their own rounding is up to 3.9e-3. Visible NaN, of any payload,
- * gives NaN; visible infinities may give NaN.
+ * rows (n_q * num_q_heads / num_kv_heads) leave the value sums of up to 32,768
+ * tokens to the tensor unit, which cuts off below the last place of fp32: less
+ * than 2^-11 of the sum p |v|, where their own rounding is up to 2^-8. Visible NaN,
+ * of any payload, gives NaN; visible infinities may give NaN.
  * Results do not depend on timing: the same call gives the same bits.
  * Any batch of lengths loads the SMs evenly: the lengths are read on the device,
  * the batch's tokens are cut into equal ranges, and items that cross a border

@@ -30,10 +30,13 @@
 // overlap. The weights go in PT = 2 bf16 parts (2^-16 together), each a product of
 // its own.
 //
-// The value sums of a piece stay in the unit, which cuts off below the last place
-// of what it adds to: with 128 rows that takes 1e-4 off the outputs over 16,384
-// tokens of one piece and 8.6e-4 over 131,072, where a bf16 output is rounded by up
-// to 3.9e-3. fp32 outputs take attn_kernel.cuh, which adds with rounding.
+// The value sums stay in the unit, which cuts off below the last place of what it
+// adds to: with 128 rows that takes 1e-4 off the outputs over 16,384 tokens and 8.6e-4
+// over 131,072, where a bf16 output is rounded by up to 3.9e-3. So a piece goes in
+// runs of up to kRun units, whose sums are joined in fp32 with rounding, and the loss
+// stays below 2^-11 (4,096 products of 16 tokens) at any length. (48 requests of
+// 60k-131k tokens, 32 rows of 128: 860 us in runs, 874 at a stretch.)
+// fp32 outputs take attn_kernel.cuh, which adds every 16 tokens with rounding.
 #pragma once
 
 #include "attn_common.cuh"
@@ -68,6 +71,7 @@ struct UCfg {
 };
 
 constexpr uint32_t kUmmaWaitTries = 1u << 26;
+constexpr int kRun = 512;  // most units of a run
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
@@ -136,14 +140,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
   float* merge = reinterpret_cast<float*>(smem);
   float2* merge_ml = reinterpret_cast<float2*>(merge + 128 * C::PITCH);
 
-  // the next unit of the ring and its phase, and tiles and pieces so far
+  // the next unit of the ring and its phase, and tiles and runs so far
   int slot = 0;
-  uint32_t phase = 0, piece = 0, tile0 = 0;
+  uint32_t phase = 0, run = 0, tile0 = 0;
   auto next = [](int& s, uint32_t& ph) {
     if (++s == U) s = 0, ph ^= 1;
   };
   // A thread whose wait runs out waits for nothing more and goes on to the
-  // piece's end, where all leave: every barrier is still met.
+  // run's end, where all leave: every barrier is still met.
   bool gone = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (gone || umma::mbar_wait(bar, parity, kUmmaWaitTries)) return;
@@ -152,10 +156,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
     report(a.status, LIN_ST_TIMEOUT);
   };
 
+  int at = w.t0;  // the run's first unit
   while (true) {
-    const int t1 = walk_until(p, w), r = w.r;
+    const int t1 = walk_until(p, w), end = min(t1, at + kRun), r = w.r;
     const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * RP;
-    const int key_begin = w.t0 * kUnit, key_end = t1 == w.u ? w.len : t1 * kUnit;
+    const int key_begin = at * kUnit, key_end = end == w.u ? w.len : end * kUnit;
     const int base = w.len - a.n_q;  // tokens that every query sees
     const int tiles = (key_end - key_begin + TK - 1) / TK;
 
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
         for (int i = 0; i < 32; ++i) z[i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < D; i += 32) umma::tmem_st32(t_o + t_lane + i, z);
-        if (piece == 0) {  // other copies' tokens keep weight 0
+        if (run == 0) {  // other copies' tokens keep weight 0
 #pragma unroll 1
           for (int i = 0; i < NB * C::PCOLS; i += 32) umma::tmem_st32(t_p + t_lane + i, z);
         }
@@ -419,13 +424,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
       // Descriptors of the buffers' starts; a step within one is a sum to the
       // address field, which holds 18-bit shared-memory addresses / 16.
       const bool scores = warp == 8;
-      if (piece == 0 && !scores) next(slot, phase);  // K of tile t is unit 2 t, V unit 2 t + 1
+      if (run == 0 && !scores) next(slot, phase);  // K of tile t is unit 2 t, V unit 2 t + 1
       if (scores) {
         constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
         const uint64_t q_desc = umma::desc_kmajor(umma::smem_u32(qbuf), 128, 0);
         const uint64_t k_desc = umma::desc_kmajor(umma::smem_u32(smem), TK, 0);
         auto step = [](int rows, int k) { return uint64_t(((k >> 6) * rows * 128 + (k & 63) * 2) >> 4); };
-        wait(&b_q, piece & 1);
+        wait(&b_q, run & 1);
         for (int i = 0; i < tiles; ++i) {
           const uint32_t gt = tile0 + i;
           wait(&b_full[slot], phase);
@@ -493,10 +498,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
       w.split.x = -1;
       break;
     }
-    finish_piece<D, C::COPIES, RP, NT, C::PITCH>(p, w, t1, merge, merge_ml, s_bad);
+    finish_piece<D, C::COPIES, RP, NT, C::PITCH>(p, w, t1, merge, merge_ml, s_bad, at == w.t0, end == t1);
     tile0 += tiles;
-    ++piece;
-    if (!walk_next(p, w, t1)) break;
+    ++run;
+    at = end;
+    if (end == t1) {
+      if (!walk_next(p, w, t1)) break;
+      at = w.t0;
+    }
     umma::fence_smem_to_async();
     __syncthreads();  // the join is read before the ring is filled again
   }

@@ -252,3 +252,47 @@ def test_bf16_outputs_lose_nothing_over_a_long_piece(D, n, G):
     in two parts less than 2^-17; another 2^-17 for chance. (A sum that cut off with every
     16 tokens took 2^-12 over half as many.)"""
     assert shift_of_bf16_outputs(D, n, G, 1 << 18) < 2.0 ** -16
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(4, 8), (8, 8), (8, 16)])
+def test_bf16_outputs_of_many_rows_lose_little_over_a_long_piece(D, n, G):
+    """More than 16 rows: a run of 32,768 tokens is 4,096 products of 16 tokens, two to
+    each, that lose a unit of the sum's last place at most: 4,096 x 2^-23 = 2^-11,
+    whatever the length. (Over 262,144 tokens at a stretch 128 rows lost 2^-9.)"""
+    assert shift_of_bf16_outputs(D, n, G, 1 << 18) < 2.0 ** -11
+
+
+@pytest.mark.parametrize("D,n,G", [(64, 8, 8), (128, 4, 8), (256, 16, 8)])
+def test_runs_of_a_long_piece_beside_short_requests(D, n, G):
+    """Whole items of several runs, items that begin and end in a range, and
+    requests without work, against 64 bits, with the bound of the other
+    tests; a bad tree is left out although its runs leave sums."""
+    long, ps = 70001, 64
+    pages = -(-long // ps)
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    k, v = (torch.randn((1, pages, ps, 1, D), generator=gen, device="cuda").to(BF) for _ in range(2))
+    lens = [long, 3, 32768, 32769 + n, -1, 0, 65536, 40000] + [long] * 300
+    bad = {7, 200}
+    q = torch.randn((len(lens), n, G, D), generator=gen, device="cuda").to(BF)
+    out = torch.full_like(q, 7.0)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(len(lens), -1).contiguous()
+    parent = torch.arange(-1, n - 1, dtype=torch.int32, device="cuda").expand(len(lens), -1).contiguous()
+    for r in bad:
+        parent[r, 1] = 5 if n > 5 else 1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L.lin_state_attn_decode(L.KVCache(1, pages, ps, 1, D, dtype=BF, k=k, v=v), layer=0, q=q, out=out, page_table=table,
+                            kv_len=torch.tensor(lens, dtype=torch.int32, device="cuda"), parent=parent, status=status)
+    assert L.lin_state_read_status(status) == L.LIN_ST_BAD_TREE
+    for r in [0, 1, 2, 3, 4, 5, 6, 7, 8, 100, 200, 307]:
+        if lens[r] < 0 or r in bad:
+            assert bool((out[r] == 7.0).all())
+            continue
+        kk, vv = (t.reshape(-1, D)[:lens[r]].double() for t in (k, v))
+        s = torch.einsum("jhd,td->jht", q[r].double(), kk) * D ** -0.5
+        hidden = torch.arange(lens[r], device="cuda") > lens[r] - n + torch.arange(n, device="cuda")[:, None]
+        p = torch.softmax(s.masked_fill(hidden[:, None], -torch.inf), -1).nan_to_num(0.0)
+        want, reach = p @ vv, p @ vv.abs()
+        spread = float((q[r].double().abs().reshape(-1, D) @ kk.abs().T).max()) * D ** -0.5 if lens[r] else 0.0
+        inner = 2 * spread * (D + 16) * 2.0 ** -24 + (lens[r] + 16) * 2.0 ** -24 + 2.0 ** -16
+        assert bool(((out[r].double() - want).abs() <= 2.0 ** -8 * want.abs() + reach * inner).all()), r
