@@ -240,9 +240,12 @@ struct Shape {
   bool umma;
   int block_rows, ctas, item_cost;
   // Items of up to so many units stay whole, as the join takes longer than their
-  // tokens one after another (one request of 256 tokens, bf16: 8.9 to 7.5 us; of
-  // 512: 8.9 against 10.4; fp32 heads of 256, 128 tokens: 13.8 to 12.9, 256: 15.8
-  // against 19.5).
+  // tokens one after another (one token, 1 and 256 requests of 128-256 tokens: bf16
+  // heads of 64 6.4 and 10.2 us against 7.9 and 14.5, of 256 9.7 and 38.3 against 10.5
+  // and 38.9; one request of 512 tokens 10.4 against 8.9; fp32, 64-128 tokens: heads of
+  // 64 6.9 and 16.0 against 7.6 and 17.9, of 256 12.1 and 48.0 against 12.6 and 50.0,
+  // 256 tokens 19.5 against 15.8). What the page table allows decides, as the lengths
+  // are the device's: short requests with a wide table are split.
   int whole_units;
 };
 
@@ -252,19 +255,33 @@ int ctas_of(bool bf16, int rt) {
   return rt == 1 ? Cfg<D, LIN_F32, 1>::CTAS : rt == 2 ? Cfg<D, LIN_F32, 2>::CTAS : Cfg<D, LIN_F32, 4>::CTAS;
 }
 
+int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
+  return sms > 0 ? sms : 152;  // no device: the size of a GB300
+}
+
 // bf16 caches: up to 16 rows per (request, kv head) on warp-level MMA, more on
-// tcgen05 in blocks of 32, 64 or 128; but 17 to 32 rows of requests of up to 256
-// tokens as two blocks of 16, for an item's start and end take longer there than
-// reading it twice (4 drafts of a group of 8: 1 request
-// of 64 tokens 8.6 to 6.3 us, 256 requests of up to 256 tokens 41 to 38 us). fp32
-// caches: warp-level MMA in blocks of 16, 32 or 64. So do fp32 outputs of bf16 caches,
-// whose long sums tcgen05 does not round (64 requests of 500-8,000 tokens, heads
-// of 128, 32, 64 and 128 rows: 81, 140 and 260 us, where it took 76, 102 and 170;
-// heads of 64, 32 rows: 86 against 135).
-Shape shape_of(const lin_kv_cache_t& c, int rows, int64_t units, int out_dtype) {
+// tcgen05 in blocks of 32, 64 or 128 (64 requests of 500-8,000 tokens, 2 kv heads, 64
+// and 128 rows: heads of 64 65 and 135 us against 74 and 131 on warp-level MMA,
+// of 128 92 and 135 against 118 and 218, of 256 126 and 179 against 245 and 469; 32
+// rows: 47, 69 and 107 against 45, 69 and 133).
+// But 17 to 32 rows of requests of up to 256 tokens go as two blocks of 16, for an
+// item's start and end take longer there than reading it twice: 4 drafts of a group
+// of 8, 2 kv heads, 1 and 256 requests of 128-256 tokens: heads of 64 6.8 and 17.8 us
+// against 8.4 and 27.6, of 128 8.7 and 38.6 against 10.8 and 42.4. Heads of 256 leave
+// room for one CTA to an SM, so there only while each block has an SM to itself (32
+// requests 11.8 us against 14.9; 64 21.0 against 16.8; 256 71.0 against 62.6).
+// fp32 caches: warp-level MMA in blocks of 16, 32 or 64. So do fp32 outputs of bf16
+// caches, whose long sums tcgen05 does not round (64 requests of 500-8,000 tokens, 2
+// kv heads of 128, 32, 64 and 128 rows: 81, 140 and 260 us, where it took 76, 102
+// and 170; 4 of 64, 32 rows: 86 against 135).
+int batch_in_two(const lin_kv_cache_t& c) { return sm_count() / 2 / c.num_kv_heads; }  // heads of 256
+Shape shape_of(const lin_kv_cache_t& c, int batch, int rows, int64_t units, int out_dtype) {
   const bool b = c.dtype == LIN_BF16;
   const bool bb = b && out_dtype == LIN_BF16;
-  if (bb && rows > 16 && (rows > 32 || units > kShortUnits)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
+  const bool in_two = units <= kShortUnits && (c.head_dim < 256 || batch <= batch_in_two(c));
+  if (bb && rows > 16 && (rows > 32 || !in_two)) return {true, rows <= 32 ? 32 : rows <= 64 ? 64 : 128, 1, 7, 4};
   const int rt = rows <= 16 || bb ? 1 : rows <= 32 ? 2 : 4;
   return {false, 16 * rt, c.head_dim == 64 ? ctas_of<64>(b, rt) : c.head_dim == 128 ? ctas_of<128>(b, rt) : ctas_of<256>(b, rt), b ? 3 : 2, b ? 4 : 2};
 }
@@ -272,13 +289,10 @@ Shape shape_of(const lin_kv_cache_t& c, int rows, int64_t units, int out_dtype) 
 // CTAs of the main kernel: what is resident at once, or one per unit where the
 // longest request allowed would give fewer.
 int grid_of(const lin_kv_cache_t& c, int batch, int rows, int64_t units, const Shape& f) {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
-  if (sms <= 0) sms = 152;  // no device: the size of a GB300
   const int64_t blocks = (rows + f.block_rows - 1) / f.block_rows;
   const int64_t items = int64_t(batch) * c.num_kv_heads * blocks;
   const int64_t most = units > 1 && items < INT32_MAX ? items * units : items;
-  const int64_t full = int64_t(sms) * f.ctas < kMaxRanges ? int64_t(sms) * f.ctas : kMaxRanges;
+  const int64_t sms = sm_count(), full = sms * f.ctas < kMaxRanges ? sms * f.ctas : kMaxRanges;
   return static_cast<int>(most < full && most > 0 ? most : full);
 }
 
@@ -305,7 +319,7 @@ void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
 size_t attn_need(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
   const int rows = attn::rows_of(c, a);
   const int64_t units = attn::units_most(c, a);
-  const attn::Shape f = attn::shape_of(c, rows, units, a.out_dtype);
+  const attn::Shape f = attn::shape_of(c, a.batch, rows, units, a.out_dtype);
   return attn::bytes_of(c, f, attn::grid_of(c, a.batch, rows, units, f));
 }
 
@@ -317,14 +331,15 @@ size_t attn_workspace(const lin_kv_cache_t& c, const lin_attn_args_t& a) {
   const int64_t units = attn::units_most(c, a);
   size_t most = 0;
   for (const int out : {LIN_BF16, LIN_F32})
-    for (const int r : {16, 32, 64, rows})
-      for (const int64_t u : {int64_t(attn::kShortUnits), units}) {
-        const int x = r < rows ? r : rows;
-        const int64_t y = u < units ? u : units;
-        const attn::Shape f = attn::shape_of(c, x, y, out);
-        const size_t n = attn::bytes_of(c, f, attn::grid_of(c, a.batch, x, y, f));
-        if (n > most) most = n;
-      }
+    for (const int b : {attn::batch_in_two(c), a.batch})
+      for (const int r : {16, 32, 64, rows})
+        for (const int64_t u : {int64_t(attn::kShortUnits), units}) {
+          const int x = b < a.batch ? b : a.batch, y = r < rows ? r : rows;
+          const int64_t z = u < units ? u : units;
+          const attn::Shape f = attn::shape_of(c, x, y, z, out);
+          const size_t n = attn::bytes_of(c, f, attn::grid_of(c, x, y, z, f));
+          if (n > most) most = n;
+        }
   return most;
 }
 
@@ -335,7 +350,7 @@ cudaError_t launch_attn_decode(const lin_kv_cache_t& c, const lin_attn_args_t& a
   p.group = a.num_q_heads / c.num_kv_heads;
   p.rows = attn::rows_of(c, a);
   const int64_t units = attn::units_most(c, a);
-  const attn::Shape f = attn::shape_of(c, p.rows, units, a.out_dtype);
+  const attn::Shape f = attn::shape_of(c, a.batch, p.rows, units, a.out_dtype);
   const int grid = attn::grid_of(c, a.batch, p.rows, units, f);
   p.grid = grid;
   p.block_rows = f.block_rows;

@@ -2,10 +2,12 @@
 which nothing is attended, NaN and infinities that are visible, long sums,
 workspaces kept for a largest call."""
 
+import numpy as np
 import pytest
 import torch
 
 import linear_attention_state_chunked_gb300 as L
+from tests.test_gpu_step import check_attn, make_cache, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -296,3 +298,19 @@ def test_runs_of_a_long_piece_beside_short_requests(D, n, G):
         spread = float((q[r].double().abs().reshape(-1, D) @ kk.abs().T).max()) * D ** -0.5 if lens[r] else 0.0
         inner = 2 * spread * (D + 16) * 2.0 ** -24 + (lens[r] + 16) * 2.0 ** -24 + 2.0 ** -16
         assert bool(((out[r].double() - want).abs() <= 2.0 ** -8 * want.abs() + reach * inner).all()), r
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B", [20, 38, 39, 100])
+def test_short_requests_of_few_rows_in_any_batch(D, B):
+    """17 to 32 rows over at most 256 tokens, on both sides of the batch from which
+    heads of 256 take another kernel; the last requests as in a batch of their own."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(-1, 241, B)]
+    cache, table, gen = make_cache(lens, 16, 2, D, BF, seed=B)
+    q = queries(B, 3, 16, 2, D, BF, gen)
+    assert table.shape[1] * 16 <= 256
+    out = check_attn(cache, table, q, lens, BF)
+    few = check_attn(cache, table[-4:].contiguous(), q[-4:], lens[-4:], BF)
+    seen = torch.tensor(lens[-4:], device="cuda") >= 0
+    assert bool((out[-4:][seen].float() - few[seen].float()).abs().max() < 2.0 ** -6)
