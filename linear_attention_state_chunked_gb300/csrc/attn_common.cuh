@@ -220,16 +220,15 @@ __device__ __forceinline__ void draft_sets(const Plan& p, int r, uint32_t (&see)
 }
 
 // Joins the KG value sums [KG][ROWS][PITCH >= D] and (m, sum) [KG][ROWS] of a piece in
-// shared memory and writes the outputs of a whole item, or the piece's part.
-// A piece may come in runs: `first` and `last` tell where this one lies, and between
-// them the piece's part holds the sums so far, in the same threads' hands each time.
+// shared memory and writes the outputs of a whole item, or the piece's part (or,
+// with t1 within the piece, what is summed so far, which carry_in takes up).
 // All NT threads.
 template <int D, int KG, int ROWS, int NT, int PITCH = D>
 __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t1, const float* merge,
-                                             const float2* merge_ml, bool bad, bool first = true, bool last = true) {
+                                             const float2* merge_ml, bool bad) {
   const lin_attn_args_t& a = p.a;
   const int hk = head_of(p, w.it), row0 = (w.it - hk * p.row_blocks) * ROWS;
-  const bool whole = last && w.t0 == 0 && t1 == w.u;
+  const bool whole = w.t0 == 0 && t1 == w.u;
   const int64_t part = 2 * int64_t(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
   constexpr int LANES = D / 4 < 32 ? D / 4 : 32;  // threads of a row, so many steps of 4 channels
   constexpr int STEPS = D / 4 / LANES, AT = NT / LANES;
@@ -264,22 +263,6 @@ __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t
         v[x].z = fmaf(f, y[k][x].z, v[x].z), v[x].w = fmaf(f, y[k][x].w, v[x].w);
       }
     }
-    if (!first) {
-      const float2 was = p.part_ml[part * ROWS + row];
-      const float now = top;
-      top = fmaxf(now, was.x);
-      const float f = sum == 0.0f ? 0.0f : now == top ? 1.0f : exp2_fast(now - top);
-      const float g = was.y == 0.0f ? 0.0f : was.x == top ? 1.0f : exp2_fast(was.x - top);
-      sum = fmaf(g, was.y, f * sum);
-#pragma unroll
-      for (int x = 0; x < STEPS; ++x) {
-        const float4 y = *reinterpret_cast<const float4*>(p.part + (part * ROWS + row) * D + (x * LANES + lane) * 4);
-        v[x].x = fmaf(g, y.x, f * v[x].x), v[x].y = fmaf(g, y.y, f * v[x].y);
-        v[x].z = fmaf(g, y.z, f * v[x].z), v[x].w = fmaf(g, y.w, f * v[x].w);
-      }
-      // every lane of the row has read part_ml
-      __syncwarp(LANES == 32 ? ~0u : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1)));
-    }
     const float scale = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int j = query_of(p, q);
     const int64_t out = ((int64_t(w.r) * a.n_q + j) * a.num_q_heads + hk * p.group + q - j * p.group) * D;
@@ -299,7 +282,33 @@ __device__ __forceinline__ void finish_piece(const Plan& p, const Walk& w, int t
             make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
       }
     }
-    if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, last && bad ? kLeftOut : sum);
+    if (!whole && lane == 0) p.part_ml[part * ROWS + row] = make_float2(top, bad ? kLeftOut : sum);
+  }
+}
+
+// Joins the piece's part, the sums so far, into the first of the value sums that
+// finish_piece is to join. All NT threads, each with the channels that it wrote.
+template <int D, int ROWS, int NT, int PITCH>
+__device__ __forceinline__ void carry_in(const Plan& p, const Walk& w, float* merge, float2* merge_ml) {
+  const int64_t part = 2 * int64_t(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+  constexpr int LANES = D / 4 < 32 ? D / 4 : 32, STEPS = D / 4 / LANES;
+  const int lane = threadIdx.x % LANES, row0 = (w.it - head_of(p, w.it) * p.row_blocks) * ROWS;
+#pragma unroll 1
+  for (int row = threadIdx.x / LANES; row < ROWS && row0 + row < p.rows; row += NT / LANES) {
+    const float2 now = merge_ml[row], was = p.part_ml[part * ROWS + row];
+    const float top = fmaxf(now.x, was.x);
+    const float f = now.y == 0.0f ? 0.0f : now.x == top ? 1.0f : exp2_fast(now.x - top);
+    const float g = was.y == 0.0f ? 0.0f : was.x == top ? 1.0f : exp2_fast(was.x - top);
+#pragma unroll
+    for (int x = 0; x < STEPS; ++x) {
+      float4& v = *reinterpret_cast<float4*>(merge + row * PITCH + (x * LANES + lane) * 4);
+      const float4 y = *reinterpret_cast<const float4*>(p.part + (part * ROWS + row) * D + (x * LANES + lane) * 4);
+      v.x = fmaf(g, y.x, f * v.x), v.y = fmaf(g, y.y, f * v.y);
+      v.z = fmaf(g, y.z, f * v.z), v.w = fmaf(g, y.w, f * v.w);
+    }
+    // every lane of the row has read its (m, sum)
+    __syncwarp(LANES == 32 ? ~0u : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1)));
+    if (lane == 0) merge_ml[row] = make_float2(top, fmaf(g, was.y, f * now.y));
   }
 }
 

@@ -35,7 +35,7 @@
 // over 131,072, where a bf16 output is rounded by up to 3.9e-3. So a piece goes in
 // runs of up to kRun units, whose sums are joined in fp32 with rounding, and the loss
 // stays below 2^-11 (4,096 products of 16 tokens) at any length. (48 requests of
-// 60k-131k tokens, 32 rows of 128: 860 us in runs, 874 at a stretch.)
+// 60k-131k tokens, 32 rows of 128: 886 us in runs, 876 at a stretch.)
 // fp32 outputs take attn_kernel.cuh, which adds every 16 tokens with rounding.
 #pragma once
 
@@ -498,7 +498,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) attn_umma_kernel(const Plan p) 
       w.split.x = -1;
       break;
     }
-    finish_piece<D, C::COPIES, RP, NT, C::PITCH>(p, w, t1, merge, merge_ml, s_bad, at == w.t0, end == t1);
+    if (at > w.t0) {
+      carry_in<D, RP, NT, C::PITCH>(p, w, merge, merge_ml);
+      __syncthreads();
+    }
+    finish_piece<D, C::COPIES, RP, NT, C::PITCH>(p, w, end, merge, merge_ml, s_bad && end == t1);
     tile0 += tiles;
     ++run;
     at = end;
