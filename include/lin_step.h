@@ -95,7 +95,8 @@ LIN_API int lin_state_kv_append(const lin_kv_cache_t* cache, const lin_kv_append
  * rows (n_q * num_q_heads / num_kv_heads) leave the value sums of up to 32,768
  * tokens to the tensor unit, which cuts off below the last place of fp32: less
  * than 2^-11 of the sum p |v|, where their own rounding is up to 2^-8. Visible NaN,
- * of any payload, gives NaN; visible infinities may give NaN.
+ * of any payload, gives NaN; visible infinities may give NaN, and values from
+ * 2^120 on infinities, as weights relative to a lagging maximum reach 2^8.
  * Results do not depend on timing: the same call gives the same bits.
  * Any batch of lengths loads the SMs evenly: the lengths are read on the device,
  * the batch's tokens are cut into equal ranges, and items that cross a border
@@ -134,7 +135,7 @@ LIN_API int lin_state_attn_decode(const lin_kv_cache_t* cache, const lin_attn_ar
  *   h = residual + scale * scale_w[c] * t (residual 0 and scale_w 1 when NULL)
  *   y = h * rsqrt(mean over the row of h^2 + eps) * w_pre[c]
  * in fp32 throughout, rounded once where h_out and y are stored (y is made
- * from the unrounded h). group divides channels: head_v for the output norm
+ * from the unrounded h); the gate's sigmoid is 0 below -87.3. group divides channels: head_v for the output norm
  * of a linear-attention layer, channels for a norm after a block.
  * x is x_dtype; gate, the weights and y io_dtype; residual and h_out h_dtype.
  * Row strides in elements, at least `channels`; rows of any alignment do,

@@ -14,15 +14,15 @@ constexpr int kShortUnits = 4;   // of a request: see shape_of
 
 // The item that begins in range c and goes on past it has the parts, in token
 // order, 2c + 1 and then 2c' of the ranges c' = c + 1, ... They are joined in that
-// order (RW warps of a row each take every RW-th), so the result does not depend
-// on timing.
+// order (where a row has kRowWarps warps, each takes every kRowWarps-th), so the result
+// does not depend on timing.
 //
 // Bound by the latency of dependent loads (split, sums, values). Many items, few
 // parts each: a block for every range, a warp per row, and most find no split. Few
 // items, many parts: a block for every item's row, which works out from the lengths
 // (while the main kernel runs) which ranges hold it, loads all sums at once and
 // the values by 16 warps (one request of 60,000 tokens, one kv head, 304 parts:
-// 24 us in all with a block for every range's row, 17 so).
+// 24 us in all with a block for every range's row, 18 so).
 struct Split {
   int parts, hk, rb;
   int64_t r;
@@ -234,7 +234,7 @@ cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int grid, int64_
 
 // Which kernel a call takes, the rows of its items and its CTAs per SM.
 // item_cost, in units of 64 tokens: an item's start and end take about 6 us of an
-// SM on tcgen05 against 0.8 us per unit, and 4 us of a CTA against 1.5 us per
+// SM on tcgen05 against 0.9 us per unit, and 4 us of a CTA against 1.5 us per
 // unit (two CTAs to an SM) on warp-level MMA.
 struct Shape {
   bool umma;
@@ -263,9 +263,9 @@ int sm_count() {
 
 // bf16 caches: up to 16 rows per (request, kv head) on warp-level MMA, more on
 // tcgen05 in blocks of 32, 64 or 128 (64 requests of 500-8,000 tokens, 2 kv heads, 64
-// and 128 rows: heads of 64 65 and 135 us against 74 and 131 on warp-level MMA,
-// of 128 92 and 135 against 118 and 218, of 256 126 and 179 against 245 and 469; 32
-// rows: 47, 69 and 107 against 45, 69 and 133).
+// and 128 rows: heads of 64 72 and 129 us against 74 and 131 on warp-level MMA, of
+// 128 85 and 140 against 118 and 218, of 256 125 and 178 against 245 and 469; 32 rows:
+// 48, 70 and 106 against 45, 69 and 133).
 // But 17 to 32 rows of requests of up to 256 tokens go as two blocks of 16, for an
 // item's start and end take longer there than reading it twice: 4 drafts of a group
 // of 8, 2 kv heads, 1 and 256 requests of 128-256 tokens: heads of 64 6.8 and 17.8 us

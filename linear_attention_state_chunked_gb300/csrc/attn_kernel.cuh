@@ -13,10 +13,14 @@
 // key-value head are read for 4 head_dim flops a row. The tensor work is
 // warp-level MMA on 16 rows, which is what a decode step has, and each warp keeps
 // its rows' whole softmax state in registers. 256 requests of 1k-16k tokens, 8
-// query heads to a kv head of 128: 334 us, 0.98 of the measured copy bandwidth.
-// fp32 is bound by the tensor unit from two row tiles on: three tf32 products to
-// an fp32 one, 8 cycles each per scheduler (trees of 8 drafts, 24 rows: 60 us for
-// a floor of 20).
+// query heads to a kv head of 128: 328-336 us, 0.98 of the measured copy bandwidth.
+// fp32 has three tf32 products to an fp32 one, and no unit is full: in trees of 8
+// drafts, 24 rows, heads of 64 (32 requests of 8-4,000 tokens: 62 us for a floor of
+// 20) the tensor pipe is busy 39% of the time, the schedulers issue 56%, HBM runs at
+// 30%. A warp owns one row tile, so with RT tiles every key and value is loaded from
+// shared memory and split RT times. 64 requests of 500-8,000 tokens, 2 kv heads, 8, 32
+// and 64 rows: heads of 64 63, 114 and 211 us for a floor of 43, of 128 125, 211 and
+// 417 for 85, of 256 250, 466 and 765 for 171.
 //
 // Inside a CTA a group of RT x DS warps (one per 16 rows, and per part of the
 // values) shares a ring of S slots of 16 tokens' K and V, filled by 16-byte
@@ -561,7 +565,7 @@ cudaError_t launch_main(const Plan& p, int grid, cudaStream_t s) {
 
 template <int D, int DT>
 cudaError_t launch_rows(const Plan& p, int row_tiles, int grid, cudaStream_t s) {
-  if constexpr (DT == LIN_BF16) {  // bf16 outputs of more rows take the kernels of attn_umma.cuh
+  if constexpr (DT == LIN_BF16) {  // bf16 outputs with larger blocks take the kernels of attn_umma.cuh
     return row_tiles == 4   ? launch_main<Cfg<D, DT, 4>, 3>(p, grid, s)
            : row_tiles == 2 ? launch_main<Cfg<D, DT, 2>, 3>(p, grid, s)
            : p.a.out_dtype == LIN_F32 ? launch_main<Cfg<D, DT, 1>, 3>(p, grid, s)

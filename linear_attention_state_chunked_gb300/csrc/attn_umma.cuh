@@ -2,13 +2,10 @@
 // cache, bf16 outputs: a verify of several drafts, or many query heads to a
 // key-value head. The products run on the 5th-generation tensor cores.
 //
-// What bounds it is HBM, as for few rows (attn_kernel.cuh); but warp-level MMA
-// of 16 rows, one m16n8k16 in 8 cycles per scheduler, takes as long as the loads
-// at about 24 rows (64 requests, 4 drafts of a group of 8: 81 us against 71 us
-// here; 8 drafts 132 against 86; heads of 256, 4 drafts 161 against 105), and
-// tcgen05 some twentieth of that. So its M = 128 need not
-// be filled with work: the RP (32, 64 or 128) rows are repeated 128 / RP times
-// along M, and copy c only ever looks at the c-th share of a tile's tokens:
+// Warp-level MMA of 16 rows, one m16n8k16 in 8 cycles per scheduler, takes as long
+// as the loads at about 24 rows, and tcgen05 some twentieth of that. So its M = 128
+// need not be filled with work: the RP (32, 64 or 128) rows are repeated 128 / RP
+// times along M, and copy c only ever looks at the c-th share of a tile's tokens:
 //   S  = Q K^T      [128 lanes][TK tokens], every lane against every token;
 //   P               lane of copy c: weights of its share, 0 elsewhere (the zero
 //                   blocks are written once);
@@ -17,10 +14,14 @@
 // between threads, and the four softmax warps share the tile's tokens evenly.
 // The copies are joined as the pieces of a split are.
 //
-// Per 64 tokens and SM: 0.80 us for 32 rows of 128 (floor 0.735), 1.40 for 32 rows
-// of 256 (1.47); 1.0 and 1.5 us for 64 and 128 rows of 128, where a thread's 32 and
-// 64 weights of a tile take longer than its loads. An item's start and end take 5-6
-// us, which the split counts (Plan::item_cost).
+// What bounds it: in the steady state HBM with 32 rows (0.88 us per 64 tokens and SM
+// with heads of 128, floor 0.735; 1.38 of 256, floor 1.47), the softmax warps with
+// more (1.00 and 1.74 us for 64 and 128 rows of 128; 0.89 for 64 of 64, floor 0.37),
+// where a thread's 32 and 64 weights of a tile take longer than its loads; and in each
+// item its start and end, with no loads in flight, about 6 us with 32 rows of 128, 9 of
+// 256, 12 with 128 rows, which the split counts (Plan::item_cost). 64 requests of
+// 500-8,000 tokens, 2 kv heads, 32, 64 and 128 rows: heads of 64 48, 72 and 129 us for a
+// floor of 21, of 128 70, 85 and 140 for 43, of 256 106, 125 and 178 for 85.
 //
 // Roles: warps 0-3 softmax (thread = TMEM lane), 4-7 load, 8 issues Q K^T, 9
 // issues P V (one warp for both would make each wait for the other's operands).

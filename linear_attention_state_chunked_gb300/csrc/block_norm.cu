@@ -15,6 +15,10 @@
 // 32,768 rows of 32 x 128 channels, fp32 in, gate and output bf16: 171 us, 0.93 of
 // the measured copy bandwidth; 4,097 rows of 1,533 (shifted): 15.5 us, by single
 // channels 27.9; one row of 4096: 2.8 us, the launch.
+// Far from that bound: single channels of rows of more than 4096, 32 to a thread, which
+// spill (4,096 rows of 6,000 in groups of 1,500, bf16: 920 us for a floor of 29), and
+// rows of more than 16,384 channels, 8 vectors to a thread (1,024 rows of 20,480:
+// 74 us for 25).
 
 #include "common.cuh"
 #include "step_internal.h"
@@ -110,7 +114,8 @@ __device__ __forceinline__ float row_sum(float v, float* part, int tpr, int tx) 
 
 // 1 / (1 + 2^(-x log2 e)) in four instructions (the gate alone would else bound a
 // long prompt's call by its instructions): off by about (|x| + 4) 2^-24 of itself,
-// from the exponent's product; 0 where the power overflows.
+// from the exponent's product; 0 below x = -87.3, where it would be less than the
+// smallest normal number (and SiLU, 1e-36 and less, 0 with it).
 __device__ __forceinline__ float sigmoid(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
