@@ -314,3 +314,35 @@ def test_short_requests_of_few_rows_in_any_batch(D, B):
     few = check_attn(cache, table[-4:].contiguous(), q[-4:], lens[-4:], BF)
     seen = torch.tensor(lens[-4:], device="cuda") >= 0
     assert bool((out[-4:][seen].float() - few[seen].float()).abs().max() < 2.0 ** -6)
+
+
+@pytest.mark.parametrize("dtype,n,G", [(BF, 2, 4), (BF, 8, 8), (F32, 4, 8)])
+@pytest.mark.parametrize("B", [3, 70])
+def test_a_split_request_that_is_left_out(dtype, n, G, B):
+    """A bad tree and a length past the table in requests that are cut over several
+    ranges, few of many parts and many of few: their outputs stay as they are, and the
+    other requests' are those of a batch without fault, bit for bit."""
+    pages, ps = 100, 64
+    gen = torch.Generator(device="cuda").manual_seed(B + n)
+    k, v = (torch.randn((1, pages, ps, 1, 64), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    cache = L.KVCache(1, pages, ps, 1, 64, dtype=dtype, k=k, v=v)
+    q = torch.randn((B, n, G, 64), generator=gen, device="cuda").to(dtype)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+    length = torch.full((B,), pages * ps - 7, dtype=torch.int32, device="cuda")
+    length[2] = -1
+    tree = torch.arange(-1, n - 1, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+
+    def attend(length, tree, status_want):
+        out = torch.full_like(q, 7.0)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        L.lin_state_attn_decode(cache, layer=0, q=q, out=out, page_table=table, kv_len=length, parent=tree, status=status)
+        assert L.lin_state_read_status(status) == status_want
+        return out
+
+    want = attend(length, tree, 0)
+    assert bool((want[2] == 7.0).all())
+    bad_tree, too_long = tree.clone(), length.clone()
+    bad_tree[1, 1], too_long[2] = 1, pages * ps + 1
+    out = attend(too_long, bad_tree, L.LIN_ST_BAD_TREE | L.LIN_ST_BAD_SEQLEN)
+    want[1] = 7.0
+    assert torch.equal(out, want)
