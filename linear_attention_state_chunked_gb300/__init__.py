@@ -454,3 +454,10 @@ from .step import (  # noqa: E402,F401
     lin_state_kv_append)
 
 EXPORTED += STEP_EXPORTED
+
+# ---- a prompt's full-attention layers (include/lin_prompt.h) ------------------
+from .prompt import (  # noqa: E402,F401
+    LIN_ST_NO_PAGES, PROMPT_EXPORTED, AttnChunkArgsT, KVPlanArgsT, RopeArgsT, lin_state_attn_chunk,
+    lin_state_attn_chunk_workspace, lin_state_kv_plan, lin_state_rope, rope_frequencies)
+
+EXPORTED += PROMPT_EXPORTED

@@ -19,10 +19,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblinstate.so")
 
-# step_api.cu holds api.cu, whose checks and error text it shares
-SOURCES = ["step_api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
+# prompt_api.cu holds step_api.cu and that api.cu, whose checks and error text they share
+SOURCES = ["prompt_api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
            "selftest.cu", "kv_cache.cu", "attn_decode.cu", "attn_d64.cu", "attn_d128.cu",
-           "attn_d256.cu", "attn_umma_d64.cu", "attn_umma_d128.cu", "attn_umma_d256.cu", "block_norm.cu"]
+           "attn_d256.cu", "attn_umma_d64.cu", "attn_umma_d128.cu", "attn_umma_d256.cu", "block_norm.cu",
+           "kv_plan.cu", "rope.cu", "chunk_attn.cu", "chunk_mma_d64.cu", "chunk_mma_d128.cu", "chunk_mma_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -44,8 +45,8 @@ def _newer(target: str, deps) -> bool:
 
 def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    hdrs += [os.path.join(ROOT, "include", f) for f in ("lin_state.h", "lin_step.h")]
-    hdrs.append(os.path.join(CSRC, "api.cu"))
+    hdrs += [os.path.join(ROOT, "include", f) for f in ("lin_state.h", "lin_step.h", "lin_prompt.h")]
+    hdrs += [os.path.join(CSRC, f) for f in ("api.cu", "step_api.cu")]
     return hdrs
 
 

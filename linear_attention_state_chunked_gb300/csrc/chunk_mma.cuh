@@ -1,0 +1,378 @@
+// Chunk attention on warp-level MMA: fp32 caches, and bf16 caches with fp32 outputs.
+//
+//   out = sum_t p_t v_t / sum_t p_t,  p_t = 2^(s_t - m),  s_t = scale log2(e) q.k_t
+//
+// over the tokens up to the query's own; one pass over tiles of TK keys with a running
+// maximum m and sum per row. A warp owns 16 rows (tokens x query heads of one kv head)
+// and keeps their softmax state and value sums in registers; K and V tiles come by
+// 16-byte asynchronous copies (pages may end anywhere) into a ring of three, swizzled so
+// that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
+// (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
+// so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
+#pragma once
+
+#include "attn_kernel.cuh"
+#include "chunk_common.cuh"
+
+namespace lin {
+namespace chunk {
+
+template <int D_, int DT_>
+struct MCfg {
+  static constexpr int D = D_, DT = DT_;
+  static constexpr bool BF = DT == LIN_BF16;
+  static constexpr int ES = BF ? 2 : 4, ROWB = D * ES;
+  static constexpr int WARPS = 4, NT = WARPS * 32, ROWS = WARPS * 16;
+  static constexpr int TK = ROWB >= 512 ? 16 : 32;
+  static constexpr int STAGES = 3, STAGE = 2 * TK * ROWB;
+  static constexpr int QB = ROWS * ROWB;
+  static constexpr int SMEM = STAGES * STAGE + QB;
+  static constexpr int FIT = 220 * 1024 / SMEM;
+  static constexpr int CTAS = FIT < 3 ? FIT : 3;
+};
+
+template <class C, int PT>
+__global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p) {
+  using namespace attn;
+  constexpr int D = C::D, TK = C::TK, NT = C::NT, ROWB = C::ROWB, CPR = ROWB / 16;
+  constexpr bool BF = C::BF;
+  constexpr int NB = TK / 8;  // key blocks of a tile
+  constexpr uint32_t ALL = TK == 32 ? ~0u : (1u << (TK & 31)) - 1u;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ WalkShared s_walk;
+  __shared__ Piece s_piece;
+  __shared__ uint32_t s_valid[4];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const lin_kv_cache_t& c = p.c;
+  const lin_attn_chunk_args_t& a = p.a;
+  Walk w;
+  if (!walk_begin<NT>(p, w, s_walk)) return;
+  const uint32_t ring = umma::smem_u32(smem), qs = ring + C::STAGES * C::STAGE;
+
+  while (true) {
+    __syncthreads();  // the last piece is done with shared memory
+    if (tid == 0) s_piece = walk_next(p, w);
+    __syncthreads();
+    const Piece x = s_piece;
+    if (x.r < 0) break;
+    const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + x.hk * c.head_stride;
+    const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
+    const int32_t* table = a.page_table + x.r * a.page_table_stride;
+
+    // lane l of every warp looks up key l % TK of a tile
+    int key = x.t0 * TK + (lane & (TK - 1));
+    int id = key < x.keys ? table[page_of(p, key)] : -1;
+    auto fill = [&](int tile, int stage) {
+      const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
+      if (key < x.keys && !live && tid < TK) report(a.status, LIN_ST_BAD_PAGE);
+      const int64_t off = live ? id * c.page_stride + (key - page_of(p, key) * c.page_size) * c.token_stride : 0;
+      const uint32_t valid = __ballot_sync(~0u, live) & ALL;
+      if (tid == 0) s_valid[tile & 3] = valid;
+      const uint32_t dst = ring + stage * C::STAGE;
+#pragma unroll
+      for (int i = 0; i < TK * CPR / NT; ++i) {
+        const int y = i * NT + tid, row = y / CPR, ch = y % CPR;
+        const int64_t o = __shfl_sync(~0u, off, row) + ch * 16;
+        const bool ok = (valid >> row) & 1u;
+        cp16(dst + chunk_at<ROWB>(row, ch), kb + o, ok);
+        cp16(dst + TK * ROWB + chunk_at<ROWB>(row, ch), vb + o, ok);
+      }
+      key += TK;
+      id = key < x.keys ? table[page_of(p, key)] : -1;
+    };
+
+    // ---- queries: row = token * bheads + head --------------------------------------
+    for (int y = tid; y < C::ROWS * CPR; y += NT) {
+      const int row = y / CPR, ch = y % CPR;
+      const int i = token_of(p, row), h = row - i * p.bheads;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (i < x.tokens && h < x.heads) {
+        v = *reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) + int64_t(x.row0 + i) * a.token_stride +
+                                            int64_t(x.head0 + h) * ROWB + ch * 16);
+        v.x ^= p.negate, v.y ^= p.negate, v.z ^= p.negate, v.w ^= p.negate;
+      }
+      *reinterpret_cast<uint4*>(smem + C::STAGES * C::STAGE + chunk_at<ROWB>(row, ch)) = v;
+    }
+    // tokens that this thread's two rows see
+    int sees[2];
+    bool mine[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int row = warp * 16 + g + 8 * k, i = token_of(p, row);
+      mine[k] = i < x.tokens && row - i * p.bheads < x.heads;
+      sees[k] = mine[k] ? max(0, x.pos + i + 1) : 0;
+    }
+    const int all_see = max(0, x.pos + 1);  // what every row of the item sees
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+
+    const int tiles = x.t1 - x.t0;
+    fill(x.t0, 0);
+    cp_commit();
+    if (tiles > 1) fill(x.t0 + 1, 1);
+    cp_commit();
+    int stage = 0;
+    for (int i = 0; i < tiles; ++i) {
+      const int tile = x.t0 + i, key0 = tile * TK;
+      cp_wait<1>();
+      __syncthreads();
+      if (i + 2 < tiles) fill(tile + 2, stage == 0 ? 2 : stage - 1);
+      cp_commit();
+      const uint32_t ks = ring + stage * C::STAGE, vs = ks + TK * ROWB;
+      if (++stage == C::STAGES) stage = 0;
+
+      // ---- scores ---------------------------------------------------------------
+      float s[NB][4];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.0f;
+      if constexpr (BF) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+          uint32_t qa[4];
+          ldsm4(qa, qs + chunk_at<ROWB>(warp * 16 + (lane & 15), 2 * d + (lane >> 4)));
+#pragma unroll
+          for (int n = 0; n < NB; n += 2) {
+            uint32_t b[4];  // keys n and n + 1, channels 16 d on
+            ldsm4(b, ks + chunk_at<ROWB>(n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * d + ((lane >> 3) & 1)));
+            mma_bf16(s[n], qa, b[0], b[1]);
+            mma_bf16(s[n + 1], qa, b[2], b[3]);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int d0 = 0; d0 < D / 8; d0 += 4) {
+          float part[NB][4];
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) part[n][k] = 0.0f;
+#pragma unroll
+          for (int dd = 0; dd < 4; ++dd) {
+            const int d = d0 + dd;
+            uint32_t q[4], hi[4], lo[4];
+            ldsm4(q, qs + chunk_at<ROWB>(warp * 16 + (lane & 15), 2 * d + (lane >> 4)));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) split_tf32(__uint_as_float(q[k]), hi[k], lo[k]);
+#pragma unroll
+            for (int n = 0; n < NB; n += 2) {
+              uint32_t b[4];
+              ldsm4(b, ks + chunk_at<ROWB>(n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t h0, l0, h1, l1;
+                split_tf32(__uint_as_float(b[2 * k]), h0, l0);
+                split_tf32(__uint_as_float(b[2 * k + 1]), h1, l1);
+                mma_tf32(part[n + k], lo, h0, h1);
+                mma_tf32(part[n + k], hi, l0, l1);
+                mma_tf32(part[n + k], hi, h0, h1);
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[n][k] += part[n][k];
+        }
+      }
+
+      // ---- softmax ----------------------------------------------------------------
+      const uint32_t valid = s_valid[tile & 3];
+      const bool masked = key0 + TK > all_see || valid != ALL;
+      uint32_t vis[2] = {~0u, ~0u};
+      if (masked) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int n = sees[k] - key0;
+          vis[k] = n <= 0 ? 0u : n >= 32 ? valid : valid & ((1u << n) - 1u);
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!((vis[k >> 1] >> (n * 8 + 2 * t4 + (k & 1))) & 1u)) s[n][k] = -INFINITY;
+      }
+      float z[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) mx = fmaxf(mx, fmaxf(s[n][2 * k], s[n][2 * k + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2)) * p.scale_log2;
+        if (mx > m[k]) {
+          const float f = exp2_fast(m[k] - mx);  // 0 at first
+          m[k] = mx, l[k] *= f;
+#pragma unroll
+          for (int y = 0; y < D / 8; ++y) o[y][2 * k] *= f, o[y][2 * k + 1] *= f;
+        }
+        z[k] = m[k] == -INFINITY ? 0.0f : -m[k];
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[n][k] = exp2_fast(fmaf(s[n][k], p.scale_log2, z[k >> 1]));
+          l[k >> 1] += s[n][k];
+        }
+
+      // Values that are infinite or NaN: 0 in the product, added by themselves to the
+      // rows that see them (0 NaN is NaN, and hidden ones must have no part).
+      if (masked) {
+        bool wild = false;
+        for (int y = tid; y < TK * CPR; y += NT) {
+          const uint4 v = *reinterpret_cast<const uint4*>(smem + (vs - ring) + y * 16);
+          const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            wild |= (q[k] & 0x7f800000u) == 0x7f800000u || (BF && (q[k] & 0x7f80u) == 0x7f80u);
+        }
+        if (__syncthreads_or(wild)) {
+#pragma unroll 1
+          for (int t = 0; t < TK; ++t) {
+#pragma unroll
+            for (int y = 0; y < D / 8; ++y)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int ch = y * 8 + 2 * t4 + k;
+                const unsigned char* at = smem + (vs - ring) + chunk_at<ROWB>(t, ch * C::ES / 16) + ch * C::ES % 16;
+                const float v = load_elem(at, 0, C::DT);
+                if (!isfinite(v)) {
+                  if ((vis[0] >> t) & 1u) o[y][k] += v;
+                  if ((vis[1] >> t) & 1u) o[y][2 + k] += v;
+                }
+              }
+          }
+          __syncthreads();
+          for (int y = tid; y < TK * ROWB / 4; y += NT) {
+            uint32_t& v = reinterpret_cast<uint32_t*>(smem + (vs - ring))[y];
+            if (BF)
+              v = finite_bf16(v);
+            else if ((v & 0x7f800000u) == 0x7f800000u)
+              v = 0;
+          }
+          __syncthreads();
+        }
+      }
+
+      // ---- value sums: the products of 16 tokens at a time are added with rounding ----
+      if constexpr (BF) {
+#pragma unroll
+        for (int n = 0; n < NB; n += 2) {
+          uint32_t pa[PT][4];
+          float y[8] = {s[n][0], s[n][1], s[n][2], s[n][3], s[n + 1][0], s[n + 1][1], s[n + 1][2], s[n + 1][3]};
+#pragma unroll
+          for (int part = 0; part < PT; ++part)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) pa[part][k] = take_bf16(y[2 * k], y[2 * k + 1]);
+#pragma unroll
+          for (int d = 0; d < D / 8; d += 2) {
+            uint32_t b[4];
+            ldsm4t(b, vs + chunk_at<ROWB>(n * 8 + (lane & 15), d + (lane >> 4)));
+            float u0[4] = {0, 0, 0, 0}, u1[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int part = PT - 1; part >= 0; --part) {
+              mma_bf16(u0, pa[part], b[0], b[1]);
+              mma_bf16(u1, pa[part], b[2], b[3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[d][k] += u0[k], o[d + 1][k] += u1[k];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NB; n += 2) {
+          // the k index t4 stands for token 2 t4, t4 + 4 for 2 t4 + 1: what the scores'
+          // accumulators hold is the A operand as it is
+          uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            split_weight(s[n + y][0], hi[y][0], lo[y][0]);
+            split_weight(s[n + y][2], hi[y][1], lo[y][1]);
+            split_weight(s[n + y][1], hi[y][2], lo[y][2]);
+            split_weight(s[n + y][3], hi[y][3], lo[y][3]);
+          }
+#pragma unroll
+          for (int d = 0; d < D / 8; ++d) {
+            float u[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int t = (n + y) * 8 + 2 * t4, ch = d * 2 + (g >> 2);
+              const float v0 = lds32(vs + chunk_at<ROWB>(t, ch) + (g & 3) * 4);
+              const float v1 = lds32(vs + chunk_at<ROWB>(t + 1, ch) + (g & 3) * 4);
+              uint32_t h0, l0, h1, l1;
+              split_tf32(v0, h0, l0);
+              split_tf32(v1, h1, l1);
+              mma_tf32(u, lo[y], h0, h1);
+              mma_tf32(u, hi[y], l0, l1);
+              mma_tf32(u, hi[y], h0, h1);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[d][k] += u[k];
+          }
+        }
+      }
+    }
+    cp_wait_all();
+
+    // ---- the piece's end ------------------------------------------------------------
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float sum = l[k];
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      const int row = warp * 16 + g + 8 * k, i = token_of(p, row);
+      const float f = !x.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (!mine[k]) continue;
+      if (x.whole) {
+        const int64_t at = (int64_t(x.row0 + i) * a.num_q_heads + x.head0 + row - i * p.bheads) * D + 2 * t4;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) {
+          if (a.out_dtype == LIN_F32)
+            *reinterpret_cast<float2*>(static_cast<float*>(a.out) + at + d * 8) = make_float2(o[d][2 * k] * f, o[d][2 * k + 1] * f);
+          else
+            *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(a.out) + at + d * 8) =
+                __floats2bfloat162_rn(o[d][2 * k] * f, o[d][2 * k + 1] * f);
+        }
+      } else {
+        float* to = p.part + (int64_t(x.part) * p.rows + row) * D + 2 * t4;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d) *reinterpret_cast<float2*>(to + d * 8) = make_float2(o[d][2 * k], o[d][2 * k + 1]);
+        if (t4 == 0) p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(m[k], sum);
+      }
+    }
+  }
+}
+
+template <class C, int PT>
+cudaError_t launch_mma(const Plan& p, cudaStream_t s) {
+  auto kern = chunk_mma_kernel<C, PT>;
+  static bool ready[kMaxDevices];  // set twice at worst, to the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  kern<<<p.grid, C::NT, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_mma_types(const Plan& p, cudaStream_t s) {
+  if (p.c.dtype == LIN_F32) return launch_mma<MCfg<D, LIN_F32>, 1>(p, s);
+  return p.a.out_dtype == LIN_BF16 ? launch_mma<MCfg<D, LIN_BF16>, 2>(p, s) : launch_mma<MCfg<D, LIN_BF16>, 3>(p, s);
+}
+
+}  // namespace chunk
+}  // namespace lin

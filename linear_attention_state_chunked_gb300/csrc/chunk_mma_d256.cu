@@ -1,0 +1,11 @@
+// Warp-level MMA chunk attention kernels for heads of 256 channels (chunk_mma.cuh).
+
+#include "chunk_mma.cuh"
+
+namespace lin {
+namespace chunk {
+
+cudaError_t launch_mma_d256(const Plan& p, cudaStream_t s) { return launch_mma_types<256>(p, s); }
+
+}  // namespace chunk
+}  // namespace lin
