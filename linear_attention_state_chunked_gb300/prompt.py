@@ -87,7 +87,7 @@ def lin_state_kv_plan(*, page_size: int, num_pages: int, length, page_table, n_n
             raise ValueError(f"parent: want [batch][n], got {tuple(parent.shape)}")
         n = parent.shape[1]
     # (a table without entries may have any strides)
-    pages, pstride = _table(page_table if page_table.numel() else page_table.contiguous(), B)
+    pages, pstride = _table(page_table if page_table.numel() else page_table.new_empty(page_table.shape), B)
     dev = _launch_device(length, "length")
     free = pfree = 0
     if free_pages is not None:
