@@ -23,7 +23,8 @@ LIB = os.path.join(PKG, "liblinstate.so")
 SOURCES = ["prompt_api.cu", "copy_kernels.cu", "token_kernels.cu", "chunked_prefill.cu", "verify_chunk.cu",
            "selftest.cu", "kv_cache.cu", "attn_decode.cu", "attn_d64.cu", "attn_d128.cu",
            "attn_d256.cu", "attn_umma_d64.cu", "attn_umma_d128.cu", "attn_umma_d256.cu", "block_norm.cu",
-           "kv_plan.cu", "rope.cu", "chunk_attn.cu", "chunk_mma_d64.cu", "chunk_mma_d128.cu", "chunk_mma_d256.cu"]
+           "kv_plan.cu", "rope.cu", "chunk_attn.cu", "chunk_mma_d64.cu", "chunk_mma_d128.cu", "chunk_mma_d256.cu",
+           "chunk_umma_d64.cu", "chunk_umma_d128.cu", "chunk_umma_d256.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

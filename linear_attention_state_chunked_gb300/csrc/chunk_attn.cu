@@ -1,5 +1,5 @@
 // Chunk attention over a paged key-value cache (lin_prompt.h): the join of split items
-// and the host side. The main kernels are in chunk_mma.cuh.
+// and the host side. The main kernels are in chunk_umma.cuh and chunk_mma.cuh.
 
 #include "chunk_common.cuh"
 
@@ -25,7 +25,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
     const int t = token_of(p, row), h = row - t * p.bheads;
     if (h >= s.heads) continue;
     float top = -INFINITY;
-    for (int i = lane; i < s.parts; i += 32) top = fmaxf(top, p.part_ml[index(i, row)].x);
+    bool out = false;
+    for (int i = lane; i < s.parts; i += 32) {
+      const float2 ml = p.part_ml[index(i, row)];
+      top = fmaxf(top, ml.x);
+      out |= ml.y == attn::kLeftOut;
+    }
+    if (__any_sync(~0u, out)) continue;  // left out after a wait that ran out
 #pragma unroll
     for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
     float sum = 0.0f, v[V];
@@ -59,12 +65,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
 
 // Which kernel a call takes.
 struct Shape {
+  bool umma;
   int rows, tk, ctas, item_cost;
 };
 
-Shape shape_of(const lin_kv_cache_t& c, int out_dtype) {
+Shape shape_of(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int out_dtype) {
+  if (c.dtype == LIN_BF16 && out_dtype == LIN_BF16) {
+    const int64_t rows = int64_t(a.tokens) * (a.num_q_heads / c.num_kv_heads);  // of a kv head
+    const bool two = c.head_dim <= 128 && rows > 128 * int64_t(a.batch);
+    return {true, two ? 256 : 128, 128, 1, 192};
+  }
   const int row_bytes = c.head_dim * dtype_size(c.dtype);
-  return {64, row_bytes >= 512 ? 16 : 32, row_bytes <= 256 ? 3 : row_bytes == 512 ? 2 : 1, 64};
+  return {false, 64, row_bytes >= 512 ? 16 : 32, row_bytes <= 256 ? 3 : row_bytes == 512 ? 2 : 1, 64};
 }
 
 int sm_count() {
@@ -90,20 +102,25 @@ void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
 }  // namespace chunk
 
 size_t chunk_need(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a) {
-  return chunk::bytes_of(c, chunk::shape_of(c, a.out_dtype));
+  return chunk::bytes_of(c, chunk::shape_of(c, a, a.out_dtype));
 }
 
 size_t chunk_workspace(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a) {
+  // of every kernel that a call over this cache may take
   size_t most = 0;
-  for (const int out : {LIN_BF16, LIN_F32}) {
-    const size_t n = chunk::bytes_of(c, chunk::shape_of(c, out));
-    if (n > most) most = n;
-  }
+  lin_attn_chunk_args_t x = a;
+  x.batch = 1;
+  for (const int out : {LIN_BF16, LIN_F32})
+    for (const int tokens : {1, 129}) {
+      x.tokens = tokens;
+      const size_t n = chunk::bytes_of(c, chunk::shape_of(c, x, out));
+      if (n > most) most = n;
+    }
   return most;
 }
 
 cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, void* ws, cudaStream_t s) {
-  const chunk::Shape f = chunk::shape_of(c, a.out_dtype);
+  const chunk::Shape f = chunk::shape_of(c, a, a.out_dtype);
   chunk::Plan p;
   p.c = c;
   p.a = a;
@@ -129,9 +146,15 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.part_ml = reinterpret_cast<float2*>(w);
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
-  const cudaError_t e = c.head_dim == 64    ? chunk::launch_mma_d64(p, s)
-                        : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)
-                                            : chunk::launch_mma_d256(p, s);
+  cudaError_t e;
+  if (f.umma)
+    e = c.head_dim == 64    ? chunk::launch_umma_d64(p, s)
+        : c.head_dim == 128 ? chunk::launch_umma_d128(p, s)
+                            : chunk::launch_umma_d256(p, s);
+  else
+    e = c.head_dim == 64    ? chunk::launch_mma_d64(p, s)
+        : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)
+                            : chunk::launch_mma_d256(p, s);
   if (e != cudaSuccess) return e;
   // the join's launch overlaps the main kernel, and it waits there for its end
   cudaLaunchAttribute attr[1];

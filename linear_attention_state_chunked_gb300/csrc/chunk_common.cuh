@@ -249,8 +249,11 @@ __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
 
 // One translation unit per head_dim and kind of kernel.
 cudaError_t launch_mma_d64(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d64(const Plan& p, cudaStream_t s);
 cudaError_t launch_mma_d128(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d128(const Plan& p, cudaStream_t s);
 cudaError_t launch_mma_d256(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d256(const Plan& p, cudaStream_t s);
 
 }  // namespace chunk
 }  // namespace lin

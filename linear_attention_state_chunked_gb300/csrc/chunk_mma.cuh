@@ -370,8 +370,7 @@ cudaError_t launch_mma(const Plan& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_mma_types(const Plan& p, cudaStream_t s) {
-  if (p.c.dtype == LIN_F32) return launch_mma<MCfg<D, LIN_F32>, 1>(p, s);
-  return p.a.out_dtype == LIN_BF16 ? launch_mma<MCfg<D, LIN_BF16>, 2>(p, s) : launch_mma<MCfg<D, LIN_BF16>, 3>(p, s);
+  return p.c.dtype == LIN_F32 ? launch_mma<MCfg<D, LIN_F32>, 1>(p, s) : launch_mma<MCfg<D, LIN_BF16>, 3>(p, s);
 }
 
 }  // namespace chunk

@@ -1,0 +1,751 @@
+// Chunk attention over bf16 caches with bf16 outputs, on the 5th-generation tensor cores.
+//
+//   S = Q K^T,  P = 2^(S scale log2(e) - m),  O = sum over tiles of P V,  out = O / sum P
+//
+// in tiles of 128 rows (new tokens x query heads of one kv head) and TK = 128 keys, with
+// a running maximum and sum per row. Bound by the tensor unit for prompts: 4 head_dim
+// flops per visible (row, key); by HBM for a few rows over a long cache.
+//
+// An item has NQ row tiles. Two (heads of 64 and 128): the unit makes O += P V and the
+// next S of one while the softmax warps of the other work. One (heads of 256, whose O
+// alone takes half of tensor memory, and few rows): S has two buffers, and the unit
+// makes the next S while the softmax works on the last.
+//
+// Roles: 4 NQ softmax warps (thread = row = tensor-memory lane, so no exchange between
+// threads), 4 warps that load K and V (16-byte asynchronous copies, as pages may end
+// anywhere) into a ring of U units, one that issues the products, one that hands out the
+// pieces (chunk_common.cuh), two that load Q and look over values (below). Each goes
+// through the pieces by itself, so one item's end overlaps the next one's start. P goes
+// back to tensor memory in the place of its S, as the A operand of P V, rounded to bf16:
+// one more rounding of 2^-9 rms beside the output's own; the sums are of the unrounded
+// weights. The reference m moves only when a score passes it by 2^8, so O is rarely
+// rescaled, by the softmax warps themselves.
+//
+// Hidden values: 0 NaN is NaN, so in tiles that some row of the item does not see whole
+// (the last ones) the values are looked over; infinities and NaN are 0 in the product
+// and go to the rows that see them by themselves.
+//
+// The value sums stay in the unit, which cuts off below the last place of what it adds
+// to; after kRun tiles they are added to sums in the workspace with rounding, which keeps
+// the loss below 2^-11 of the sum p |v| at any length.
+#pragma once
+
+#include "chunk_common.cuh"
+
+namespace lin {
+namespace chunk {
+
+template <int D_, int NQ_>
+struct UCfg {
+  static constexpr int D = D_, NQ = NQ_;
+  static constexpr int TK = 128;
+  static constexpr int DK = D < 128 ? D : 128;  // channels of a ring unit
+  static constexpr int KU = D / DK;             // units of a tile's K, or V
+  static constexpr int UNIT = TK * DK * 2;
+  static constexpr int QT = 128 * D * 2;        // a row tile's queries
+  static constexpr int FREE = 224 * 1024 - NQ * QT;
+  static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
+  static constexpr int SMEM = U * UNIT + NQ * QT;
+  static constexpr int SOFT = 4 * NQ;           // softmax warps
+  static constexpr int THREADS = SOFT * 32 + 256;
+  // tensor memory columns: 2 of S (and P), NQ of O
+  static constexpr int T_O = 2 * TK;
+  static constexpr int TMEM = 512;
+  static_assert(T_O + NQ * D <= TMEM && U >= 2 * KU, "");
+};
+
+constexpr uint32_t kWaitTries = 1u << 24;
+constexpr int kRun = 256;     // most tiles whose value sums stay in the unit
+constexpr int kPieces = 4;    // pieces handed out ahead
+constexpr int kValidRing = 16, kCheckRing = 8;
+
+struct UPiece {
+  Piece x;
+  int nt[2];    // tiles of the row tiles
+  int n;        // the larger
+  int g0;       // tiles of the pieces before
+  int check0;   // values are looked over from this tile on
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void arrive_copies(uint64_t* bar) {  // when this thread's copies have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
+}
+// D += A B with A in tensor memory: row i in lane i, two bf16 of a row to a column.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      :
+      : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One lane of the warp, always the same (what it does stays in uniform registers).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void f2unpack(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 32 columns of this thread's lane, without a wait.
+__device__ __forceinline__ void tmem_issue32(uint32_t at, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+        "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+        "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+      : "r"(at));
+}
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The values are there from here on: no use of them moves above.
+__device__ __forceinline__ void landed32(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
+}
+__device__ __forceinline__ void tmem_put32(uint32_t at, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A place of the ring and its phase.
+template <int U>
+struct At {
+  int slot;
+  uint32_t phase;
+  __device__ __forceinline__ void step(int n) {
+    slot += n;
+    if (slot >= U) slot -= U, phase ^= 1;
+  }
+  __device__ __forceinline__ At plus(int n) const {
+    At y = *this;
+    y.step(n);
+    return y;
+  }
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p) {
+  constexpr int D = C::D, NQ = C::NQ, TK = C::TK, DK = C::DK, KU = C::KU, U = C::U, NT = C::THREADS, SOFT = C::SOFT;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ uint64_t b_full[U], b_empty[U], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[NQ], b_check[kCheckRing],
+      b_pfull[kPieces], b_pempty[kPieces], b_drain;
+  __shared__ UPiece s_piece[kPieces];
+  __shared__ uint4 s_valid[kValidRing];  // live keys of a tile; a ring of tiles
+  __shared__ uint4 s_wild[kCheckRing];   // keys of a looked-over tile with values that are not finite
+  __shared__ WalkShared s_walk;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead;
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const lin_kv_cache_t& c = p.c;
+  const lin_attn_chunk_args_t& a = p.a;
+  if (tid == 0) {
+    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 128 + 4), umma::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1), umma::mbar_init(&b_o[i], 1);
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4);
+    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_check[i], 2);
+    for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 4 + 1 + 2);
+    umma::mbar_init(&b_drain, 1);
+    umma::mbar_fence_init();
+    s_dead = 0;
+  }
+  Walk w;
+  if (!walk_begin<NT>(p, w, s_walk)) return;
+  if (warp == SOFT + 4) umma::tmem_alloc(&s_tmem, C::TMEM);
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = s_tmem, t_o = tmem + C::T_O;
+  unsigned char* const qbuf = smem + U * C::UNIT;
+
+  // A warp whose wait runs out waits for nothing more; the others learn of it where
+  // they wait, and all go to the end. Called by whole warps, and the same for all lanes.
+  bool gone = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (gone) return;
+    for (uint32_t i = 0; i < kWaitTries; ++i) {
+      if (__all_sync(~0u, umma::mbar_try_wait(bar, parity))) return;
+      if ((i & 63) == 63 && __any_sync(~0u, *static_cast<volatile int*>(&s_dead))) {
+        gone = true;
+        return;
+      }
+    }
+    gone = true;
+    s_dead = 1;
+    report(a.status, LIN_ST_TIMEOUT);
+  };
+  int at_piece = 0;
+  uint32_t piece_phase = 0;
+  // The next piece, by a whole warp; false at the end.
+  auto fetch = [&](UPiece& y) {
+    wait(&b_pfull[at_piece], piece_phase);
+    if (gone) return false;
+    y = s_piece[at_piece];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b_pempty[at_piece]);
+    if (++at_piece == kPieces) at_piece = 0, piece_phase ^= 1;
+    return y.x.r >= 0;
+  };
+
+  if (warp < SOFT) {
+    // ---- softmax ------------------------------------------------------------------------
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    const int st = warp >> 2;  // row tile
+    const int row = st * 128 + (tid & 127);
+    const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t to = t_o + t_lane + st * D;
+    const uint64_t scale2 = f2pack(p.scale_log2, p.scale_log2);
+    uint32_t ct = 0, chk = 0;  // tiles, looked-over tiles so far
+    UPiece y;
+    while (fetch(y)) {
+      const Piece& x = y.x;
+      const int tok = token_of(p, row), head = row - tok * p.bheads;
+      const bool mine = tok < x.tokens && head < x.heads;
+      const int sees = mine ? max(0, x.pos + tok + 1) : 0;
+      const int all_see = max(0, x.pos + token_of(p, st * 128) + 1);  // what every row of the tile sees
+      const int nt = st == 0 ? y.nt[0] : y.nt[1];
+      float* const acc = p.part + (int64_t(x.part) * p.rows + row) * D;  // sums of earlier runs
+      float cut = -INFINITY, z = 0.0f, l = 0.0f, z_acc = 0.0f;
+      bool has_acc = false;
+      // looked-over tiles that are not this row tile's
+      const int first_chk = max(x.t0, y.check0), chk_before = chk;
+      for (int i = 0; i < nt && !gone; ++i) {
+        const int tile = x.t0 + i, key0 = tile * TK;
+        const int buf = NQ == 2 ? st : ct & 1;
+        const uint32_t ts = tmem + t_lane + buf * TK;
+        wait(&b_s[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+        umma::fence_after_sync();
+        float s[128];
+#pragma unroll
+        for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
+        const uint4 valid = s_valid[(y.g0 + i) & (kValidRing - 1)];
+        const bool first = i % kRun == 0;
+        tmem_loaded();
+#pragma unroll
+        for (int k = 0; k < 128; k += 32) landed32(s + k);
+        if (first && i > 0) {  // a run's end: its sums to the workspace
+          wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+          umma::fence_after_sync();
+          const float f = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
+#pragma unroll 1
+          for (int d = 0; d < D; d += 8) {
+            float o[8];
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                         "tcgen05.wait::ld.sync.aligned;"
+                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                         : "r"(to + d)
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+              float4* m = reinterpret_cast<float4*>(acc + d + k);
+              const float4 was = i == kRun ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *m;
+              *m = make_float4(fmaf(was.x, f, o[k]), fmaf(was.y, f, o[k + 1]), fmaf(was.z, f, o[k + 2]), fmaf(was.w, f, o[k + 3]));
+            }
+          }
+          z_acc = z, has_acc = cut != -INFINITY;
+        }
+        if (p.negate) {
+#pragma unroll
+          for (int k = 0; k < 128; ++k) s[k] = -s[k];
+        }
+        if (key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u) {
+          const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int n = sees - key0 - 32 * h;
+            const uint32_t vis = n <= 0 ? 0u : n >= 32 ? live[h] : live[h] & ((1u << n) - 1u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((vis >> k) & 1u)) s[32 * h + k] = -INFINITY;
+          }
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int k = 4; k < 124; k += 8)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) top[h] = max3(top[h], s[k + h], s[k + 4 + h]);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) top[h] = fmaxf(top[h], s[124 + h]);
+        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+        float f = 1.0f;
+        if (mx > cut) {
+          const float y0 = -mx * p.scale_log2;
+          f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
+          z = y0, cut = mx + p.slack, l *= f;
+        }
+        if (!first && __any_sync(~0u, f != 1.0f)) {
+          wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);  // the last product has ended
+          umma::fence_after_sync();
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+            umma::tmem_ld16(to + d, o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] *= f;
+            umma::tmem_st16(to + d, o);
+          }
+        }
+        if (tile >= y.check0) {
+          wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+          const uint4 wv = s_wild[chk & (kCheckRing - 1)];
+          ++chk;
+          if (wv.x | wv.y | wv.z | wv.w) {
+            if (!first) wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+            umma::fence_after_sync();
+            const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
+            const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 8) {
+              float o[8];
+              asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+                           "tcgen05.wait::ld.sync.aligned;"
+                           : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                           : "r"(to + d)
+                           : "memory");
+              if (first) {  // the product adds to these, as it does not start from 0
+#pragma unroll
+                for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+              }
+#pragma unroll 1
+              for (int h = 0; h < 4; ++h) {
+                uint32_t left = h == 0 ? wild[0] : h == 1 ? wild[1] : h == 2 ? wild[2] : wild[3];
+                for (; left; left &= left - 1) {
+                  const int t = key0 + 32 * h + __ffs(left) - 1;
+                  if (t >= sees) break;
+                  const int pg = page_of(p, t);
+                  const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
+                                  (t - pg * c.page_size) * c.token_stride + d * 2;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);
+                    if (!isfinite(e)) o[k] += e;
+                  }
+                }
+              }
+              __syncwarp();
+              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+                           "tcgen05.wait::st.sync.aligned;" ::"r"(to + d),
+                           "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
+                           : "memory");
+            }
+          }
+        }
+        const uint64_t z2 = f2pack(z, z);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 128; h += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float e0, e1;
+            f2unpack(ffma2(f2pack(s[h + 2 * k], s[h + 2 * k + 1]), scale2, z2), e0, e1);
+            e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
+            sum[k & 1] = fadd2(sum[k & 1], f2pack(e0, e1));
+            pk[k] = pack_bf16(e0, e1);
+          }
+          tmem_put32(ts + h / 2, pk);
+        }
+        l += f2sum(fadd2(sum[0], sum[1]));
+        tmem_stored();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_p[buf]);
+        ++ct;
+      }
+      if (gone) break;
+      // the piece's looked-over tiles, those of the other row tile too
+      chk = chk_before + max(0, x.t0 + y.n - first_chk);
+      // ---- the piece's end ------------------------------------------------------------
+      if (nt > 0) wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+      if (gone) break;
+      umma::fence_after_sync();
+      const float fa = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
+      const float fo = !x.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+      uint16_t* const out =
+          static_cast<uint16_t*>(a.out) + (int64_t(x.row0 + tok) * a.num_q_heads + x.head0 + head) * D;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float o[32];
+        __syncwarp();
+        if (nt > 0) {
+          tmem_issue32(to + d, o);
+          tmem_loaded();
+          landed32(o);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+        }
+        if (!mine) continue;
+        if (has_acc) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = fmaf(acc[d + k], fa, o[k]);
+        }
+        if (x.whole) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(out + d + k) =
+                make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
+                           pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4*>(acc + d + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        }
+      }
+      if (mine && !x.whole)
+        p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(cut == -INFINITY ? cut : -z, l);
+      __syncwarp();
+    }
+  } else if (warp < SOFT + 4) {
+    // ---- loads: each warp brings 32 keys of a tile --------------------------------------
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    constexpr int CPR = DK / 8, STEP = 32 / CPR;
+    const int lw = warp - SOFT;
+    const uint32_t place = umma::smem_u32(smem) + umma::rp_offset(lw * 32 + lane / CPR, (lane % CPR) * 8, TK);
+    At<U> r{0, 0};
+    UPiece y;
+    while (fetch(y)) {
+      const Piece& x = y.x;
+      const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + x.hk * c.head_stride;
+      const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
+      const int32_t* table = a.page_table + x.r * a.page_table_stride;
+      int key = x.t0 * TK + lw * 32 + lane;
+      int id = key < x.keys && y.n > 0 ? table[page_of(p, key)] : -1;
+      for (int i = 0; i < y.n && !gone; ++i) {
+        const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
+        if (key < x.keys && !live) report(a.status, LIN_ST_BAD_PAGE);
+        const int64_t off = live ? id * c.page_stride + (key - page_of(p, key) * c.page_size) * c.token_stride : 0;
+        const uint32_t valid = __ballot_sync(~0u, live);
+        key += TK;
+        id = key < x.keys ? table[page_of(p, key)] : -1;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+          for (int j = 0; j < KU; ++j) {
+            wait(&b_empty[r.slot], r.phase ^ 1);
+            if (kv == 0 && j == 0 && lane == 0)
+              reinterpret_cast<uint32_t*>(&s_valid[(y.g0 + i) & (kValidRing - 1)])[lw] = valid;
+            const uint32_t dst = place + r.slot * C::UNIT;
+            const char* src = (kv ? vb : kb) + j * (DK * 2) + (lane % CPR) * 16;
+#pragma unroll
+            for (int k = 0; k < 32 / STEP; ++k) {
+              const int row = k * STEP + lane / CPR;
+              const int64_t o = __shfl_sync(~0u, off, row);
+              attn::cp16((dst ^ ((k * STEP & 7) << 4)) + k * STEP * 128, src + o, (valid >> row) & 1u);
+            }
+            // full when every lane's copies have landed: nobody waits here
+            arrive_copies(&b_full[r.slot]);
+            if (lane == 0) mbar_arrive(&b_full[r.slot]);  // and passes on s_valid
+            r.step(1);
+          }
+      }
+      if (gone) break;
+    }
+    attn::cp_wait_all();
+  } else {
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == SOFT + 4) {
+      // ---- products ----------------------------------------------------------------------
+      constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
+      constexpr uint32_t id_o = umma::idesc_f16(128, DK, true, false, true);
+      const uint64_t q_desc = umma::desc_kmajor(umma::smem_u32(qbuf), 128, 0);
+      const uint64_t k_desc = umma::desc_kmajor(umma::smem_u32(smem), TK, 0);
+      const uint64_t v_desc = umma::desc_mnmajor(umma::smem_u32(smem), TK, 0);
+      auto kstep = [](int k) { return uint64_t(((k >> 6) * 128 * 128 + (k & 63) * 2) >> 4); };
+      At<U> rk{0, 0}, rv{KU, 0};
+      uint32_t ct[2] = {0, 0}, qn[2] = {0, 0}, chk = 0;
+      // (every lane waits, one issues; called by the whole warp)
+      auto wait_units = [&](const At<U>& r) {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+          const At<U> q = r.plus(j);
+          wait(&b_full[q.slot], q.phase);
+        }
+        umma::fence_smem_to_async();
+      };
+      auto free_units = [&](const At<U>& r) {  // the elected lane
+#pragma unroll
+        for (int j = 0; j < KU; ++j) umma::mma_commit(&b_empty[r.plus(j).slot]);
+      };
+      // S of row tile st into buffer buf; the elected lane
+      auto issue_s = [&](int st, int buf, bool last) {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+          const uint64_t kd = k_desc + rk.plus(j).slot * (C::UNIT >> 4);
+#pragma unroll
+          for (int k = 0; k < DK; k += 16)
+            umma::mma_f16(tmem + buf * TK, q_desc + st * (C::QT >> 4) + kstep(j * DK + k), kd + kstep(k), id_s, j + k > 0);
+        }
+        umma::mma_commit(&b_s[buf]);
+        if (last) umma::mma_commit(&b_qfree[st]);
+        mbar_arrive(&b_s[buf]);  // passes on what the loaders wrote besides the tile
+      };
+      auto issue_o = [&](int st, int buf, uint32_t add) {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) {
+          const uint64_t vd = v_desc + rv.plus(j).slot * (C::UNIT >> 4);
+#pragma unroll
+          for (int k = 0; k < TK; k += 16)
+            mma_ts(t_o + st * D + j * DK, tmem + buf * TK + k / 2, vd + ((k * 128) >> 4), id_o, k > 0 ? 1u : add);
+        }
+        umma::mma_commit(&b_o[st]);
+      };
+      // the next piece with tiles
+      auto next_piece = [&](UPiece& y) {
+        do {
+          if (!fetch(y)) return false;
+        } while (y.n == 0);
+        return true;
+      };
+      // the first S of a piece
+      auto begin = [&](const UPiece& y) {
+        wait_units(rk);
+#pragma unroll
+        for (int st = 0; st < NQ; ++st) {
+          if (y.nt[st] == 0) continue;
+          wait(&b_qfull[st], qn[st] & 1);
+          ++qn[st];
+          umma::fence_smem_to_async();
+          umma::fence_after_sync();
+          if (elect_one()) issue_s(st, NQ == 2 ? st : ct[0] & 1, y.nt[st] == 1);
+          __syncwarp();
+        }
+        if (elect_one()) free_units(rk);
+        __syncwarp();
+        rk.step(2 * KU);
+      };
+      UPiece y, after;
+      bool have = next_piece(y);
+      if (have) begin(y);
+      while (have && !gone) {
+        bool more = false;
+        for (int i = 0; i < y.n && !gone; ++i) {
+          const bool end = i + 1 == y.n;
+          if (NQ == 1 && !end) {  // the next S goes first
+            wait_units(rk);
+            umma::fence_after_sync();
+            if (elect_one()) {
+              issue_s(0, (ct[0] + 1) & 1, i + 2 == y.n);
+              free_units(rk);
+            }
+            __syncwarp();
+            rk.step(2 * KU);
+          }
+          wait_units(rv);
+          uint32_t add = i % kRun != 0;
+          if (y.x.t0 + i >= y.check0) {
+            wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+            const uint4 wv = s_wild[chk & (kCheckRing - 1)];
+            if (wv.x | wv.y | wv.z | wv.w) add = 1;
+            ++chk;
+          }
+          if (NQ == 2 && !end) wait_units(rk);
+#pragma unroll
+          for (int st = 0; st < NQ; ++st) {
+            if (i < y.nt[st]) {
+              const int buf = NQ == 2 ? st : ct[st] & 1;
+              wait(&b_p[buf], (NQ == 2 ? ct[st] : ct[st] >> 1) & 1);
+              umma::fence_after_sync();
+              if (elect_one()) issue_o(st, buf, add);
+              __syncwarp();
+              ++ct[st];
+            }
+            if (NQ == 2 && !end && i + 1 < y.nt[st]) {
+              if (elect_one()) issue_s(st, st, i + 2 == y.nt[st]);
+              __syncwarp();
+            }
+          }
+          if (elect_one()) {
+            free_units(rv);
+            if (NQ == 2 && !end) free_units(rk);
+          }
+          __syncwarp();
+          rv.step(2 * KU);
+          if (NQ == 2 && !end) rk.step(2 * KU);
+          if (end) {
+            more = next_piece(after);
+            if (more) begin(after);
+          }
+        }
+        have = more;
+        y = after;
+      }
+      // products in flight end before tensor memory is given back
+      if (elect_one()) umma::mma_commit(&b_drain);
+      __syncwarp();
+      for (uint32_t i = 0; i < kWaitTries && !umma::mbar_try_wait(&b_drain, 0); ++i) {
+      }
+    } else if (warp == SOFT + 5) {
+      // ---- pieces -------------------------------------------------------------------------
+      if (lane == 0) {
+        UPiece y;
+        int g = 0;
+        do {
+          y.x = walk_next(p, w);
+          const Piece& x = y.x;
+          y.n = 0, y.g0 = g, y.check0 = INT_MAX;
+          y.nt[0] = y.nt[1] = 0;
+          if (x.r >= 0) {
+#pragma unroll
+            for (int st = 0; st < NQ; ++st) {
+              if (st * 128 >= x.tokens * p.bheads) continue;
+              const int last = min(x.tokens - 1, token_of(p, st * 128 + 127));
+              const int keys = max(0, x.pos + last + 1);
+              y.nt[st] = max(0, min(x.t1, (keys + TK - 1) / TK) - x.t0);
+              y.n = max(y.n, y.nt[st]);
+            }
+            if (x.keys > max(0, x.pos + 1)) y.check0 = max(0, x.pos + 1) / TK;
+            g += y.n;
+          }
+          bool free = false;
+          for (uint32_t i = 0; i < kWaitTries && !free && !*static_cast<volatile int*>(&s_dead); ++i)
+            free = umma::mbar_try_wait(&b_pempty[at_piece], piece_phase ^ 1);
+          if (!free) {  // this range's pieces are lost either way
+            s_dead = 1;
+            report(a.status, LIN_ST_TIMEOUT);
+            break;
+          }
+          s_piece[at_piece] = y;
+          mbar_arrive(&b_pfull[at_piece]);
+          if (++at_piece == kPieces) at_piece = 0, piece_phase ^= 1;
+        } while (y.x.r >= 0);
+      }
+      __syncwarp();
+    } else {
+      // ---- queries, and a look at the values -------------------------------------------------
+      constexpr int CPR = D / 8;
+      const int me = tid - (SOFT + 6) * 32;
+      At<U> rv{KU, 0};
+      uint32_t qn[2] = {0, 0}, chk = 0;
+      UPiece y;
+      while (fetch(y)) {
+        const Piece& x = y.x;
+#pragma unroll
+        for (int st = 0; st < NQ; ++st) {
+          if (y.nt[st] == 0) continue;
+          wait(&b_qfree[st], (qn[st] & 1) ^ 1);
+          if (gone) break;
+          ++qn[st];
+          const uint32_t dst = umma::smem_u32(qbuf) + st * C::QT;
+          const char* src = static_cast<const char*>(a.q) + int64_t(x.row0) * a.token_stride + int64_t(x.head0) * (D * 2);
+#pragma unroll 4
+          for (int k = me; k < 128 * CPR; k += 64) {
+            const int row = k / CPR, ch = k % CPR;
+            const int t = token_of(p, st * 128 + row), h = st * 128 + row - t * p.bheads;
+            const bool live = t < x.tokens && h < x.heads;
+            attn::cp16(dst + umma::rp_offset(row, ch * 8, 128),
+                       src + (live ? t * a.token_stride + h * (D * 2) + ch * 16 : 0), live);
+          }
+          arrive_copies(&b_qfull[st]);
+        }
+        for (int i = 0; i < y.n && !gone; ++i) {
+          if (x.t0 + i >= y.check0) {
+            bool wild[2] = {false, false};
+#pragma unroll
+            for (int j = 0; j < KU; ++j) {
+              const At<U> q = rv.plus(j);
+              wait(&b_full[q.slot], q.phase);
+              if (gone) break;
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll 4
+                for (int ch = 0; ch < DK / 8; ++ch) {
+                  uint4* at = reinterpret_cast<uint4*>(smem + q.slot * C::UNIT + umma::rp_offset(h * 64 + me, ch * 8, TK));
+                  const uint4 v = *at;
+                  uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                  bool bad = false;
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    if ((e[k] & 0x7f80u) == 0x7f80u) e[k] &= 0xffff0000u, bad = true;
+                    if ((e[k] & 0x7f800000u) == 0x7f800000u) e[k] &= 0x0000ffffu, bad = true;
+                  }
+                  if (bad) *at = make_uint4(e[0], e[1], e[2], e[3]), wild[h] = true;
+                }
+            }
+            umma::fence_smem_to_async();
+            const uint32_t w0 = __ballot_sync(~0u, wild[0]), w1 = __ballot_sync(~0u, wild[1]);
+            if (lane == 0) {
+              uint32_t* to = reinterpret_cast<uint32_t*>(&s_wild[chk & (kCheckRing - 1)]) + (warp - SOFT - 6);
+              to[0] = w0, to[2] = w1;
+              mbar_arrive(&b_check[chk & (kCheckRing - 1)]);
+            }
+            ++chk;
+          }
+          rv.step(2 * KU);
+        }
+        if (gone) break;
+      }
+      attn::cp_wait_all();
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  if (warp == SOFT + 4) umma::tmem_dealloc(tmem, C::TMEM);
+  if (s_dead) {
+    // a wait ran out: what this range leaves unwritten counts as left out
+    for (int x = tid; x < 2 * p.rows; x += NT) p.part_ml[2 * int64_t(blockIdx.x) * p.rows + x] = make_float2(-INFINITY, attn::kLeftOut);
+    if (tid == 0) p.split[blockIdx.x].parts = 0;
+  }
+}
+
+template <class C>
+cudaError_t launch_umma(const Plan& p, cudaStream_t s) {
+  auto kern = chunk_umma_kernel<C>;
+  static bool ready[kMaxDevices];  // set twice at worst, to the same value
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= kMaxDevices || !ready[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices) ready[dev] = true;
+  }
+  kern<<<p.grid, C::THREADS, C::SMEM, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_umma_tiles(const Plan& p, cudaStream_t s) {
+  if constexpr (D <= 128)
+    if (p.rows == 256) return launch_umma<UCfg<D, 2>>(p, s);
+  return launch_umma<UCfg<D, 1>>(p, s);
+}
+
+}  // namespace chunk
+}  // namespace lin

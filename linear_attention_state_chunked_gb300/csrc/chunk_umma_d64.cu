@@ -1,0 +1,11 @@
+// Tensor-memory chunk attention kernels for heads of 64 channels (chunk_umma.cuh).
+
+#include "chunk_umma.cuh"
+
+namespace lin {
+namespace chunk {
+
+cudaError_t launch_umma_d64(const Plan& p, cudaStream_t s) { return launch_umma_tiles<64>(p, s); }
+
+}  // namespace chunk
+}  // namespace lin
