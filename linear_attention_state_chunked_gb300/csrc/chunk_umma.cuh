@@ -162,7 +162,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p) {
   constexpr int D = C::D, NQ = C::NQ, TK = C::TK, DK = C::DK, KU = C::KU, U = C::U, NT = C::THREADS, SOFT = C::SOFT;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ uint64_t b_full[U], b_empty[U], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[NQ], b_check[kCheckRing],
+  __shared__ uint64_t b_full[U], b_empty[U], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
       b_pfull[kPieces], b_pempty[kPieces], b_drain;
   __shared__ UPiece s_piece[kPieces];
   __shared__ uint4 s_valid[kValidRing];  // live keys of a tile; a ring of tiles
@@ -177,9 +177,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
   const lin_attn_chunk_args_t& a = p.a;
   if (tid == 0) {
     for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 128 + 4), umma::mbar_init(&b_empty[i], 1);
-    for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1), umma::mbar_init(&b_o[i], 1);
-    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4);
-    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_check[i], 2);
+    for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
+    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], 128), umma::mbar_init(&b_check[i], 2);
     for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 4 + 1 + 2);
     umma::mbar_init(&b_drain, 1);
     umma::mbar_fence_init();
@@ -232,6 +232,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
     const uint32_t to = t_o + t_lane + st * D;
     const uint64_t scale2 = f2pack(p.scale_log2, p.scale_log2);
     uint32_t ct = 0, chk = 0;  // tiles, looked-over tiles so far
+    // The product of tile t has ended. (A barrier for each buffer: when S of tile t is
+    // there, the product of t - 2 has ended, and that of t - 1 need not have.)
+    auto wait_o = [&](uint32_t t) { wait(&b_o[NQ == 2 ? st : t & 1], (NQ == 2 ? t : t >> 1) & 1); };
     UPiece y;
     while (fetch(y)) {
       const Piece& x = y.x;
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll
         for (int k = 0; k < 128; k += 32) landed32(s + k);
         if (first && i > 0) {  // a run's end: its sums to the workspace
-          wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+          wait_o(ct - 1);
           umma::fence_after_sync();
           const float f = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
 #pragma unroll 1
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
           z = y0, cut = mx + p.slack, l *= f;
         }
         if (!first && __any_sync(~0u, f != 1.0f)) {
-          wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);  // the last product has ended
+          wait_o(ct - 1);  // the last product has ended
           umma::fence_after_sync();
 #pragma unroll 1
           for (int d = 0; d < D; d += 16) {
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
           const uint4 wv = s_wild[chk & (kCheckRing - 1)];
           ++chk;
           if (wv.x | wv.y | wv.z | wv.w) {
-            if (!first) wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+            if (!first) wait_o(ct - 1);
             umma::fence_after_sync();
             const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
             const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
       // the piece's looked-over tiles, those of the other row tile too
       chk = chk_before + max(0, x.t0 + y.n - first_chk);
       // ---- the piece's end ------------------------------------------------------------
-      if (nt > 0) wait(&b_o[NQ == 2 ? st : 0], (ct - 1) & 1);
+      if (nt > 0) wait_o(ct - 1);
       if (gone) break;
       umma::fence_after_sync();
       const float fa = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
@@ -402,7 +405,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float o[32];
-        __syncwarp();
         if (nt > 0) {
           tmem_issue32(to + d, o);
           tmem_loaded();
@@ -411,22 +413,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.0f;
         }
-        if (!mine) continue;
-        if (has_acc) {
+        if (mine) {  // (the loads are the whole warp's: no lane may leave the loop)
+          if (has_acc) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = fmaf(acc[d + k], fa, o[k]);
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(acc[d + k], fa, o[k]);
+          }
+          if (x.whole) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(out + d + k) =
+                  make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
+                             pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+              *reinterpret_cast<float4*>(acc + d + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
         }
-        if (x.whole) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(out + d + k) =
-                make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
-                           pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4*>(acc + d + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-        }
+        __syncwarp();
       }
       if (mine && !x.whole)
         p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(cut == -INFINITY ? cut : -z, l);
@@ -439,6 +443,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
     const int lw = warp - SOFT;
     const uint32_t place = umma::smem_u32(smem) + umma::rp_offset(lw * 32 + lane / CPR, (lane % CPR) * 8, TK);
     At<U> r{0, 0};
+    uint32_t chk = 0;
     UPiece y;
     while (fetch(y)) {
       const Piece& x = y.x;
@@ -472,6 +477,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
             // full when every lane's copies have landed: nobody waits here
             arrive_copies(&b_full[r.slot]);
             if (lane == 0) mbar_arrive(&b_full[r.slot]);  // and passes on s_valid
+            if (kv == 1 && j == KU - 1 && x.t0 + i >= y.check0) arrive_copies(&b_look[chk++ & (kCheckRing - 1)]);
             r.step(1);
           }
       }
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
           for (int k = 0; k < TK; k += 16)
             mma_ts(t_o + st * D + j * DK, tmem + buf * TK + k / 2, vd + ((k * 128) >> 4), id_o, k > 0 ? 1u : add);
         }
-        umma::mma_commit(&b_o[st]);
+        umma::mma_commit(&b_o[buf]);
       };
       // the next piece with tiles
       auto next_piece = [&](UPiece& y) {
@@ -676,12 +682,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
         }
         for (int i = 0; i < y.n && !gone; ++i) {
           if (x.t0 + i >= y.check0) {
+            // (a barrier of these tiles alone: the ring's may be many phases behind)
+            wait(&b_look[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+            if (gone) break;
             bool wild[2] = {false, false};
 #pragma unroll
             for (int j = 0; j < KU; ++j) {
               const At<U> q = rv.plus(j);
-              wait(&b_full[q.slot], q.phase);
-              if (gone) break;
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll 4
