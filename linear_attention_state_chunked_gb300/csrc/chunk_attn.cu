@@ -1,6 +1,8 @@
 // Chunk attention over a paged key-value cache (lin_prompt.h): the join of split items
 // and the host side. The main kernels are in chunk_umma.cuh and chunk_mma.cuh.
 
+#include <cudaTypedefs.h>
+
 #include "chunk_common.cuh"
 
 namespace lin {
@@ -8,57 +10,117 @@ namespace chunk {
 namespace {
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinRows = 32;      // rows of a block: a lane each
+constexpr int kManyParts = 8;      // see launch_attn_chunk
+
+// The x-th of the ranges whose last item goes on past them, by a whole warp; false
+// where there are fewer.
+__device__ __forceinline__ bool find_split(const Plan& p, int x, int& range, Split& s) {
+  const int lane = threadIdx.x & 31;
+  for (int c = 0; c < p.grid; c += 32) {
+    const uint32_t some = __ballot_sync(~0u, c + lane < p.grid && p.split[c + lane].parts > 0);
+    const int n = __popc(some);
+    if (x < n) {
+      range = c + static_cast<int>(__fns(some, 0, x + 1));
+      s = p.split[range];
+      return true;
+    }
+    x -= n;
+  }
+  return false;
+}
 
 // The item that begins in range c and goes on past it has the parts, in token order,
-// 2c + 1 and then 2c' of the ranges c' = c + 1, ... A warp per row; blockIdx.y takes
-// every gridDim.y-th set of rows.
-template <int D>
+// 2c + 1 and then 2c' of the ranges c' = c + 1, ... A lane joins a row, so that a part's
+// loads are whole lines. WP warps share the parts (each takes every WP-th, and they are
+// added in a fixed order), the others the channels. Bound by the latency of dependent
+// loads: split, sums, values.
+template <int D, int WP>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
-  constexpr int V = D / 32;
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int WC = kJoinWarps / WP;                   // warps side by side
+  constexpr int CG = WP == 1 ? D / 4 / WC : 4;          // a warp's groups of 4 channels
+  constexpr int CH = WC * CG * 4;                       // a block's channels
+  __shared__ float s_out[kJoinRows][CH + 4];
+  __shared__ float s_sum[kJoinRows];
+  __shared__ float4 s_part[WP > 1 ? WP : 1][CG][kJoinRows];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wp = warp % WP, wc = warp / WP;
   // the stream's next launch is ordered behind this grid alone: every block waits
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Split s = p.split[c];
-  if (s.parts == 0) return;
-  auto index = [&](int i, int row) { return (2 * int64_t(c) + (i == 0 ? 1 : 2 * i)) * p.rows + row; };
-  for (int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5); row < s.tokens * p.bheads; row += gridDim.y * kJoinWarps) {
-    const int t = token_of(p, row), h = row - t * p.bheads;
-    if (h >= s.heads) continue;
-    float top = -INFINITY;
-    bool out = false;
-    for (int i = lane; i < s.parts; i += 32) {
-      const float2 ml = p.part_ml[index(i, row)];
-      top = fmaxf(top, ml.x);
-      out |= ml.y == attn::kLeftOut;
-    }
-    if (__any_sync(~0u, out)) continue;  // left out after a wait that ran out
+  Split s;
+  int c;
+  if (!find_split(p, blockIdx.x, c, s)) return;
+  const int row0 = blockIdx.y * kJoinRows, row = row0 + lane;
+  if (row0 >= s.tokens * p.bheads) return;
+  const int ch0 = blockIdx.z * CH;
+  auto part = [&](int i) { return int64_t(2) * c + (i == 0 ? 1 : 2 * i); };
+  float top = -INFINITY;
+  bool out = false;
+#pragma unroll 8
+  for (int i = 0; i < s.parts; ++i) {
+    const float2 ml = p.part_ml[part(i) * p.rows + row];
+    top = fmaxf(top, ml.x);
+    out |= ml.y == attn::kLeftOut;
+  }
+  float sum = 0.0f;
+  float4 v[CG];
 #pragma unroll
-    for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-    float sum = 0.0f, v[V];
-#pragma unroll
-    for (int x = 0; x < V; ++x) v[x] = 0.0f;
+  for (int k = 0; k < CG; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int i = 0; i < s.parts; ++i) {
-      const int64_t at = index(i, row);
-      const float2 ml = p.part_ml[at];
-      // 0 where a part saw nothing (a NaN sum goes on)
-      const float f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : attn::exp2_fast(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
+  for (int i = wp; i < s.parts; i += WP) {
+    const float2 ml = p.part_ml[part(i) * p.rows + row];
+    const float4* src = reinterpret_cast<const float4*>(p.part) + (part(i) * (D / 4) + ch0 / 4 + wc * CG) * p.rows + row;
+    float4 y[CG];
 #pragma unroll
-      for (int x = 0; x < V; x += 2) {
-        const float2 y = *reinterpret_cast<const float2*>(p.part + at * D + lane * V + x);
-        v[x] = fmaf(f, y.x, v[x]), v[x + 1] = fmaf(f, y.y, v[x + 1]);
+    for (int k = 0; k < CG; ++k) y[k] = src[int64_t(k) * p.rows];
+    // 0 where a part saw nothing (a NaN sum goes on)
+    const float f = ml.y == 0.0f ? 0.0f : ml.x == top ? 1.0f : attn::exp2_fast(ml.x - top);
+    sum = fmaf(f, ml.y, sum);
+#pragma unroll
+    for (int k = 0; k < CG; ++k) {
+      v[k].x = fmaf(f, y[k].x, v[k].x), v[k].y = fmaf(f, y[k].y, v[k].y);
+      v[k].z = fmaf(f, y[k].z, v[k].z), v[k].w = fmaf(f, y[k].w, v[k].w);
+    }
+  }
+  if constexpr (WP > 1) {
+    s_out[lane][warp] = sum;  // (joined below)
+#pragma unroll
+    for (int k = 0; k < CG; ++k) s_part[wp][k][lane] = v[k];
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int x = 0; x < WP; ++x) sum += s_out[lane][x];
+#pragma unroll
+    for (int k = 0; k < CG; ++k) {
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int x = 0; x < WP; ++x) {
+        const float4 y = s_part[x][k][lane];
+        v[k].x += y.x, v[k].y += y.y, v[k].z += y.z, v[k].w += y.w;
       }
     }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int64_t at = (int64_t(s.row0 + t) * p.a.num_q_heads + s.head0 + h) * D + lane * V;
+    __syncthreads();
+  }
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (wp == 0) {
 #pragma unroll
-    for (int x = 0; x < V; x += 2) {
-      if (p.a.out_dtype == LIN_F32)
-        *reinterpret_cast<float2*>(static_cast<float*>(p.a.out) + at + x) = make_float2(v[x] * f, v[x + 1] * f);
-      else
-        *reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(p.a.out) + at + x) =
-            __floats2bfloat162_rn(v[x] * f, v[x + 1] * f);
+    for (int k = 0; k < CG; ++k)
+      *reinterpret_cast<float4*>(&s_out[lane][(wc * CG + k) * 4]) = make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f);
+  }
+  if (warp == 0) s_sum[lane] = out ? attn::kLeftOut : 0.0f;
+  __syncthreads();
+  // rows as they lie in the outputs
+  constexpr int PER = CH / 4;  // threads of a row
+  for (int x = threadIdx.x; x < kJoinRows * PER; x += kJoinWarps * 32) {
+    const int r = x / PER, q = row0 + r, t = token_of(p, q), h = q - t * p.bheads;
+    if (t >= s.tokens || h >= s.heads || s_sum[r] == attn::kLeftOut) continue;  // left out after a wait that ran out
+    const float4 y = *reinterpret_cast<const float4*>(&s_out[r][x % PER * 4]);
+    const int64_t at = (int64_t(s.row0 + t) * p.a.num_q_heads + s.head0 + h) * D + ch0 + x % PER * 4;
+    if (p.a.out_dtype == LIN_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at) = y;
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.a.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
     }
   }
 }
@@ -96,6 +158,47 @@ void divide_by(int64_t d, uint32_t& mul, uint32_t& shift) {
   shift = 0;
   while ((int64_t(1) << shift) < d) ++shift;
   mul = static_cast<uint32_t>((((uint64_t(1) << shift) - d) << 32) / d + 1);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }
+  return fn;
+}
+
+// A layer's K or V as [page][head][token][channel], in boxes of 64 channels x `box` tokens.
+// False where the strides are none that a tensor map takes.
+bool encode(CUtensorMap* map, const lin_kv_cache_t& c, void* base, int layer, int box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.head_dim) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.num_kv_heads), static_cast<cuuint64_t>(c.num_pages)};
+  // (the stride of an axis of one is not looked at)
+  const cuuint64_t strides[3] = {c.page_size > 1 ? static_cast<cuuint64_t>(c.token_stride) : row,
+                                 c.num_kv_heads > 1 ? static_cast<cuuint64_t>(c.head_stride) : row,
+                                 c.num_pages > 1 ? static_cast<cuuint64_t>(c.page_stride) : row};
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, ones[4] = {1, 1, 1, 1};
+  char* at = static_cast<char*>(base) + (c.num_layers > 1 ? layer * c.layer_stride : 0);
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, at, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int64_t items, int rows) {
+  const unsigned x = static_cast<unsigned>(items < p.grid ? items : p.grid), y = (rows + kJoinRows - 1) / kJoinRows;
+  if (items * kManyParts > p.grid) {
+    cfg.gridDim = dim3(x, y, 1);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p);
+  }
+  cfg.gridDim = dim3(x, y, D / 16);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, kJoinWarps>, p);
 }
 
 }  // namespace
@@ -136,7 +239,6 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.item_cost = f.item_cost;
   p.scale_log2 = fabsf(a.scale) * 1.4426950408889634f;  // log2(e)
   if (p.scale_log2 < 0x1p-126f) p.scale_log2 = 0x1p-126f;  // not 0: hidden scores are -inf
-  p.slack = attn::kSlack / p.scale_log2;
   p.negate = !(a.scale < 0.0f) ? 0u : c.dtype == LIN_BF16 ? 0x80008000u : 0x80000000u;
   chunk::divide_by(c.page_size, p.page_mul, p.page_shift);
   chunk::divide_by(p.bheads, p.bhead_mul, p.bhead_shift);
@@ -146,15 +248,20 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.part_ml = reinterpret_cast<float2*>(w);
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
+  p.box = 0;
   cudaError_t e;
-  if (f.umma)
-    e = c.head_dim == 64    ? chunk::launch_umma_d64(p, s)
-        : c.head_dim == 128 ? chunk::launch_umma_d128(p, s)
-                            : chunk::launch_umma_d256(p, s);
-  else
+  if (f.umma) {
+    CUtensorMap k = {}, v = {};
+    const int box = c.page_size % 32 == 0 ? 32 : c.page_size % 16 == 0 ? 16 : c.page_size % 8 == 0 ? 8 : 0;
+    if (box && chunk::encode(&k, c, c.k, a.layer, box) && chunk::encode(&v, c, c.v, a.layer, box)) p.box = box;
+    e = c.head_dim == 64    ? chunk::launch_umma_d64(p, k, v, s)
+        : c.head_dim == 128 ? chunk::launch_umma_d128(p, k, v, s)
+                            : chunk::launch_umma_d256(p, k, v, s);
+  } else {
     e = c.head_dim == 64    ? chunk::launch_mma_d64(p, s)
         : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)
                             : chunk::launch_mma_d256(p, s);
+  }
   if (e != cudaSuccess) return e;
   // the join's launch overlaps the main kernel, and it waits there for its end
   cudaLaunchAttribute attr[1];
@@ -164,11 +271,15 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(p.grid, 4);
   cfg.blockDim = dim3(chunk::kJoinWarps * 32);
-  return c.head_dim == 64    ? cudaLaunchKernelEx(&cfg, chunk::join_kernel<64>, p)
-         : c.head_dim == 128 ? cudaLaunchKernelEx(&cfg, chunk::join_kernel<128>, p)
-                             : cudaLaunchKernelEx(&cfg, chunk::join_kernel<256>, p);
+  // Items of the batch at most, and rows of one: few items have many parts each (one
+  // request's last tokens over a long cache), which the warps of a block then share.
+  const int64_t items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
+  const int64_t most = int64_t(a.tokens) * p.bheads;
+  const int rows = most < p.rows ? static_cast<int>(most) : p.rows;
+  return c.head_dim == 64    ? chunk::launch_join<64>(cfg, p, items, rows)
+         : c.head_dim == 128 ? chunk::launch_join<128>(cfg, p, items, rows)
+                             : chunk::launch_join<256>(cfg, p, items, rows);
 }
 
 }  // namespace lin

@@ -14,6 +14,7 @@
 // from one to the next), so no kernel has to lay the items out.
 #pragma once
 
+#include <cuda.h>
 #include <math.h>
 
 #include "attn_common.cuh"
@@ -41,12 +42,12 @@ struct Plan {
   int heads;        // kv heads * blocks
   int tk;           // keys of a tile
   int grid, item_cost;
+  int box;          // tokens of a TMA box of the cache; 0: none
   float scale_log2;  // |scale| log2(e), never 0; q is negated where scale < 0
   uint32_t negate;
-  float slack;       // kSlack in units of q.k
   uint32_t page_mul, page_shift;    // t / page_size = (mulhi(t, mul) + t) >> shift
   uint32_t bhead_mul, bhead_shift;  // row / bheads
-  float* part;       // [2 grid][rows][D] value sums of unfinished pieces
+  float* part;       // [2 grid][D / 4][rows][4] value sums of unfinished pieces: a warp's rows side by side
   float2* part_ml;   // [2 grid][rows] their (maximum, sum)
   Split* split;      // [grid]
 };
@@ -249,11 +250,11 @@ __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
 
 // One translation unit per head_dim and kind of kernel.
 cudaError_t launch_mma_d64(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d64(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d64(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 cudaError_t launch_mma_d128(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d128(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d128(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 cudaError_t launch_mma_d256(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d256(const Plan& p, cudaStream_t s);
+cudaError_t launch_umma_d256(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
 
 }  // namespace chunk
 }  // namespace lin

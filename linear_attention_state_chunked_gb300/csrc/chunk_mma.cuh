@@ -343,9 +343,10 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
                 __floats2bfloat162_rn(o[d][2 * k] * f, o[d][2 * k + 1] * f);
         }
       } else {
-        float* to = p.part + (int64_t(x.part) * p.rows + row) * D + 2 * t4;
+        float* to = p.part + ((int64_t(x.part) * (D / 4) + (t4 >> 1)) * p.rows + row) * 4 + (t4 & 1) * 2;
 #pragma unroll
-        for (int d = 0; d < D / 8; ++d) *reinterpret_cast<float2*>(to + d * 8) = make_float2(o[d][2 * k], o[d][2 * k + 1]);
+        for (int d = 0; d < D / 8; ++d)
+          *reinterpret_cast<float2*>(to + int64_t(d) * 8 * p.rows) = make_float2(o[d][2 * k], o[d][2 * k + 1]);
         if (t4 == 0) p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(m[k], sum);
       }
     }

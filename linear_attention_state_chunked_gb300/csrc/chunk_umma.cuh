@@ -12,14 +12,20 @@
 // makes the next S while the softmax works on the last.
 //
 // Roles: 4 NQ softmax warps (thread = row = tensor-memory lane, so no exchange between
-// threads), 4 warps that load K and V (16-byte asynchronous copies, as pages may end
-// anywhere) into a ring of U units, one that issues the products, one that hands out the
-// pieces (chunk_common.cuh), two that load Q and look over values (below). Each goes
-// through the pieces by itself, so one item's end overlaps the next one's start. P goes
-// back to tensor memory in the place of its S, as the A operand of P V, rounded to bf16:
-// one more rounding of 2^-9 rms beside the output's own; the sums are of the unrounded
-// weights. The reference m moves only when a score passes it by 2^8, so O is rarely
-// rescaled, by the softmax warps themselves.
+// threads), 4 warps that load K and V into a ring of U units, one that issues the
+// products, one that hands out the pieces (chunk_common.cuh), two that load Q and look
+// over values (below). Each goes through the pieces by itself, so one item's end overlaps
+// the next one's start. Pages of a multiple of 8 tokens come by TMA, in boxes of 8, 16 or
+// 32 tokens; others, whose tokens may begin anywhere in a tile's swizzle, by 16-byte
+// asynchronous copies, after which the products need a proxy fence (250 cycles a unit).
+// P goes back to tensor memory in the place of its S, as the A operand of P V, rounded to
+// bf16: one more rounding of 2^-9 rms beside the output's own; the sums are of the
+// unrounded weights.
+//
+// The reference m. A piece's first tile takes its rows' maxima. After that the weights
+// are made at once with the reference at hand, and only where a tile's sum of a row passes
+// 2^8 (or is no number) are the maxima looked up, the row's sums rescaled and the weights
+// made again: a tile in some thousand, which saves the others the pass over the scores.
 //
 // Hidden values: 0 NaN is NaN, so in tiles that some row of the item does not see whole
 // (the last ones) the values are looked over; infinities and NaN are 0 in the product
@@ -35,29 +41,33 @@
 namespace lin {
 namespace chunk {
 
-template <int D_, int NQ_>
+constexpr int kValidRing = 16, kCheckRing = 8;  // tiles, looked-over tiles under way and some more
+
+template <int D_, int NQ_, bool TMA_>
 struct UCfg {
   static constexpr int D = D_, NQ = NQ_;
+  static constexpr bool TMA = TMA_;
   static constexpr int TK = 128;
-  static constexpr int DK = D < 128 ? D : 128;  // channels of a ring unit
+  static constexpr int DK = D == 128 ? 128 : 64;  // channels of a ring unit
   static constexpr int KU = D / DK;             // units of a tile's K, or V
   static constexpr int UNIT = TK * DK * 2;
   static constexpr int QT = 128 * D * 2;        // a row tile's queries
-  static constexpr int FREE = 224 * 1024 - NQ * QT;
-  static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
-  static constexpr int SMEM = U * UNIT + NQ * QT;
   static constexpr int SOFT = 4 * NQ;           // softmax warps
+  static constexpr int STAGE = SOFT * 4096;     // where outputs are turned into rows
+  static constexpr int FREE = 224 * 1024 - NQ * QT - STAGE;
+  static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
+  static constexpr int SMEM = U * UNIT + NQ * QT + STAGE;
   static constexpr int THREADS = SOFT * 32 + 256;
   // tensor memory columns: 2 of S (and P), NQ of O
   static constexpr int T_O = 2 * TK;
   static constexpr int TMEM = 512;
-  static_assert(T_O + NQ * D <= TMEM && U >= 2 * KU, "");
+  static_assert(T_O + NQ * D <= TMEM && U >= 2 * KU && U < 2 * kValidRing, "");
 };
 
 constexpr uint32_t kWaitTries = 1u << 24;
 constexpr int kRun = 256;     // most tiles whose value sums stay in the unit
 constexpr int kPieces = 4;    // pieces handed out ahead
-constexpr int kValidRing = 16, kCheckRing = 8;
+constexpr float kMostSum = 256.0f;  // of a tile's weights, before the reference moves
 
 struct UPiece {
   Piece x;
@@ -81,6 +91,20 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       :
       : "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_many(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(umma::smem_u32(bar)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(umma::smem_u32(bar)), "r"(bytes) : "memory");
+}
+// A box of 64 channels x some tokens of one head and page; zeros where the page is none.
+__device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int channel, int token,
+                                         int head, int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(channel), "r"(token), "r"(head), "r"(page), "r"(umma::smem_u32(bar))
       : "memory");
 }
 // One lane of the warp, always the same (what it does stays in uniform registers).
@@ -129,7 +153,7 @@ __device__ __forceinline__ void landed32(float* v) {
                  "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
                  "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
-__device__ __forceinline__ void tmem_put32(uint32_t at, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_put32(uint32_t at, const uint32_t* v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -141,6 +165,19 @@ __device__ __forceinline__ void tmem_put32(uint32_t at, const uint32_t (&v)[32])
       : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 8 columns of this thread's lane, there and back.
+__device__ __forceinline__ void tmem_get8(uint32_t at, float (&o)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_set8(uint32_t at, const float (&o)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\ttcgen05.wait::st.sync.aligned;" ::"r"(at),
+               "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
+               : "memory");
+}
 
 // A place of the ring and its phase.
 template <int U>
@@ -159,8 +196,11 @@ struct At {
 };
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p) {
+__global__ void __launch_bounds__(C::THREADS, 1)
+chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   constexpr int D = C::D, NQ = C::NQ, TK = C::TK, DK = C::DK, KU = C::KU, U = C::U, NT = C::THREADS, SOFT = C::SOFT;
+  constexpr bool TMA = C::TMA;
+  constexpr int FULL = TMA ? 4 : 128 + 4;  // arrivals of a full unit
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ uint64_t b_full[U], b_empty[U], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
       b_pfull[kPieces], b_pempty[kPieces], b_drain;
@@ -176,10 +216,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
   const lin_kv_cache_t& c = p.c;
   const lin_attn_chunk_args_t& a = p.a;
   if (tid == 0) {
-    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], 128 + 4), umma::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], FULL), umma::mbar_init(&b_empty[i], 1);
     for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
     for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
-    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], 128), umma::mbar_init(&b_check[i], 2);
+    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 4 : 128) * KU), umma::mbar_init(&b_check[i], 2);
     for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 4 + 1 + 2);
     umma::mbar_init(&b_drain, 1);
     umma::mbar_fence_init();
@@ -193,6 +233,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
   umma::fence_after_sync();
   const uint32_t tmem = s_tmem, t_o = tmem + C::T_O;
   unsigned char* const qbuf = smem + U * C::UNIT;
+  unsigned char* const stage = qbuf + NQ * C::QT;
 
   // A warp whose wait runs out waits for nothing more; the others learn of it where
   // they wait, and all go to the end. Called by whole warps, and the same for all lanes.
@@ -212,20 +253,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
   };
   int at_piece = 0;
   uint32_t piece_phase = 0;
-  // The next piece, by a whole warp; false at the end.
-  auto fetch = [&](UPiece& y) {
+  // The next piece, by a whole warp, NULL at the end; what is needed of it is copied
+  // before it is given back.
+  auto take = [&]() -> const UPiece* {
     wait(&b_pfull[at_piece], piece_phase);
-    if (gone) return false;
-    y = s_piece[at_piece];
+    if (gone || s_piece[at_piece].x.r < 0) return nullptr;
+    return &s_piece[at_piece];
+  };
+  auto give_back = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&b_pempty[at_piece]);
     if (++at_piece == kPieces) at_piece = 0, piece_phase ^= 1;
-    return y.x.r >= 0;
   };
 
   if (warp < SOFT) {
     // ---- softmax ------------------------------------------------------------------------
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int st = warp >> 2;  // row tile
     const int row = st * 128 + (tid & 127);
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -235,17 +278,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
     // The product of tile t has ended. (A barrier for each buffer: when S of tile t is
     // there, the product of t - 2 has ended, and that of t - 1 need not have.)
     auto wait_o = [&](uint32_t t) { wait(&b_o[NQ == 2 ? st : t & 1], (NQ == 2 ? t : t >> 1) & 1); };
-    UPiece y;
-    while (fetch(y)) {
+    while (const UPiece* piece = take()) {
+      const UPiece y = *piece;
+      give_back();
       const Piece& x = y.x;
       const int tok = token_of(p, row), head = row - tok * p.bheads;
       const bool mine = tok < x.tokens && head < x.heads;
       const int sees = mine ? max(0, x.pos + tok + 1) : 0;
       const int all_see = max(0, x.pos + token_of(p, st * 128) + 1);  // what every row of the tile sees
       const int nt = st == 0 ? y.nt[0] : y.nt[1];
-      float* const acc = p.part + (int64_t(x.part) * p.rows + row) * D;  // sums of earlier runs
+      float4* const acc = reinterpret_cast<float4*>(p.part) + int64_t(x.part) * (D / 4) * p.rows + row;  // sums of earlier runs
       float cut = -INFINITY, z = 0.0f, l = 0.0f, z_acc = 0.0f;
-      bool has_acc = false;
+      bool has_acc = false, unset = true;
       // looked-over tiles that are not this row tile's
       const int first_chk = max(x.t0, y.check0), chk_before = chk;
       for (int i = 0; i < nt && !gone; ++i) {
@@ -258,7 +302,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll
         for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
         const uint4 valid = s_valid[(y.g0 + i) & (kValidRing - 1)];
-        const bool first = i % kRun == 0;
+        const bool first = i % kRun == 0, fresh = unset;
         tmem_loaded();
 #pragma unroll
         for (int k = 0; k < 128; k += 32) landed32(s + k);
@@ -269,61 +313,95 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll 1
           for (int d = 0; d < D; d += 8) {
             float o[8];
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                         "tcgen05.wait::ld.sync.aligned;"
-                         : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
-                         : "r"(to + d)
-                         : "memory");
+            tmem_get8(to + d, o);
 #pragma unroll
             for (int k = 0; k < 8; k += 4) {
-              float4* m = reinterpret_cast<float4*>(acc + d + k);
+              float4* m = acc + int64_t((d + k) / 4) * p.rows;
               const float4 was = i == kRun ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *m;
               *m = make_float4(fmaf(was.x, f, o[k]), fmaf(was.y, f, o[k + 1]), fmaf(was.z, f, o[k + 2]), fmaf(was.w, f, o[k + 3]));
             }
           }
           z_acc = z, has_acc = cut != -INFINITY;
         }
-        if (p.negate) {
+        const bool masked = key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u;
+        // the scores as the softmax takes them
+        auto see = [&]() {
+          if (p.negate) {
 #pragma unroll
-          for (int k = 0; k < 128; ++k) s[k] = -s[k];
-        }
-        if (key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u) {
-          const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int n = sees - key0 - 32 * h;
-            const uint32_t vis = n <= 0 ? 0u : n >= 32 ? live[h] : live[h] & ((1u << n) - 1u);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (!((vis >> k) & 1u)) s[32 * h + k] = -INFINITY;
+            for (int k = 0; k < 128; ++k) s[k] = -s[k];
           }
-        }
-        float top[4] = {s[0], s[1], s[2], s[3]};
+          if (masked) {
+            const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
 #pragma unroll
-        for (int k = 4; k < 124; k += 8)
+            for (int h = 0; h < 4; ++h) {
+              const int n = sees - key0 - 32 * h;
+              const uint32_t vis = n <= 0 ? 0u : n >= 32 ? live[h] : live[h] & ((1u << n) - 1u);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) top[h] = max3(top[h], s[k + h], s[k + 4 + h]);
+              for (int k = 0; k < 32; ++k)
+                if (!((vis >> k) & 1u)) s[32 * h + k] = -INFINITY;
+            }
+          }
+        };
+        // the reference, and what follows from its move
+        auto refer = [&]() {
+          float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int h = 0; h < 4; ++h) top[h] = fmaxf(top[h], s[124 + h]);
-        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-        float f = 1.0f;
-        if (mx > cut) {
-          const float y0 = -mx * p.scale_log2;
-          f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
-          z = y0, cut = mx + p.slack, l *= f;
-        }
-        if (!first && __any_sync(~0u, f != 1.0f)) {
-          wait_o(ct - 1);  // the last product has ended
-          umma::fence_after_sync();
+          for (int k = 4; k < 124; k += 8)
+#pragma unroll
+            for (int h = 0; h < 4; ++h) top[h] = max3(top[h], s[k + h], s[k + 4 + h]);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) top[h] = fmaxf(top[h], s[124 + h]);
+          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+          float f = 1.0f;
+          if (mx > cut) {
+            const float y0 = -mx * p.scale_log2;
+            f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
+            z = y0, cut = mx, l *= f;
+          }
+          if (!first && __any_sync(~0u, f != 1.0f)) {
+            wait_o(ct - 1);  // the last product has ended
+            umma::fence_after_sync();
 #pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            float o[16];
-            umma::tmem_ld16(to + d, o);
+            for (int d = 0; d < D; d += 8) {
+              float o[8];
+              tmem_get8(to + d, o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] *= f;
-            umma::tmem_st16(to + d, o);
+              for (int k = 0; k < 8; ++k) o[k] *= f;
+              tmem_set8(to + d, o);
+            }
           }
+          // a row that has seen nothing yet, and will see something
+          unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + TK);
+        };
+        uint32_t pk[64];
+        float tile_sum;
+        auto weigh = [&]() {
+          const uint64_t z2 = f2pack(z, z);
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            float e0, e1;
+            f2unpack(ffma2(f2pack(s[2 * k], s[2 * k + 1]), scale2, z2), e0, e1);
+            e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
+            sum[k & 1] = fadd2(sum[k & 1], f2pack(e0, e1));
+            pk[k] = pack_bf16(e0, e1);
+          }
+          tile_sum = f2sum(fadd2(sum[0], sum[1]));
+        };
+        see();
+        if (unset) refer();
+        weigh();
+        if (__any_sync(~0u, !(tile_sum <= kMostSum)) && !fresh) {
+#pragma unroll
+          for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
+          tmem_loaded();
+#pragma unroll
+          for (int k = 0; k < 128; k += 32) landed32(s + k);
+          see();
+          refer();
+          weigh();
         }
+        l += tile_sum;
         if (tile >= y.check0) {
           wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
           const uint4 wv = s_wild[chk & (kCheckRing - 1)];
@@ -336,11 +414,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll 1
             for (int d = 0; d < D; d += 8) {
               float o[8];
-              asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
-                           "tcgen05.wait::ld.sync.aligned;"
-                           : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
-                           : "r"(to + d)
-                           : "memory");
+              tmem_get8(to + d, o);
               if (first) {  // the product adds to these, as it does not start from 0
 #pragma unroll
                 for (int k = 0; k < 8; ++k) o[k] = 0.0f;
@@ -362,29 +436,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
                 }
               }
               __syncwarp();
-              asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-                           "tcgen05.wait::st.sync.aligned;" ::"r"(to + d),
-                           "f"(o[0]), "f"(o[1]), "f"(o[2]), "f"(o[3]), "f"(o[4]), "f"(o[5]), "f"(o[6]), "f"(o[7])
-                           : "memory");
+              tmem_set8(to + d, o);
             }
           }
         }
-        const uint64_t z2 = f2pack(z, z);
-        uint64_t sum[2] = {0, 0};
-#pragma unroll
-        for (int h = 0; h < 128; h += 64) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float e0, e1;
-            f2unpack(ffma2(f2pack(s[h + 2 * k], s[h + 2 * k + 1]), scale2, z2), e0, e1);
-            e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
-            sum[k & 1] = fadd2(sum[k & 1], f2pack(e0, e1));
-            pk[k] = pack_bf16(e0, e1);
-          }
-          tmem_put32(ts + h / 2, pk);
-        }
-        l += f2sum(fadd2(sum[0], sum[1]));
+        tmem_put32(ts, pk);
+        tmem_put32(ts + 32, pk + 32);
         tmem_stored();
         umma::fence_before_sync();
         __syncwarp();
@@ -400,8 +457,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
       umma::fence_after_sync();
       const float fa = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
       const float fo = !x.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
-      uint16_t* const out =
-          static_cast<uint16_t*>(a.out) + (int64_t(x.row0 + tok) * a.num_q_heads + x.head0 + head) * D;
+      unsigned char* const rows = stage + warp * 4096;  // 32 rows of 64 outputs, swizzled
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         float o[32];
@@ -413,24 +469,38 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.0f;
         }
-        if (mine) {  // (the loads are the whole warp's: no lane may leave the loop)
-          if (has_acc) {
+        if (has_acc) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(acc[d + k], fa, o[k]);
-          }
-          if (x.whole) {
-#pragma unroll
-            for (int k = 0; k < 32; k += 8)
-              *reinterpret_cast<uint4*>(out + d + k) =
-                  make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
-                             pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; k += 4)
-              *reinterpret_cast<float4*>(acc + d + k) = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          for (int k = 0; k < 32; k += 4) {
+            const float4 was = acc[int64_t((d + k) / 4) * p.rows];
+            o[k] = fmaf(was.x, fa, o[k]), o[k + 1] = fmaf(was.y, fa, o[k + 1]);
+            o[k + 2] = fmaf(was.z, fa, o[k + 2]), o[k + 3] = fmaf(was.w, fa, o[k + 3]);
           }
         }
-        __syncwarp();
+        if (!x.whole) {  // rows of all lanes side by side
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            acc[int64_t((d + k) / 4) * p.rows] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4*>(rows + lane * 128 + ((((d & 32) + k) / 8 ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
+                           pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
+          if (d & 32) {
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {  // 4 rows at a time, 128 bytes of each
+              const int q = k * 4 + lane / 8, ch = lane & 7;
+              const int r = st * 128 + (warp & 3) * 32 + q, t = token_of(p, r), h = r - t * p.bheads;
+              const uint4 v = *reinterpret_cast<const uint4*>(rows + q * 128 + ((ch ^ (q & 7)) << 4));
+              if (t < x.tokens && h < x.heads)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
+                                          (int64_t(x.row0 + t) * a.num_q_heads + x.head0 + h) * D + d - 32 + ch * 8) = v;
+            }
+            __syncwarp();
+          }
+        }
       }
       if (mine && !x.whole)
         p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(cut == -INFINITY ? cut : -z, l);
@@ -438,54 +508,71 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
     }
   } else if (warp < SOFT + 4) {
     // ---- loads: each warp brings 32 keys of a tile --------------------------------------
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    constexpr int CPR = DK / 8, STEP = 32 / CPR;
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    constexpr int CPR = DK / 8, STEP = 32 / CPR, PAN = DK / 64;
     const int lw = warp - SOFT;
     const uint32_t place = umma::smem_u32(smem) + umma::rp_offset(lw * 32 + lane / CPR, (lane % CPR) * 8, TK);
     At<U> r{0, 0};
     uint32_t chk = 0;
-    UPiece y;
-    while (fetch(y)) {
-      const Piece& x = y.x;
-      const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + x.hk * c.head_stride;
-      const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
-      const int32_t* table = a.page_table + x.r * a.page_table_stride;
-      int key = x.t0 * TK + lw * 32 + lane;
-      int id = key < x.keys && y.n > 0 ? table[page_of(p, key)] : -1;
-      for (int i = 0; i < y.n && !gone; ++i) {
+    while (const UPiece* piece = take()) {
+      const int n = piece->n, g0 = piece->g0, keys = piece->x.keys, hk = piece->x.hk, look0 = piece->check0 - piece->x.t0;
+      const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
+      const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
+      const int32_t* table = a.page_table + piece->x.r * a.page_table_stride;
+      int key = piece->x.t0 * TK + lw * 32 + lane;
+      give_back();
+      int id = key < keys && n > 0 ? table[page_of(p, key)] : -1;
+      for (int i = 0; i < n && !gone; ++i) {
         const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
-        if (key < x.keys && !live) report(a.status, LIN_ST_BAD_PAGE);
-        const int64_t off = live ? id * c.page_stride + (key - page_of(p, key) * c.page_size) * c.token_stride : 0;
+        if (key < keys && !live) report(a.status, LIN_ST_BAD_PAGE);
+        const int in_page = key - page_of(p, key) * c.page_size;
+        const int64_t off = live ? id * c.page_stride + in_page * c.token_stride : 0;
         const uint32_t valid = __ballot_sync(~0u, live);
-        key += TK;
-        id = key < x.keys ? table[page_of(p, key)] : -1;
+        const int next = key + TK < keys ? table[page_of(p, key + TK)] : -1;
+        // values that are looked over go to their barrier, and are full after that
+        const bool look = i >= look0;
+        uint64_t* const to_look = &b_look[chk & (kCheckRing - 1)];
+        if (look) ++chk;
+        // (TMA) this lane's box: its first token's place and page
+        const int box_id = __shfl_sync(~0u, live ? id : c.num_pages, (lane / PAN) * p.box & 31);
+        const int box_row = __shfl_sync(~0u, in_page, (lane / PAN) * p.box & 31);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
           for (int j = 0; j < KU; ++j) {
             wait(&b_empty[r.slot], r.phase ^ 1);
             if (kv == 0 && j == 0 && lane == 0)
-              reinterpret_cast<uint32_t*>(&s_valid[(y.g0 + i) & (kValidRing - 1)])[lw] = valid;
-            const uint32_t dst = place + r.slot * C::UNIT;
-            const char* src = (kv ? vb : kb) + j * (DK * 2) + (lane % CPR) * 16;
+              reinterpret_cast<uint32_t*>(&s_valid[(g0 + i) & (kValidRing - 1)])[lw] = valid;
+            uint64_t* const bar = kv == 1 && look ? to_look : &b_full[r.slot];
+            if constexpr (TMA) {
+              if (lane == 0) mbar_expect(bar, C::UNIT / 4);  // and passes on s_valid
+              __syncwarp();
+              if (lane < (32 / p.box) * PAN)
+                load_box(kv ? &v_map : &k_map,
+                         umma::smem_u32(smem) + r.slot * C::UNIT + (lane % PAN) * (TK * 128) + (lw * 32 + (lane / PAN) * p.box) * 128,
+                         bar, j * DK + (lane % PAN) * 64, box_row, hk, box_id);
+            } else {
+              const uint32_t dst = place + r.slot * C::UNIT;
+              const char* src = (kv ? vb : kb) + j * (DK * 2) + (lane % CPR) * 16;
 #pragma unroll
-            for (int k = 0; k < 32 / STEP; ++k) {
-              const int row = k * STEP + lane / CPR;
-              const int64_t o = __shfl_sync(~0u, off, row);
-              attn::cp16((dst ^ ((k * STEP & 7) << 4)) + k * STEP * 128, src + o, (valid >> row) & 1u);
+              for (int k = 0; k < 32 / STEP; ++k) {
+                const int row = k * STEP + lane / CPR;
+                const int64_t o = __shfl_sync(~0u, off, row);
+                attn::cp16((dst ^ ((k * STEP & 7) << 4)) + k * STEP * 128, src + o, (valid >> row) & 1u);
+              }
+              // full when every lane's copies have landed: nobody waits here
+              arrive_copies(bar);
+              if (!(kv == 1 && look) && lane == 0) mbar_arrive(bar);  // and passes on s_valid
             }
-            // full when every lane's copies have landed: nobody waits here
-            arrive_copies(&b_full[r.slot]);
-            if (lane == 0) mbar_arrive(&b_full[r.slot]);  // and passes on s_valid
-            if (kv == 1 && j == KU - 1 && x.t0 + i >= y.check0) arrive_copies(&b_look[chk++ & (kCheckRing - 1)]);
             r.step(1);
           }
+        key += TK, id = next;
       }
       if (gone) break;
     }
     attn::cp_wait_all();
   } else {
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == SOFT + 4) {
       // ---- products ----------------------------------------------------------------------
       constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
@@ -503,7 +590,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
           const At<U> q = r.plus(j);
           wait(&b_full[q.slot], q.phase);
         }
-        umma::fence_smem_to_async();
+        if (!TMA) umma::fence_smem_to_async();
       };
       auto free_units = [&](const At<U>& r) {  // the elected lane
 #pragma unroll
@@ -532,15 +619,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
         }
         umma::mma_commit(&b_o[buf]);
       };
-      // the next piece with tiles
-      auto next_piece = [&](UPiece& y) {
+      // the next piece with tiles: how many, of each row tile, and the first looked over
+      struct Tiles {
+        int n, nt[NQ], look0;
+      };
+      auto next_piece = [&](Tiles& y) {
         do {
-          if (!fetch(y)) return false;
+          const UPiece* piece = take();
+          if (!piece) return false;
+          y.n = piece->n, y.look0 = piece->check0 - piece->x.t0;
+#pragma unroll
+          for (int st = 0; st < NQ; ++st) y.nt[st] = piece->nt[st];
+          give_back();
         } while (y.n == 0);
         return true;
       };
       // the first S of a piece
-      auto begin = [&](const UPiece& y) {
+      auto begin = [&](const Tiles& y) {
         wait_units(rk);
 #pragma unroll
         for (int st = 0; st < NQ; ++st) {
@@ -556,7 +651,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
         __syncwarp();
         rk.step(2 * KU);
       };
-      UPiece y, after;
+      Tiles y, after;
       bool have = next_piece(y);
       if (have) begin(y);
       while (have && !gone) {
@@ -575,11 +670,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
           }
           wait_units(rv);
           uint32_t add = i % kRun != 0;
-          if (y.x.t0 + i >= y.check0) {
-            wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
-            const uint4 wv = s_wild[chk & (kCheckRing - 1)];
+          if (i >= y.look0) {  // (its values are full once they are looked over)
+            const uint4 wv = s_wild[chk++ & (kCheckRing - 1)];
             if (wv.x | wv.y | wv.z | wv.w) add = 1;
-            ++chk;
           }
           if (NQ == 2 && !end) wait_units(rk);
 #pragma unroll
@@ -637,6 +730,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
               y.n = max(y.n, y.nt[st]);
             }
             if (x.keys > max(0, x.pos + 1)) y.check0 = max(0, x.pos + 1) / TK;
+            // TMA brings what lies behind the last key in its box
+            if (TMA && x.keys % p.box) y.check0 = min(y.check0, x.keys / TK);
             g += y.n;
           }
           bool free = false;
@@ -659,29 +754,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
       const int me = tid - (SOFT + 6) * 32;
       At<U> rv{KU, 0};
       uint32_t qn[2] = {0, 0}, chk = 0;
-      UPiece y;
-      while (fetch(y)) {
-        const Piece& x = y.x;
+      while (const UPiece* piece = take()) {
+        const int n = piece->n, look0 = piece->check0 - piece->x.t0, tokens = piece->x.tokens, heads = piece->x.heads;
+        const int nt[2] = {piece->nt[0], piece->nt[1]};
+        const char* const src = static_cast<const char*>(a.q) + int64_t(piece->x.row0) * a.token_stride + int64_t(piece->x.head0) * (D * 2);
+        give_back();
 #pragma unroll
         for (int st = 0; st < NQ; ++st) {
-          if (y.nt[st] == 0) continue;
+          if (nt[st] == 0) continue;
           wait(&b_qfree[st], (qn[st] & 1) ^ 1);
           if (gone) break;
           ++qn[st];
           const uint32_t dst = umma::smem_u32(qbuf) + st * C::QT;
-          const char* src = static_cast<const char*>(a.q) + int64_t(x.row0) * a.token_stride + int64_t(x.head0) * (D * 2);
 #pragma unroll 4
           for (int k = me; k < 128 * CPR; k += 64) {
             const int row = k / CPR, ch = k % CPR;
             const int t = token_of(p, st * 128 + row), h = st * 128 + row - t * p.bheads;
-            const bool live = t < x.tokens && h < x.heads;
+            const bool live = t < tokens && h < heads;
             attn::cp16(dst + umma::rp_offset(row, ch * 8, 128),
                        src + (live ? t * a.token_stride + h * (D * 2) + ch * 16 : 0), live);
           }
           arrive_copies(&b_qfull[st]);
         }
-        for (int i = 0; i < y.n && !gone; ++i) {
-          if (x.t0 + i >= y.check0) {
+        for (int i = 0; i < n && !gone; ++i) {
+          if (i >= look0) {
             // (a barrier of these tiles alone: the ring's may be many phases behind)
             wait(&b_look[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
             if (gone) break;
@@ -706,11 +802,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
                 }
             }
             umma::fence_smem_to_async();
+            __syncwarp();
             const uint32_t w0 = __ballot_sync(~0u, wild[0]), w1 = __ballot_sync(~0u, wild[1]);
             if (lane == 0) {
               uint32_t* to = reinterpret_cast<uint32_t*>(&s_wild[chk & (kCheckRing - 1)]) + (warp - SOFT - 6);
               to[0] = w0, to[2] = w1;
               mbar_arrive(&b_check[chk & (kCheckRing - 1)]);
+#pragma unroll
+              for (int j = 0; j < KU; ++j) mbar_arrive_many(&b_full[rv.plus(j).slot], FULL / 2);
             }
             ++chk;
           }
@@ -732,7 +831,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) chunk_umma_kernel(const Plan p)
 }
 
 template <class C>
-cudaError_t launch_umma(const Plan& p, cudaStream_t s) {
+cudaError_t launch_umma(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   auto kern = chunk_umma_kernel<C>;
   static bool ready[kMaxDevices];  // set twice at worst, to the same value
   int dev = 0;
@@ -743,15 +842,20 @@ cudaError_t launch_umma(const Plan& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
-  kern<<<p.grid, C::THREADS, C::SMEM, s>>>(p);
+  kern<<<p.grid, C::THREADS, C::SMEM, s>>>(p, k, v);
   return cudaGetLastError();
 }
 
+template <int D, int NQ>
+cudaError_t launch_umma_loads(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  return p.box ? launch_umma<UCfg<D, NQ, true>>(p, k, v, s) : launch_umma<UCfg<D, NQ, false>>(p, k, v, s);
+}
+
 template <int D>
-cudaError_t launch_umma_tiles(const Plan& p, cudaStream_t s) {
+cudaError_t launch_umma_tiles(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
   if constexpr (D <= 128)
-    if (p.rows == 256) return launch_umma<UCfg<D, 2>>(p, s);
-  return launch_umma<UCfg<D, 1>>(p, s);
+    if (p.rows == 256) return launch_umma_loads<D, 2>(p, k, v, s);
+  return launch_umma_loads<D, 1>(p, k, v, s);
 }
 
 }  // namespace chunk

@@ -5,7 +5,9 @@
 namespace lin {
 namespace chunk {
 
-cudaError_t launch_umma_d128(const Plan& p, cudaStream_t s) { return launch_umma_tiles<128>(p, s); }
+cudaError_t launch_umma_d128(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+  return launch_umma_tiles<128>(p, k, v, s);
+}
 
 }  // namespace chunk
 }  // namespace lin
