@@ -7,17 +7,19 @@
 // flops per visible (row, key); by HBM for a few rows over a long cache.
 //
 // An item has NQ row tiles. Two (heads of 64 and 128): the unit makes O += P V and the
-// next S of one while the softmax warps of the other work. One (heads of 256, whose O
-// alone takes half of tensor memory, and few rows): S has two buffers, and the unit
-// makes the next S while the softmax works on the last.
+// next S of one while the softmax warps of the other work; a warp each issues them, as an
+// issue waits until the unit is near it. One (heads of 256, whose O alone takes half of
+// tensor memory, and few rows): S has two buffers, and the unit makes the next S while the
+// softmax works on the last; a warp issues S, another P V.
 //
 // Roles: 4 NQ softmax warps (thread = row = tensor-memory lane, so no exchange between
-// threads), 4 warps that load K and V into a ring of U units, one that issues the
-// products, one that hands out the pieces (chunk_common.cuh), two that load Q and look
+// threads), a warp that loads K and one that loads V, each into a ring of its own, two that
+// issue products, one that hands out the pieces (chunk_common.cuh), two that load Q and look
 // over values (below). Each goes through the pieces by itself, so one item's end overlaps
 // the next one's start. Pages of a multiple of 8 tokens come by TMA, in boxes of 8, 16 or
 // 32 tokens; others, whose tokens may begin anywhere in a tile's swizzle, by 16-byte
-// asynchronous copies, after which the products need a proxy fence (250 cycles a unit).
+// asynchronous copies, after which the products need a proxy fence.
+//
 // P goes back to tensor memory in the place of its S, as the A operand of P V, rounded to
 // bf16: one more rounding of 2^-9 rms beside the output's own; the sums are of the
 // unrounded weights.
@@ -48,20 +50,22 @@ struct UCfg {
   static constexpr int D = D_, NQ = NQ_;
   static constexpr bool TMA = TMA_;
   static constexpr int TK = 128;
-  static constexpr int DK = D == 128 ? 128 : 64;  // channels of a ring unit
-  static constexpr int KU = D / DK;             // units of a tile's K, or V
-  static constexpr int UNIT = TK * DK * 2;
+  // a ring unit: 64 channels of a tile's K, up to 128 of its V
+  static constexpr int KU = D / 64, KB = TK * 64 * 2;
+  static constexpr int DV = D < 128 ? D : 128, VU = D / DV, VB = TK * DV * 2;
   static constexpr int QT = 128 * D * 2;        // a row tile's queries
   static constexpr int SOFT = 4 * NQ;           // softmax warps
   static constexpr int STAGE = SOFT * 4096;     // where outputs are turned into rows
-  static constexpr int FREE = 224 * 1024 - NQ * QT - STAGE;
-  static constexpr int U = FREE / UNIT < 12 ? FREE / UNIT : 12;
-  static constexpr int SMEM = U * UNIT + NQ * QT + STAGE;
+  // units of the rings: at least a tile of each
+  static constexpr int NK = D == 64 ? (NQ == 2 ? 5 : 6) : D == 256 ? 5 : NQ == 2 ? 4 : 6;
+  static constexpr int NV = D == 64 ? (NQ == 2 ? 5 : 6) : 2;
+  static constexpr int RING = NK * KB + NV * VB;
+  static constexpr int SMEM = RING + NQ * QT + STAGE;
   static constexpr int THREADS = SOFT * 32 + 256;
   // tensor memory columns: 2 of S (and P), NQ of O
   static constexpr int T_O = 2 * TK;
   static constexpr int TMEM = 512;
-  static_assert(T_O + NQ * D <= TMEM && U >= 2 * KU && U < 2 * kValidRing, "");
+  static_assert(T_O + NQ * D <= TMEM && NK >= KU && NV >= VU && SMEM <= 224 * 1024, "");
 };
 
 constexpr uint32_t kWaitTries = 1u << 24;
@@ -198,11 +202,12 @@ struct At {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
 chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-  constexpr int D = C::D, NQ = C::NQ, TK = C::TK, DK = C::DK, KU = C::KU, U = C::U, NT = C::THREADS, SOFT = C::SOFT;
+  constexpr int D = C::D, NQ = C::NQ, TK = C::TK, KU = C::KU, VU = C::VU, DV = C::DV, NK = C::NK, NV = C::NV;
+  constexpr int NT = C::THREADS, SOFT = C::SOFT;
   constexpr bool TMA = C::TMA;
-  constexpr int FULL = TMA ? 4 : 128 + 4;  // arrivals of a full unit
+  constexpr int KFULL = TMA ? 1 : 32 + 1, VFULL = TMA ? 2 : 32 + 2;  // arrivals of a full unit
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ uint64_t b_full[U], b_empty[U], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
+  __shared__ uint64_t b_kfull[NK], b_kempty[NK], b_vfull[NV], b_vempty[NV], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
       b_pfull[kPieces], b_pempty[kPieces], b_drain;
   __shared__ UPiece s_piece[kPieces];
   __shared__ uint4 s_valid[kValidRing];  // live keys of a tile; a ring of tiles
@@ -216,23 +221,25 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   const lin_kv_cache_t& c = p.c;
   const lin_attn_chunk_args_t& a = p.a;
   if (tid == 0) {
-    for (int i = 0; i < U; ++i) umma::mbar_init(&b_full[i], FULL), umma::mbar_init(&b_empty[i], 1);
+    for (int i = 0; i < NK; ++i) umma::mbar_init(&b_kfull[i], KFULL), umma::mbar_init(&b_kempty[i], NQ);
+    for (int i = 0; i < NV; ++i) umma::mbar_init(&b_vfull[i], VFULL), umma::mbar_init(&b_vempty[i], NQ);
     for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
     for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
-    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 4 : 128) * KU), umma::mbar_init(&b_check[i], 2);
-    for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 4 + 1 + 2);
-    umma::mbar_init(&b_drain, 1);
+    for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 1 : 32) * VU), umma::mbar_init(&b_check[i], 2);
+    for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 2 + 2 + 2);
+    umma::mbar_init(&b_drain, 2);
     umma::mbar_fence_init();
     s_dead = 0;
   }
   Walk w;
   if (!walk_begin<NT>(p, w, s_walk)) return;
-  if (warp == SOFT + 4) umma::tmem_alloc(&s_tmem, C::TMEM);
+  if (warp == SOFT + 2) umma::tmem_alloc(&s_tmem, C::TMEM);
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
   const uint32_t tmem = s_tmem, t_o = tmem + C::T_O;
-  unsigned char* const qbuf = smem + U * C::UNIT;
+  unsigned char* const vbuf = smem + NK * C::KB;
+  unsigned char* const qbuf = smem + C::RING;
   unsigned char* const stage = qbuf + NQ * C::QT;
 
   // A warp whose wait runs out waits for nothing more; the others learn of it where
@@ -268,7 +275,10 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
 
   if (warp < SOFT) {
     // ---- softmax ------------------------------------------------------------------------
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    if constexpr (NQ == 2)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const int st = warp >> 2;  // row tile
     const int row = st * 128 + (tid & 127);
     const uint32_t t_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -298,14 +308,8 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         const uint32_t ts = tmem + t_lane + buf * TK;
         wait(&b_s[buf], (NQ == 2 ? ct : ct >> 1) & 1);
         umma::fence_after_sync();
-        float s[128];
-#pragma unroll
-        for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
         const uint4 valid = s_valid[(y.g0 + i) & (kValidRing - 1)];
-        const bool first = i % kRun == 0, fresh = unset;
-        tmem_loaded();
-#pragma unroll
-        for (int k = 0; k < 128; k += 32) landed32(s + k);
+        const bool first = i % kRun == 0;
         if (first && i > 0) {  // a run's end: its sums to the workspace
           wait_o(ct - 1);
           umma::fence_after_sync();
@@ -323,6 +327,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           }
           z_acc = z, has_acc = cut != -INFINITY;
         }
+        float s[128];
         const bool masked = key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u;
         // the scores as the softmax takes them
         auto see = [&]() {
@@ -388,18 +393,16 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           }
           tile_sum = f2sum(fadd2(sum[0], sum[1]));
         };
-        see();
-        if (unset) refer();
-        weigh();
-        if (__any_sync(~0u, !(tile_sum <= kMostSum)) && !fresh) {
+        for (bool look_up = unset;; look_up = true) {
 #pragma unroll
           for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
           tmem_loaded();
 #pragma unroll
           for (int k = 0; k < 128; k += 32) landed32(s + k);
           see();
-          refer();
+          if (look_up) refer();
           weigh();
+          if (look_up || !__any_sync(~0u, !(tile_sum <= kMostSum))) break;
         }
         l += tile_sum;
         if (tile >= y.check0) {
@@ -506,211 +509,234 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         p.part_ml[int64_t(x.part) * p.rows + row] = make_float2(cut == -INFINITY ? cut : -z, l);
       __syncwarp();
     }
-  } else if (warp < SOFT + 4) {
-    // ---- loads: each warp brings 32 keys of a tile --------------------------------------
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    constexpr int CPR = DK / 8, STEP = 32 / CPR, PAN = DK / 64;
-    const int lw = warp - SOFT;
-    const uint32_t place = umma::smem_u32(smem) + umma::rp_offset(lw * 32 + lane / CPR, (lane % CPR) * 8, TK);
-    At<U> r{0, 0};
-    uint32_t chk = 0;
-    while (const UPiece* piece = take()) {
-      const int n = piece->n, g0 = piece->g0, keys = piece->x.keys, hk = piece->x.hk, look0 = piece->check0 - piece->x.t0;
-      const char* kb = static_cast<const char*>(c.k) + a.layer * c.layer_stride + hk * c.head_stride;
-      const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + hk * c.head_stride;
-      const int32_t* table = a.page_table + piece->x.r * a.page_table_stride;
-      int key = piece->x.t0 * TK + lw * 32 + lane;
-      give_back();
-      int id = key < keys && n > 0 ? table[page_of(p, key)] : -1;
-      for (int i = 0; i < n && !gone; ++i) {
-        const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
-        if (key < keys && !live) report(a.status, LIN_ST_BAD_PAGE);
-        const int in_page = key - page_of(p, key) * c.page_size;
-        const int64_t off = live ? id * c.page_stride + in_page * c.token_stride : 0;
-        const uint32_t valid = __ballot_sync(~0u, live);
-        const int next = key + TK < keys ? table[page_of(p, key + TK)] : -1;
-        // values that are looked over go to their barrier, and are full after that
-        const bool look = i >= look0;
-        uint64_t* const to_look = &b_look[chk & (kCheckRing - 1)];
-        if (look) ++chk;
-        // (TMA) this lane's box: its first token's place and page
-        const int box_id = __shfl_sync(~0u, live ? id : c.num_pages, (lane / PAN) * p.box & 31);
-        const int box_row = __shfl_sync(~0u, in_page, (lane / PAN) * p.box & 31);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-          for (int j = 0; j < KU; ++j) {
-            wait(&b_empty[r.slot], r.phase ^ 1);
-            if (kv == 0 && j == 0 && lane == 0)
-              reinterpret_cast<uint32_t*>(&s_valid[(g0 + i) & (kValidRing - 1)])[lw] = valid;
-            uint64_t* const bar = kv == 1 && look ? to_look : &b_full[r.slot];
-            if constexpr (TMA) {
-              if (lane == 0) mbar_expect(bar, C::UNIT / 4);  // and passes on s_valid
-              __syncwarp();
-              if (lane < (32 / p.box) * PAN)
-                load_box(kv ? &v_map : &k_map,
-                         umma::smem_u32(smem) + r.slot * C::UNIT + (lane % PAN) * (TK * 128) + (lw * 32 + (lane / PAN) * p.box) * 128,
-                         bar, j * DK + (lane % PAN) * 64, box_row, hk, box_id);
-            } else {
-              const uint32_t dst = place + r.slot * C::UNIT;
-              const char* src = (kv ? vb : kb) + j * (DK * 2) + (lane % CPR) * 16;
-#pragma unroll
-              for (int k = 0; k < 32 / STEP; ++k) {
-                const int row = k * STEP + lane / CPR;
-                const int64_t o = __shfl_sync(~0u, off, row);
-                attn::cp16((dst ^ ((k * STEP & 7) << 4)) + k * STEP * 128, src + o, (valid >> row) & 1u);
-              }
-              // full when every lane's copies have landed: nobody waits here
-              arrive_copies(bar);
-              if (!(kv == 1 && look) && lane == 0) mbar_arrive(bar);  // and passes on s_valid
-            }
-            r.step(1);
-          }
-        key += TK, id = next;
-      }
-      if (gone) break;
-    }
-    attn::cp_wait_all();
   } else {
-    if constexpr (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == SOFT + 4) {
+    if constexpr (NQ == 2)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 128;");
+    if (warp < SOFT + 2) {
+      // ---- loads of K (first warp) and V --------------------------------------------------
+      const bool is_v = warp == SOFT + 1;
+      At<NK> rk{0, 0};
+      At<NV> rv{0, 0};
+      uint32_t chk = 0;
+      while (const UPiece* piece = take()) {
+        const int n = piece->n, g0 = piece->g0, keys = piece->x.keys, hk = piece->x.hk, look0 = piece->check0 - piece->x.t0;
+        const int32_t* table = a.page_table + piece->x.r * a.page_table_stride;
+        int key0 = piece->x.t0 * TK;
+        give_back();
+        // (TMA) lane b has box b of a tile
+        int key = key0 + lane * p.box, id = -1;
+        auto look = [&](int k) { return lane * p.box < TK && k < keys ? table[page_of(p, k)] : -1; };
+        if (TMA && n > 0) id = look(key);
+        for (int i = 0; i < n && !gone; ++i) {
+          uint32_t valid = 0;  // of keys 32 lane and on, in lanes 0 to 3
+          bool live = false;
+          int in_page = 0, page = 0;
+          int64_t off[4];      // (no TMA) of keys lane, lane + 32, ...
+          if constexpr (TMA) {
+            live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
+            if (!is_v && lane * p.box < TK && key < keys && !live) report(a.status, LIN_ST_BAD_PAGE);
+            in_page = key - page_of(p, key) * c.page_size;
+            const uint32_t some = __ballot_sync(~0u, live);
+            const uint32_t whole = p.box == 32 ? ~0u : (1u << p.box) - 1u;
+            for (int b = 0; b < 32; b += p.box)
+              if ((some >> ((32 * lane + b) / p.box & 31)) & 1u) valid |= whole << b;
+            const int left = keys - key0 - 32 * lane;
+            if (left < 32) valid = left <= 0 ? 0u : valid & ((1u << left) - 1u);
+            page = live ? id : c.num_pages;  // (past the last: zeros)
+            key += TK;
+            id = look(key);
+          } else {
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int k = key0 + 32 * h + lane;
+              const int pg = page_of(p, k), at = k < keys ? table[pg] : -1;
+              const bool ok = static_cast<uint32_t>(at) < static_cast<uint32_t>(c.num_pages);
+              if (!is_v && k < keys && !ok) report(a.status, LIN_ST_BAD_PAGE);
+              off[h] = ok ? at * c.page_stride + (k - pg * c.page_size) * c.token_stride : 0;
+              const uint32_t some = __ballot_sync(~0u, ok);
+              if (lane == h) valid = some;
+            }
+          }
+          key0 += TK;
+          // 16-byte copies of a unit's rows, `chunks` to each, from channel ch0 on
+          auto copies = [&](const void* base, uint32_t dst, int chunks, int ch0) {
+            const char* src = static_cast<const char*>(base) + a.layer * c.layer_stride + hk * c.head_stride + ch0 * 2;
+            const int step = 32 / chunks, ch = lane % chunks;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t ok = __shfl_sync(~0u, valid, h);
+#pragma unroll 4
+              for (int x = 0; x < 32; x += step) {
+                const int row = x + lane / chunks;
+                const int64_t o = __shfl_sync(~0u, off[h], row);
+                attn::cp16(dst + umma::rp_offset(32 * h + row, ch * 8, TK), src + o + ch * 16, (ok >> row) & 1u);
+              }
+            }
+          };
+          if (!is_v) {
+#pragma unroll 1
+            for (int j = 0; j < KU; ++j) {
+              wait(&b_kempty[rk.slot], rk.phase ^ 1);
+              if (j == 0 && lane < 4) reinterpret_cast<uint32_t*>(&s_valid[(g0 + i) & (kValidRing - 1)])[lane] = valid;
+              __syncwarp();
+              const uint32_t dst = umma::smem_u32(smem) + rk.slot * C::KB;
+              if constexpr (TMA) {
+                if (lane == 0) mbar_expect(&b_kfull[rk.slot], C::KB);  // and passes on s_valid
+                __syncwarp();
+                if (lane * p.box < TK)
+                  load_box(&k_map, dst + lane * p.box * 128, &b_kfull[rk.slot], j * 64, in_page, hk, page);
+              } else {
+                copies(c.k, dst, 8, j * 64);
+                arrive_copies(&b_kfull[rk.slot]);  // when they have landed: nobody waits here
+                if (lane == 0) mbar_arrive(&b_kfull[rk.slot]);
+              }
+              rk.step(1);
+            }
+          } else {
+            // values that are looked over go to their barrier, and are full after that
+            const bool looked = i >= look0;
+            uint64_t* const to_look = &b_look[chk & (kCheckRing - 1)];
+            if (looked) ++chk;
+#pragma unroll 1
+            for (int j = 0; j < VU; ++j) {
+              wait(&b_vempty[rv.slot], rv.phase ^ 1);
+              const uint32_t dst = umma::smem_u32(vbuf) + rv.slot * C::VB;
+              uint64_t* const bar = looked ? to_look : &b_vfull[rv.slot];
+              if constexpr (TMA) {
+                if (lane == 0) {
+                  mbar_expect(bar, C::VB);
+                  if (!looked) mbar_arrive(bar);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < DV / 64; ++h)
+                  if (lane * p.box < TK)
+                    load_box(&v_map, dst + h * (TK * 128) + lane * p.box * 128, bar, j * DV + h * 64, in_page, hk, page);
+              } else {
+                copies(c.v, dst, DV / 8, j * DV);
+                arrive_copies(bar);
+                if (!looked && lane == 0) mbar_arrive_many(bar, 2);
+              }
+              rv.step(1);
+            }
+          }
+        }
+        if (gone) break;
+      }
+      if (gone) {  // copies in flight land before the block ends
+        auto land = [&](uint64_t* bar, uint32_t parity) {
+          for (uint32_t i = 0; i < kWaitTries >> 8 && !umma::mbar_try_wait(bar, parity); ++i) {
+          }
+        };
+        for (int j = 0; !is_v && j < NK; ++j) land(&b_kfull[j], j < rk.slot ? rk.phase : rk.phase ^ 1);
+        for (int j = 0; is_v && j < NV; ++j) land(&b_vfull[j], j < rv.slot ? rv.phase : rv.phase ^ 1);
+        for (uint32_t j = 0; is_v && j < kCheckRing && j < chk; ++j) land(&b_look[(chk - 1 - j) & (kCheckRing - 1)], ((chk - 1 - j) / kCheckRing) & 1);
+      }
+      attn::cp_wait_all();
+    } else if (warp < SOFT + 4) {
       // ---- products ----------------------------------------------------------------------
       constexpr uint32_t id_s = umma::idesc_f16(128, TK, true, false, false);
-      constexpr uint32_t id_o = umma::idesc_f16(128, DK, true, false, true);
+      constexpr uint32_t id_o = umma::idesc_f16(128, DV, true, false, true);
       const uint64_t q_desc = umma::desc_kmajor(umma::smem_u32(qbuf), 128, 0);
       const uint64_t k_desc = umma::desc_kmajor(umma::smem_u32(smem), TK, 0);
-      const uint64_t v_desc = umma::desc_mnmajor(umma::smem_u32(smem), TK, 0);
-      auto kstep = [](int k) { return uint64_t(((k >> 6) * 128 * 128 + (k & 63) * 2) >> 4); };
-      At<U> rk{0, 0}, rv{KU, 0};
-      uint32_t ct[2] = {0, 0}, qn[2] = {0, 0}, chk = 0;
-      // (every lane waits, one issues; called by the whole warp)
-      auto wait_units = [&](const At<U>& r) {
+      const uint64_t v_desc = umma::desc_mnmajor(umma::smem_u32(vbuf), TK, 0);
+      const int me = warp - SOFT - 2;                // NQ 2: the row tile; NQ 1: S, or P V
+      const int st = NQ == 2 ? me : 0;
+      At<NK> rk{0, 0};
+      At<NV> rv{0, 0};
+      uint32_t ct = 0, qn = 0, chk = 0;
+      // (whole warps wait, and one lane issues)
+      // S of the next tile of K into buffer buf; left out: the tile is passed by
+      auto make_s = [&](int buf, bool use, bool last) {
 #pragma unroll
         for (int j = 0; j < KU; ++j) {
-          const At<U> q = r.plus(j);
-          wait(&b_full[q.slot], q.phase);
-        }
-        if (!TMA) umma::fence_smem_to_async();
-      };
-      auto free_units = [&](const At<U>& r) {  // the elected lane
-#pragma unroll
-        for (int j = 0; j < KU; ++j) umma::mma_commit(&b_empty[r.plus(j).slot]);
-      };
-      // S of row tile st into buffer buf; the elected lane
-      auto issue_s = [&](int st, int buf, bool last) {
-#pragma unroll
-        for (int j = 0; j < KU; ++j) {
-          const uint64_t kd = k_desc + rk.plus(j).slot * (C::UNIT >> 4);
-#pragma unroll
-          for (int k = 0; k < DK; k += 16)
-            umma::mma_f16(tmem + buf * TK, q_desc + st * (C::QT >> 4) + kstep(j * DK + k), kd + kstep(k), id_s, j + k > 0);
-        }
-        umma::mma_commit(&b_s[buf]);
-        if (last) umma::mma_commit(&b_qfree[st]);
-        mbar_arrive(&b_s[buf]);  // passes on what the loaders wrote besides the tile
-      };
-      auto issue_o = [&](int st, int buf, uint32_t add) {
-#pragma unroll
-        for (int j = 0; j < KU; ++j) {
-          const uint64_t vd = v_desc + rv.plus(j).slot * (C::UNIT >> 4);
-#pragma unroll
-          for (int k = 0; k < TK; k += 16)
-            mma_ts(t_o + st * D + j * DK, tmem + buf * TK + k / 2, vd + ((k * 128) >> 4), id_o, k > 0 ? 1u : add);
-        }
-        umma::mma_commit(&b_o[buf]);
-      };
-      // the next piece with tiles: how many, of each row tile, and the first looked over
-      struct Tiles {
-        int n, nt[NQ], look0;
-      };
-      auto next_piece = [&](Tiles& y) {
-        do {
-          const UPiece* piece = take();
-          if (!piece) return false;
-          y.n = piece->n, y.look0 = piece->check0 - piece->x.t0;
-#pragma unroll
-          for (int st = 0; st < NQ; ++st) y.nt[st] = piece->nt[st];
-          give_back();
-        } while (y.n == 0);
-        return true;
-      };
-      // the first S of a piece
-      auto begin = [&](const Tiles& y) {
-        wait_units(rk);
-#pragma unroll
-        for (int st = 0; st < NQ; ++st) {
-          if (y.nt[st] == 0) continue;
-          wait(&b_qfull[st], qn[st] & 1);
-          ++qn[st];
-          umma::fence_smem_to_async();
-          umma::fence_after_sync();
-          if (elect_one()) issue_s(st, NQ == 2 ? st : ct[0] & 1, y.nt[st] == 1);
-          __syncwarp();
-        }
-        if (elect_one()) free_units(rk);
-        __syncwarp();
-        rk.step(2 * KU);
-      };
-      Tiles y, after;
-      bool have = next_piece(y);
-      if (have) begin(y);
-      while (have && !gone) {
-        bool more = false;
-        for (int i = 0; i < y.n && !gone; ++i) {
-          const bool end = i + 1 == y.n;
-          if (NQ == 1 && !end) {  // the next S goes first
-            wait_units(rk);
+          wait(&b_kfull[rk.slot], rk.phase);
+          if (!TMA) umma::fence_smem_to_async();
+          if (use) {
             umma::fence_after_sync();
             if (elect_one()) {
-              issue_s(0, (ct[0] + 1) & 1, i + 2 == y.n);
-              free_units(rk);
+              const uint64_t kd = k_desc + rk.slot * (C::KB >> 4), qd = q_desc + ((st * C::QT + j * (128 * 128)) >> 4);
+#pragma unroll
+              for (int k = 0; k < 64; k += 16) umma::mma_f16(tmem + buf * TK, qd + (k * 2 >> 4), kd + (k * 2 >> 4), id_s, j + k > 0);
+              if (j == KU - 1) {
+                umma::mma_commit(&b_s[buf]);
+                if (last) umma::mma_commit(&b_qfree[st]);
+                mbar_arrive(&b_s[buf]);  // passes on what the loader wrote besides the tile
+              }
+              umma::mma_commit(&b_kempty[rk.slot]);
             }
             __syncwarp();
-            rk.step(2 * KU);
+          } else if (lane == 0) {
+            mbar_arrive(&b_kempty[rk.slot]);
           }
-          wait_units(rv);
-          uint32_t add = i % kRun != 0;
-          if (i >= y.look0) {  // (its values are full once they are looked over)
-            const uint4 wv = s_wild[chk++ & (kCheckRing - 1)];
-            if (wv.x | wv.y | wv.z | wv.w) add = 1;
-          }
-          if (NQ == 2 && !end) wait_units(rk);
+          rk.step(1);
+        }
+      };
+      // O += P V of the next tile of V
+      auto make_o = [&](int buf, bool use, bool fresh, bool looked) {
 #pragma unroll
-          for (int st = 0; st < NQ; ++st) {
-            if (i < y.nt[st]) {
-              const int buf = NQ == 2 ? st : ct[st] & 1;
-              wait(&b_p[buf], (NQ == 2 ? ct[st] : ct[st] >> 1) & 1);
-              umma::fence_after_sync();
-              if (elect_one()) issue_o(st, buf, add);
-              __syncwarp();
-              ++ct[st];
-            }
-            if (NQ == 2 && !end && i + 1 < y.nt[st]) {
-              if (elect_one()) issue_s(st, st, i + 2 == y.nt[st]);
-              __syncwarp();
-            }
+        for (int j = 0; j < VU; ++j) {
+          wait(&b_vfull[rv.slot], rv.phase);
+          if (j == 0 && looked) {  // (its values are full once they are looked over)
+            const uint4 wv = s_wild[chk++ & (kCheckRing - 1)];
+            if (wv.x | wv.y | wv.z | wv.w) fresh = false;
           }
-          if (elect_one()) {
-            free_units(rv);
-            if (NQ == 2 && !end) free_units(rk);
+          if (!TMA) umma::fence_smem_to_async();
+          if (use) {
+            if (j == 0) wait(&b_p[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+            umma::fence_after_sync();
+            if (elect_one()) {
+              const uint64_t vd = v_desc + rv.slot * (C::VB >> 4);
+#pragma unroll
+              for (int k = 0; k < TK; k += 16)
+                mma_ts(t_o + st * D + j * DV, tmem + buf * TK + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || !fresh);
+              if (j == VU - 1) umma::mma_commit(&b_o[buf]);
+              umma::mma_commit(&b_vempty[rv.slot]);
+            }
+            __syncwarp();
+          } else if (lane == 0) {
+            mbar_arrive(&b_vempty[rv.slot]);
           }
-          __syncwarp();
-          rv.step(2 * KU);
-          if (NQ == 2 && !end) rk.step(2 * KU);
-          if (end) {
-            more = next_piece(after);
-            if (more) begin(after);
+          rv.step(1);
+        }
+      };
+      auto wait_q = [&]() {
+        wait(&b_qfull[st], qn++ & 1);
+        umma::fence_smem_to_async();
+      };
+      while (const UPiece* piece = take()) {
+        const int n = piece->n, nt = st == 0 ? piece->nt[0] : piece->nt[1], look0 = piece->check0 - piece->x.t0;
+        give_back();
+        if (nt > 0 && (NQ == 2 || me == 0)) wait_q();
+        if constexpr (NQ == 2) {
+          if (n > 0) make_s(st, nt > 0, nt == 1);
+          for (int i = 0; i < n && !gone; ++i) {
+            make_o(st, i < nt, i % kRun == 0, i >= look0);
+            if (i < nt) ++ct;
+            if (i + 1 < n) make_s(st, i + 1 < nt, i + 2 == nt);
+          }
+        } else {
+          for (int i = 0; i < n && !gone; ++i) {
+            const int buf = ct & 1;
+            if (me == 0) {
+              wait(&b_o[buf], (ct >> 1 & 1) ^ 1);  // the weights that lie there have been used
+              make_s(buf, true, i + 1 == n);
+            } else {
+              make_o(buf, true, i % kRun == 0, i >= look0);
+            }
+            ++ct;
           }
         }
-        have = more;
-        y = after;
+        if (gone) break;
       }
       // products in flight end before tensor memory is given back
       if (elect_one()) umma::mma_commit(&b_drain);
       __syncwarp();
       for (uint32_t i = 0; i < kWaitTries && !umma::mbar_try_wait(&b_drain, 0); ++i) {
       }
-    } else if (warp == SOFT + 5) {
+    } else if (warp == SOFT + 4) {
       // ---- pieces -------------------------------------------------------------------------
       if (lane == 0) {
         UPiece y;
@@ -748,11 +774,11 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         } while (y.x.r >= 0);
       }
       __syncwarp();
-    } else {
+    } else if (warp < SOFT + 7) {
       // ---- queries, and a look at the values -------------------------------------------------
       constexpr int CPR = D / 8;
-      const int me = tid - (SOFT + 6) * 32;
-      At<U> rv{KU, 0};
+      const int me = tid - (SOFT + 5) * 32;
+      At<NV> rv{0, 0};
       uint32_t qn[2] = {0, 0}, chk = 0;
       while (const UPiece* piece = take()) {
         const int n = piece->n, look0 = piece->check0 - piece->x.t0, tokens = piece->x.tokens, heads = piece->x.heads;
@@ -783,13 +809,13 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             if (gone) break;
             bool wild[2] = {false, false};
 #pragma unroll
-            for (int j = 0; j < KU; ++j) {
-              const At<U> q = rv.plus(j);
+            for (int j = 0; j < VU; ++j) {
+              unsigned char* const unit = vbuf + rv.plus(j).slot * C::VB;
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll 4
-                for (int ch = 0; ch < DK / 8; ++ch) {
-                  uint4* at = reinterpret_cast<uint4*>(smem + q.slot * C::UNIT + umma::rp_offset(h * 64 + me, ch * 8, TK));
+                for (int ch = 0; ch < DV / 8; ++ch) {
+                  uint4* at = reinterpret_cast<uint4*>(unit + umma::rp_offset(h * 64 + me, ch * 8, TK));
                   const uint4 v = *at;
                   uint32_t e[4] = {v.x, v.y, v.z, v.w};
                   bool bad = false;
@@ -805,15 +831,15 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             __syncwarp();
             const uint32_t w0 = __ballot_sync(~0u, wild[0]), w1 = __ballot_sync(~0u, wild[1]);
             if (lane == 0) {
-              uint32_t* to = reinterpret_cast<uint32_t*>(&s_wild[chk & (kCheckRing - 1)]) + (warp - SOFT - 6);
+              uint32_t* to = reinterpret_cast<uint32_t*>(&s_wild[chk & (kCheckRing - 1)]) + (warp - SOFT - 5);
               to[0] = w0, to[2] = w1;
               mbar_arrive(&b_check[chk & (kCheckRing - 1)]);
 #pragma unroll
-              for (int j = 0; j < KU; ++j) mbar_arrive_many(&b_full[rv.plus(j).slot], FULL / 2);
+              for (int j = 0; j < VU; ++j) mbar_arrive_many(&b_vfull[rv.plus(j).slot], VFULL / 2);
             }
             ++chk;
           }
-          rv.step(2 * KU);
+          rv.step(VU);
         }
         if (gone) break;
       }
@@ -822,7 +848,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   }
   umma::fence_before_sync();
   __syncthreads();
-  if (warp == SOFT + 4) umma::tmem_dealloc(tmem, C::TMEM);
+  if (warp == SOFT + 2) umma::tmem_dealloc(tmem, C::TMEM);
   if (s_dead) {
     // a wait ran out: what this range leaves unwritten counts as left out
     for (int x = tid; x < 2 * p.rows; x += NT) p.part_ml[2 * int64_t(blockIdx.x) * p.rows + x] = make_float2(-INFINITY, attn::kLeftOut);
