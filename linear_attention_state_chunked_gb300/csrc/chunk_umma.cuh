@@ -84,6 +84,17 @@ struct UPiece {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(umma::smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void arrive_copies(uint64_t* bar) {  // when this thread's copies have landed
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(umma::smem_u32(bar)) : "memory");
 }
@@ -207,7 +218,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   constexpr bool TMA = C::TMA;
   constexpr int KFULL = TMA ? 1 : 32 + 1, VFULL = TMA ? 2 : 32 + 2;  // arrivals of a full unit
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ uint64_t b_kfull[NK], b_kempty[NK], b_vfull[NV], b_vempty[NV], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
+  __shared__ uint64_t b_kfull[NK], b_kempty[NK], b_vfull[NV], b_vempty[NV], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2][2], b_h[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
       b_pfull[kPieces], b_pempty[kPieces], b_drain;
   __shared__ UPiece s_piece[kPieces];
   __shared__ uint4 s_valid[kValidRing];  // live keys of a tile; a ring of tiles
@@ -224,7 +235,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     for (int i = 0; i < NK; ++i) umma::mbar_init(&b_kfull[i], KFULL), umma::mbar_init(&b_kempty[i], NQ);
     for (int i = 0; i < NV; ++i) umma::mbar_init(&b_vfull[i], VFULL), umma::mbar_init(&b_vempty[i], NQ);
     for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
-    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i][0], 4), umma::mbar_init(&b_p[i][1], 4), umma::mbar_init(&b_h[i], 1), umma::mbar_init(&b_o[i], 1);
     for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 1 : 32) * VU), umma::mbar_init(&b_check[i], 2);
     for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 2 + 2 + 2);
     umma::mbar_init(&b_drain, 2);
@@ -242,21 +253,18 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   unsigned char* const qbuf = smem + C::RING;
   unsigned char* const stage = qbuf + NQ * C::QT;
 
-  // A warp whose wait runs out waits for nothing more; the others learn of it where
-  // they wait, and all go to the end. Called by whole warps, and the same for all lanes.
+  // A warp whose wait runs out waits for nothing more and goes to the end, and so do the
+  // others in their turn. Called by whole warps, and the same for all lanes. (A look at a
+  // barrier takes 70 cycles, a wait that may sleep 200 even where the phase is over.)
   bool gone = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (gone) return;
-    for (uint32_t i = 0; i < kWaitTries; ++i) {
-      if (__all_sync(~0u, umma::mbar_try_wait(bar, parity))) return;
-      if ((i & 63) == 63 && __any_sync(~0u, *static_cast<volatile int*>(&s_dead))) {
+    if (gone || __all_sync(~0u, mbar_test(bar, parity))) return;
+    uint32_t left = kWaitTries;
+    while (!__all_sync(~0u, umma::mbar_try_wait(bar, parity)))
+      if (--left == 0) {
         gone = true;
-        return;
+        break;
       }
-    }
-    gone = true;
-    s_dead = 1;
-    report(a.status, LIN_ST_TIMEOUT);
   };
   int at_piece = 0;
   uint32_t piece_phase = 0;
@@ -327,128 +335,131 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           }
           z_acc = z, has_acc = cut != -INFINITY;
         }
-        float s[128];
-        const bool masked = key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u;
-        // the scores as the softmax takes them
-        auto see = [&]() {
-          if (p.negate) {
-#pragma unroll
-            for (int k = 0; k < 128; ++k) s[k] = -s[k];
-          }
-          if (masked) {
-            const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-              const int n = sees - key0 - 32 * h;
-              const uint32_t vis = n <= 0 ? 0u : n >= 32 ? live[h] : live[h] & ((1u << n) - 1u);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((vis >> k) & 1u)) s[32 * h + k] = -INFINITY;
-            }
-          }
-        };
-        // the reference, and what follows from its move
-        auto refer = [&]() {
-          float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int k = 4; k < 124; k += 8)
-#pragma unroll
-            for (int h = 0; h < 4; ++h) top[h] = max3(top[h], s[k + h], s[k + 4 + h]);
-#pragma unroll
-          for (int h = 0; h < 4; ++h) top[h] = fmaxf(top[h], s[124 + h]);
-          const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-          float f = 1.0f;
-          if (mx > cut) {
-            const float y0 = -mx * p.scale_log2;
-            f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
-            z = y0, cut = mx, l *= f;
-          }
-          if (!first && __any_sync(~0u, f != 1.0f)) {
-            wait_o(ct - 1);  // the last product has ended
-            umma::fence_after_sync();
+        const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
+        const bool masked = key0 + TK > all_see || (live[0] & live[1] & live[2] & live[3]) != ~0u;
+        // Half a tile at a time: P V of the first half is under way while the second one's
+        // weights are made.
 #pragma unroll 1
-            for (int d = 0; d < D; d += 8) {
-              float o[8];
-              tmem_get8(to + d, o);
+        for (int h = 0; h < 2; ++h) {
+          float s[64], sum = 0.0f;
+          // the reference, and what follows from its move
+          auto refer = [&]() {
+            float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[k] *= f;
-              tmem_set8(to + d, o);
+            for (int k = 4; k < 60; k += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[k + x], s[k + 4 + x]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[60 + x]);
+            const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
+            float f = 1.0f;
+            // (a row goes by its own scores alone, whatever made its warp look)
+            if (mx > cut && (cut == -INFINITY || !(sum <= kMostSum))) {
+              const float y0 = -mx * p.scale_log2;
+              f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
+              z = y0, cut = mx, l *= f;
             }
-          }
-          // a row that has seen nothing yet, and will see something
-          unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + TK);
-        };
-        uint32_t pk[64];
-        float tile_sum;
-        auto weigh = [&]() {
-          const uint64_t z2 = f2pack(z, z);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 64; ++k) {
-            float e0, e1;
-            f2unpack(ffma2(f2pack(s[2 * k], s[2 * k + 1]), scale2, z2), e0, e1);
-            e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
-            sum[k & 1] = fadd2(sum[k & 1], f2pack(e0, e1));
-            pk[k] = pack_bf16(e0, e1);
-          }
-          tile_sum = f2sum(fadd2(sum[0], sum[1]));
-        };
-        for (bool look_up = unset;; look_up = true) {
-#pragma unroll
-          for (int k = 0; k < 128; k += 32) tmem_issue32(ts + k, s + k);
-          tmem_loaded();
-#pragma unroll
-          for (int k = 0; k < 128; k += 32) landed32(s + k);
-          see();
-          if (look_up) refer();
-          weigh();
-          if (look_up || !__any_sync(~0u, !(tile_sum <= kMostSum))) break;
-        }
-        l += tile_sum;
-        if (tile >= y.check0) {
-          wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
-          const uint4 wv = s_wild[chk & (kCheckRing - 1)];
-          ++chk;
-          if (wv.x | wv.y | wv.z | wv.w) {
-            if (!first) wait_o(ct - 1);
-            umma::fence_after_sync();
-            const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
-            const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
+            if ((h == 1 || !first) && __any_sync(~0u, f != 1.0f)) {
+              // the last product has ended
+              if (h == 0)
+                wait_o(ct - 1);
+              else
+                wait(&b_h[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+              umma::fence_after_sync();
 #pragma unroll 1
-            for (int d = 0; d < D; d += 8) {
-              float o[8];
-              tmem_get8(to + d, o);
-              if (first) {  // the product adds to these, as it does not start from 0
+              for (int d = 0; d < D; d += 8) {
+                float o[8];
+                tmem_get8(to + d, o);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+                for (int k = 0; k < 8; ++k) o[k] *= f;
+                tmem_set8(to + d, o);
               }
-#pragma unroll 1
-              for (int h = 0; h < 4; ++h) {
-                uint32_t left = h == 0 ? wild[0] : h == 1 ? wild[1] : h == 2 ? wild[2] : wild[3];
-                for (; left; left &= left - 1) {
-                  const int t = key0 + 32 * h + __ffs(left) - 1;
-                  if (t >= sees) break;
-                  const int pg = page_of(p, t);
-                  const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
-                                  (t - pg * c.page_size) * c.token_stride + d * 2;
+            }
+            // a row that has seen nothing yet, and will see something
+            unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + 64 * (h + 1));
+          };
+          uint32_t pk[32];
+          for (bool look_up = unset;; look_up = true) {
+            tmem_issue32(ts + 64 * h, s);
+            tmem_issue32(ts + 64 * h + 32, s + 32);
+            tmem_loaded();
+            landed32(s);
+            landed32(s + 32);
+            if (p.negate) {
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);
-                    if (!isfinite(e)) o[k] += e;
+              for (int k = 0; k < 64; ++k) s[k] = -s[k];
+            }
+            if (masked) {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const int n = sees - key0 - 64 * h - 32 * x;
+                const uint32_t w = h == 0 ? live[x] : live[2 + x];
+                const uint32_t vis = n <= 0 ? 0u : n >= 32 ? w : w & ((1u << n) - 1u);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!((vis >> k) & 1u)) s[32 * x + k] = -INFINITY;
+              }
+            }
+            if (look_up) refer();
+            const uint64_t z2 = f2pack(z, z);
+            uint64_t add[2] = {0, 0};
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              float e0, e1;
+              f2unpack(ffma2(f2pack(s[2 * k], s[2 * k + 1]), scale2, z2), e0, e1);
+              e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
+              add[k & 1] = fadd2(add[k & 1], f2pack(e0, e1));
+              pk[k] = pack_bf16(e0, e1);
+            }
+            sum = f2sum(fadd2(add[0], add[1]));
+            if (look_up || !__any_sync(~0u, !(sum <= kMostSum))) break;
+          }
+          l += sum;
+          if (h == 0 && tile >= y.check0) {
+            wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+            const uint4 wv = s_wild[chk & (kCheckRing - 1)];
+            ++chk;
+            if (wv.x | wv.y | wv.z | wv.w) {
+              if (!first) wait_o(ct - 1);
+              umma::fence_after_sync();
+              const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
+              const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
+#pragma unroll 1
+              for (int d = 0; d < D; d += 8) {
+                float o[8];
+                tmem_get8(to + d, o);
+                if (first) {  // the product adds to these, as it does not start from 0
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+                }
+#pragma unroll 1
+                for (int g = 0; g < 4; ++g) {
+                  uint32_t left = g == 0 ? wild[0] : g == 1 ? wild[1] : g == 2 ? wild[2] : wild[3];
+                  for (; left; left &= left - 1) {
+                    const int t = key0 + 32 * g + __ffs(left) - 1;
+                    if (t >= sees) break;
+                    const int pg = page_of(p, t);
+                    const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
+                                    (t - pg * c.page_size) * c.token_stride + d * 2;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                      const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);
+                      if (!isfinite(e)) o[k] += e;
+                    }
                   }
                 }
+                __syncwarp();
+                tmem_set8(to + d, o);
               }
-              __syncwarp();
-              tmem_set8(to + d, o);
             }
           }
+          // (both halves' weights lie where the first half's scores were)
+          tmem_put32(ts + 32 * h, pk);
+          tmem_stored();
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_p[buf][h]);
         }
-        tmem_put32(ts, pk);
-        tmem_put32(ts + 32, pk + 32);
-        tmem_stored();
-        umma::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b_p[buf]);
         ++ct;
       }
       if (gone) break;
@@ -648,18 +659,26 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       At<NV> rv{0, 0};
       uint32_t ct = 0, qn = 0, chk = 0;
       // (whole warps wait, and one lane issues)
+      // all of a tile's K is there
+      auto wait_k = [&]() {
+#pragma unroll
+        for (int j = 0; j < KU; ++j) wait(&b_kfull[rk.plus(j).slot], rk.plus(j).phase);
+        if (!TMA) umma::fence_smem_to_async();
+      };
       // S of the next tile of K into buffer buf; left out: the tile is passed by
       auto make_s = [&](int buf, bool use, bool last) {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < KU; ++j) {
-          wait(&b_kfull[rk.slot], rk.phase);
-          if (!TMA) umma::fence_smem_to_async();
+          if (NQ == 1) {  // a unit at a time; else wait_k() has waited
+            wait(&b_kfull[rk.slot], rk.phase);
+            if (!TMA) umma::fence_smem_to_async();
+          }
           if (use) {
             umma::fence_after_sync();
             if (elect_one()) {
               const uint64_t kd = k_desc + rk.slot * (C::KB >> 4), qd = q_desc + ((st * C::QT + j * (128 * 128)) >> 4);
 #pragma unroll
-              for (int k = 0; k < 64; k += 16) umma::mma_f16(tmem + buf * TK, qd + (k * 2 >> 4), kd + (k * 2 >> 4), id_s, j + k > 0);
+              for (int k = 0; k < 64; k += 16) umma::mma_f16(tmem + buf * TK, qd + (k * 2 >> 4), kd + (k * 2 >> 4), id_s, j > 0 || k > 0);
               if (j == KU - 1) {
                 umma::mma_commit(&b_s[buf]);
                 if (last) umma::mma_commit(&b_qfree[st]);
@@ -674,27 +693,37 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           rk.step(1);
         }
       };
-      // O += P V of the next tile of V
+      // O += P V of the next tile of V, by halves of its keys
       auto make_o = [&](int buf, bool use, bool fresh, bool looked) {
 #pragma unroll
-        for (int j = 0; j < VU; ++j) {
-          wait(&b_vfull[rv.slot], rv.phase);
-          if (j == 0 && looked) {  // (its values are full once they are looked over)
-            const uint4 wv = s_wild[chk++ & (kCheckRing - 1)];
-            if (wv.x | wv.y | wv.z | wv.w) fresh = false;
-          }
-          if (!TMA) umma::fence_smem_to_async();
-          if (use) {
-            if (j == 0) wait(&b_p[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+        for (int j = 0; j < VU; ++j) wait(&b_vfull[rv.plus(j).slot], rv.plus(j).phase);
+        if (looked) {  // (its values are full once they are looked over)
+          const uint4 wv = s_wild[chk++ & (kCheckRing - 1)];
+          if (wv.x | wv.y | wv.z | wv.w) fresh = false;
+        }
+        if (!TMA) umma::fence_smem_to_async();
+        if (use) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            wait(&b_p[buf][h], (NQ == 2 ? ct : ct >> 1) & 1);
             umma::fence_after_sync();
             if (elect_one()) {
-              const uint64_t vd = v_desc + rv.slot * (C::VB >> 4);
 #pragma unroll
-              for (int k = 0; k < TK; k += 16)
-                mma_ts(t_o + st * D + j * DV, tmem + buf * TK + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || !fresh);
-              if (j == VU - 1) umma::mma_commit(&b_o[buf]);
-              umma::mma_commit(&b_vempty[rv.slot]);
+              for (int j = 0; j < VU; ++j) {
+                const uint64_t vd = v_desc + ((rv.plus(j).slot * C::VB + h * (64 * 128)) >> 4);
+#pragma unroll
+                for (int k = 0; k < 64; k += 16)
+                  mma_ts(t_o + st * D + j * DV, tmem + buf * TK + 32 * h + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || h > 0 || !fresh);
+              }
+              umma::mma_commit(h == 0 ? &b_h[buf] : &b_o[buf]);
             }
+            __syncwarp();
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < VU; ++j) {
+          if (use) {
+            if (elect_one()) umma::mma_commit(&b_vempty[rv.slot]);
             __syncwarp();
           } else if (lane == 0) {
             mbar_arrive(&b_vempty[rv.slot]);
@@ -711,8 +740,9 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         give_back();
         if (nt > 0 && (NQ == 2 || me == 0)) wait_q();
         if constexpr (NQ == 2) {
-          if (n > 0) make_s(st, nt > 0, nt == 1);
+          if (n > 0) wait_k(), make_s(st, nt > 0, nt == 1);
           for (int i = 0; i < n && !gone; ++i) {
+            if (i + 1 < n) wait_k();
             make_o(st, i < nt, i % kRun == 0, i >= look0);
             if (i < nt) ++ct;
             if (i + 1 < n) make_s(st, i + 1 < nt, i + 2 == nt);
@@ -760,12 +790,10 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             if (TMA && x.keys % p.box) y.check0 = min(y.check0, x.keys / TK);
             g += y.n;
           }
-          bool free = false;
-          for (uint32_t i = 0; i < kWaitTries && !free && !*static_cast<volatile int*>(&s_dead); ++i)
-            free = umma::mbar_try_wait(&b_pempty[at_piece], piece_phase ^ 1);
-          if (!free) {  // this range's pieces are lost either way
-            s_dead = 1;
-            report(a.status, LIN_ST_TIMEOUT);
+          uint32_t left = kWaitTries;
+          while (left > 0 && !umma::mbar_try_wait(&b_pempty[at_piece], piece_phase ^ 1)) --left;
+          if (left == 0) {
+            gone = true;
             break;
           }
           s_piece[at_piece] = y;
@@ -846,13 +874,17 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       attn::cp_wait_all();
     }
   }
+  if (gone) s_dead = 1;
   umma::fence_before_sync();
   __syncthreads();
   if (warp == SOFT + 2) umma::tmem_dealloc(tmem, C::TMEM);
   if (s_dead) {
     // a wait ran out: what this range leaves unwritten counts as left out
     for (int x = tid; x < 2 * p.rows; x += NT) p.part_ml[2 * int64_t(blockIdx.x) * p.rows + x] = make_float2(-INFINITY, attn::kLeftOut);
-    if (tid == 0) p.split[blockIdx.x].parts = 0;
+    if (tid == 0) {
+      p.split[blockIdx.x].parts = 0;
+      report(a.status, LIN_ST_TIMEOUT);
+    }
   }
 }
 
