@@ -134,6 +134,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, WalkShared& s
   const int batch = p.a.batch, span = (batch + NT - 1) / NT;
   const int r0 = min(batch, tid * span), r1 = min(batch, r0 + span);
   int64_t mine = 0;
+#pragma unroll 1
   for (int r = r0; r < r1; ++r) {
     const Req q = request(p, r, blockIdx.x == 0);
     if (q.items) mine += units_before(p, q, q.items) * p.heads;
@@ -164,6 +165,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, WalkShared& s
   w.end = w.total * (blockIdx.x + 1) / w.ranges;
   if (cur >= upto - mine && cur < upto) {
     int64_t at = upto - mine;
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       const Req q = request(p, r, false);
       const int64_t n = q.items ? units_before(p, q, q.items) * p.heads : 0;
@@ -182,6 +184,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, WalkShared& s
   w.h = static_cast<int>(off / per_head);
   off -= w.h * per_head;
   int lo = 0, hi = w.q.items - 1;  // the last item that begins at or before the border
+#pragma unroll 1
   while (lo < hi) {
     const int mid = lo + (hi - lo + 1) / 2;
     if (units_before(p, w.q, mid) <= off)
@@ -200,6 +203,7 @@ __device__ __forceinline__ bool walk_begin(const Plan& p, Walk& w, WalkShared& s
 // The next piece, r = -1 at the range's end. Leaves the range's split there.
 __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
   Piece x;
+#pragma unroll 1
   while (w.pos < w.end) {
     const int64_t keys = keys_of(p, w.q, w.j);
     const int tiles = static_cast<int>((keys + p.tk - 1) / p.tk);
@@ -236,6 +240,7 @@ __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
         w.j = 0;
         if (++w.h == p.heads) {
           w.h = 0;
+#pragma unroll 1
           do {
             w.q = request(p, ++w.r, false);
           } while (w.q.items == 0);

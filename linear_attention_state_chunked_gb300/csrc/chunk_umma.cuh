@@ -260,6 +260,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (gone || __all_sync(~0u, mbar_test(bar, parity))) return;
     uint32_t left = kWaitTries;
+#pragma unroll 1
     while (!__all_sync(~0u, umma::mbar_try_wait(bar, parity)))
       if (--left == 0) {
         gone = true;
@@ -296,6 +297,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     // The product of tile t has ended. (A barrier for each buffer: when S of tile t is
     // there, the product of t - 2 has ended, and that of t - 1 need not have.)
     auto wait_o = [&](uint32_t t) { wait(&b_o[NQ == 2 ? st : t & 1], (NQ == 2 ? t : t >> 1) & 1); };
+#pragma unroll 1
     while (const UPiece* piece = take()) {
       const UPiece y = *piece;
       give_back();
@@ -310,6 +312,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       bool has_acc = false, unset = true;
       // looked-over tiles that are not this row tile's
       const int first_chk = max(x.t0, y.check0), chk_before = chk;
+#pragma unroll 1
       for (int i = 0; i < nt && !gone; ++i) {
         const int tile = x.t0 + i, key0 = tile * TK;
         const int buf = NQ == 2 ? st : ct & 1;
@@ -531,6 +534,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       At<NK> rk{0, 0};
       At<NV> rv{0, 0};
       uint32_t chk = 0;
+#pragma unroll 1
       while (const UPiece* piece = take()) {
         const int n = piece->n, g0 = piece->g0, keys = piece->x.keys, hk = piece->x.hk, look0 = piece->check0 - piece->x.t0;
         const int32_t* table = a.page_table + piece->x.r * a.page_table_stride;
@@ -540,6 +544,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         int key = key0 + lane * p.box, id = -1;
         auto look = [&](int k) { return lane * p.box < TK && k < keys ? table[page_of(p, k)] : -1; };
         if (TMA && n > 0) id = look(key);
+#pragma unroll 1
         for (int i = 0; i < n && !gone; ++i) {
           uint32_t valid = 0;  // of keys 32 lane and on, in lanes 0 to 3
           bool live = false;
@@ -551,6 +556,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             in_page = key - page_of(p, key) * c.page_size;
             const uint32_t some = __ballot_sync(~0u, live);
             const uint32_t whole = p.box == 32 ? ~0u : (1u << p.box) - 1u;
+#pragma unroll 1
             for (int b = 0; b < 32; b += p.box)
               if ((some >> ((32 * lane + b) / p.box & 31)) & 1u) valid |= whole << b;
             const int left = keys - key0 - 32 * lane;
@@ -735,19 +741,21 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         wait(&b_qfull[st], qn++ & 1);
         umma::fence_smem_to_async();
       };
+#pragma unroll 1
       while (const UPiece* piece = take()) {
         const int n = piece->n, nt = st == 0 ? piece->nt[0] : piece->nt[1], look0 = piece->check0 - piece->x.t0;
         give_back();
         if (nt > 0 && (NQ == 2 || me == 0)) wait_q();
         if constexpr (NQ == 2) {
-          if (n > 0) wait_k(), make_s(st, nt > 0, nt == 1);
-          for (int i = 0; i < n && !gone; ++i) {
+#pragma unroll 1
+          for (int i = -1; i < n && !gone; ++i) {  // P V of tile i, S of tile i + 1
             if (i + 1 < n) wait_k();
-            make_o(st, i < nt, i % kRun == 0, i >= look0);
-            if (i < nt) ++ct;
+            if (i >= 0) make_o(st, i < nt, i % kRun == 0, i >= look0);
+            if (i >= 0 && i < nt) ++ct;
             if (i + 1 < n) make_s(st, i + 1 < nt, i + 2 == nt);
           }
         } else {
+#pragma unroll 1
           for (int i = 0; i < n && !gone; ++i) {
             const int buf = ct & 1;
             if (me == 0) {
@@ -771,6 +779,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       if (lane == 0) {
         UPiece y;
         int g = 0;
+#pragma unroll 1
         do {
           y.x = walk_next(p, w);
           const Piece& x = y.x;
@@ -791,6 +800,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             g += y.n;
           }
           uint32_t left = kWaitTries;
+#pragma unroll 1
           while (left > 0 && !umma::mbar_try_wait(&b_pempty[at_piece], piece_phase ^ 1)) --left;
           if (left == 0) {
             gone = true;
@@ -808,6 +818,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       const int me = tid - (SOFT + 5) * 32;
       At<NV> rv{0, 0};
       uint32_t qn[2] = {0, 0}, chk = 0;
+#pragma unroll 1
       while (const UPiece* piece = take()) {
         const int n = piece->n, look0 = piece->check0 - piece->x.t0, tokens = piece->x.tokens, heads = piece->x.heads;
         const int nt[2] = {piece->nt[0], piece->nt[1]};
@@ -820,7 +831,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           if (gone) break;
           ++qn[st];
           const uint32_t dst = umma::smem_u32(qbuf) + st * C::QT;
-#pragma unroll 4
+#pragma unroll 2
           for (int k = me; k < 128 * CPR; k += 64) {
             const int row = k / CPR, ch = k % CPR;
             const int t = token_of(p, st * 128 + row), h = st * 128 + row - t * p.bheads;
@@ -830,6 +841,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           }
           arrive_copies(&b_qfull[st]);
         }
+#pragma unroll 1
         for (int i = 0; i < n && !gone; ++i) {
           if (i >= look0) {
             // (a barrier of these tiles alone: the ring's may be many phases behind)
@@ -841,7 +853,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               unsigned char* const unit = vbuf + rv.plus(j).slot * C::VB;
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-#pragma unroll 4
+#pragma unroll 2
                 for (int ch = 0; ch < DV / 8; ++ch) {
                   uint4* at = reinterpret_cast<uint4*>(unit + umma::rp_offset(h * 64 + me, ch * 8, TK));
                   const uint4 v = *at;
