@@ -475,20 +475,31 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       const float fa = has_acc ? attn::exp2_fast(z - z_acc) : 0.0f;
       const float fo = !x.whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
       unsigned char* const rows = stage + warp * 4096;  // 32 rows of 64 outputs, swizzled
+      // the rows that this lane writes 16 bytes of: 4 at a time, 128 bytes of each
+      uint16_t* to_row[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = st * 128 + (warp & 3) * 32 + k * 4 + lane / 8, t = token_of(p, r), h = r - t * p.bheads;
+        to_row[k] = x.whole && t < x.tokens && h < x.heads
+                        ? static_cast<uint16_t*>(a.out) + (int64_t(x.row0 + t) * a.num_q_heads + x.head0 + h) * D + (lane & 7) * 8
+                        : nullptr;
+      }
 #pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        float o[32];
+      for (int d = 0; d < D; d += 64) {
+        float o[64];
         if (nt > 0) {
           tmem_issue32(to + d, o);
+          tmem_issue32(to + d + 32, o + 32);
           tmem_loaded();
           landed32(o);
+          landed32(o + 32);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+          for (int k = 0; k < 64; ++k) o[k] = 0.0f;
         }
         if (has_acc) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
+          for (int k = 0; k < 64; k += 4) {
             const float4 was = acc[int64_t((d + k) / 4) * p.rows];
             o[k] = fmaf(was.x, fa, o[k]), o[k + 1] = fmaf(was.y, fa, o[k + 1]);
             o[k + 2] = fmaf(was.z, fa, o[k + 2]), o[k + 3] = fmaf(was.w, fa, o[k + 3]);
@@ -496,27 +507,25 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         }
         if (!x.whole) {  // rows of all lanes side by side
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
+          for (int k = 0; k < 64; k += 4)
             acc[int64_t((d + k) / 4) * p.rows] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4*>(rows + lane * 128 + ((((d & 32) + k) / 8 ^ (lane & 7)) << 4)) =
+          for (int k = 0; k < 64; k += 8)
+            *reinterpret_cast<uint4*>(rows + lane * 128 + ((k / 8 ^ (lane & 7)) << 4)) =
                 make_uint4(pack_bf16(o[k] * fo, o[k + 1] * fo), pack_bf16(o[k + 2] * fo, o[k + 3] * fo),
                            pack_bf16(o[k + 4] * fo, o[k + 5] * fo), pack_bf16(o[k + 6] * fo, o[k + 7] * fo));
-          if (d & 32) {
-            __syncwarp();
+          __syncwarp();
+          uint4 v[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {  // 4 rows at a time, 128 bytes of each
-              const int q = k * 4 + lane / 8, ch = lane & 7;
-              const int r = st * 128 + (warp & 3) * 32 + q, t = token_of(p, r), h = r - t * p.bheads;
-              const uint4 v = *reinterpret_cast<const uint4*>(rows + q * 128 + ((ch ^ (q & 7)) << 4));
-              if (t < x.tokens && h < x.heads)
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) +
-                                          (int64_t(x.row0 + t) * a.num_q_heads + x.head0 + h) * D + d - 32 + ch * 8) = v;
-            }
-            __syncwarp();
+          for (int k = 0; k < 8; ++k) {
+            const int q = k * 4 + lane / 8;
+            v[k] = *reinterpret_cast<const uint4*>(rows + q * 128 + (((lane & 7) ^ (q & 7)) << 4));
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (to_row[k]) *reinterpret_cast<uint4*>(to_row[k] + d) = v[k];
+          __syncwarp();
         }
       }
       if (mine && !x.whole)
