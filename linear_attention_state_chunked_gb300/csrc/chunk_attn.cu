@@ -135,7 +135,7 @@ Shape shape_of(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int out_
   if (c.dtype == LIN_BF16 && out_dtype == LIN_BF16) {
     const int64_t rows = int64_t(a.tokens) * (a.num_q_heads / c.num_kv_heads);  // of a kv head
     const bool two = c.head_dim <= 128 && rows > 128 * int64_t(a.batch);
-    return {true, two ? 256 : 128, 128, 1, 192};
+    return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 192};
   }
   const int row_bytes = c.head_dim * dtype_size(c.dtype);
   return {false, 64, row_bytes >= 512 ? 16 : 32, row_bytes <= 256 ? 3 : row_bytes == 512 ? 2 : 1, 64};
@@ -252,7 +252,9 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   cudaError_t e;
   if (f.umma) {
     CUtensorMap k = {}, v = {};
-    const int box = c.page_size % 32 == 0 ? 32 : c.page_size % 16 == 0 ? 16 : c.page_size % 8 == 0 ? 8 : 0;
+    int box = 32;  // of whole pages and tiles
+    while (box >= 8 && (c.page_size % box || p.tk % box)) box /= 2;
+    if (box < 8) box = 0;
     if (box && chunk::encode(&k, c, c.k, a.layer, box) && chunk::encode(&v, c, c.v, a.layer, box)) p.box = box;
     e = c.head_dim == 64    ? chunk::launch_umma_d64(p, k, v, s)
         : c.head_dim == 128 ? chunk::launch_umma_d128(p, k, v, s)

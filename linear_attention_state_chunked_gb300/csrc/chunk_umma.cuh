@@ -2,15 +2,21 @@
 //
 //   S = Q K^T,  P = 2^(S scale log2(e) - m),  O = sum over tiles of P V,  out = O / sum P
 //
-// in tiles of 128 rows (new tokens x query heads of one kv head) and TK = 128 keys, with
-// a running maximum and sum per row. Bound by the tensor unit for prompts: 4 head_dim
+// in tiles of 128 rows (new tokens x query heads of one kv head) and TK keys, with a
+// running maximum and sum per row. Bound by the tensor unit for prompts: 4 head_dim
 // flops per visible (row, key); by HBM for a few rows over a long cache.
 //
-// An item has NQ row tiles. Two (heads of 64 and 128): the unit makes O += P V and the
-// next S of one while the softmax warps of the other work; a warp each issues them, as an
-// issue waits until the unit is near it. One (heads of 256, whose O alone takes half of
-// tensor memory, and few rows): S has two buffers, and the unit makes the next S while the
-// softmax works on the last; a warp issues S, another P V.
+// An item has NQ row tiles. What counts is that the unit always has a product to make: a
+// tile's chain (S, its way to the registers, the weights, their way back, P V) is some
+// 4,000 cycles long for 128 keys of heads of 128, of which the unit works 1,100. So the
+// next S is made while the softmax works on the last, which takes room in tensor memory
+// for a second S or for P beside S.
+//   NQ = 1 (heads of 256, whose O alone takes half of tensor memory, and few rows): two
+//   buffers of S with TK = 128, P in its S's place. A warp issues S, another P V.
+//   NQ = 2 (heads of 64 and 128): one S each, which is free once it is in registers, and P
+//   beside it: TK = 96 and 80, as S, P and O of both fit. (With TK = 128 and P in S's
+//   place, 653 us for 8 prompts of 4,096 tokens, 16 heads of 128.) A warp for each row
+//   tile issues its products, as an issue waits until the unit is near it.
 //
 // Roles: 4 NQ softmax warps (thread = row = tensor-memory lane, so no exchange between
 // threads), a warp that loads K and one that loads V, each into a ring of its own, two that
@@ -49,7 +55,7 @@ template <int D_, int NQ_, bool TMA_>
 struct UCfg {
   static constexpr int D = D_, NQ = NQ_;
   static constexpr bool TMA = TMA_;
-  static constexpr int TK = 128;
+  static constexpr int TK = NQ == 1 ? 128 : D == 64 ? 96 : 80;
   // a ring unit: 64 channels of a tile's K, up to 128 of its V
   static constexpr int KU = D / 64, KB = TK * 64 * 2;
   static constexpr int DV = D < 128 ? D : 128, VU = D / DV, VB = TK * DV * 2;
@@ -57,15 +63,17 @@ struct UCfg {
   static constexpr int SOFT = 4 * NQ;           // softmax warps
   static constexpr int STAGE = SOFT * 4096;     // where outputs are turned into rows
   // units of the rings: at least a tile of each
-  static constexpr int NK = D == 64 ? (NQ == 2 ? 5 : 6) : D == 256 ? 5 : NQ == 2 ? 4 : 6;
-  static constexpr int NV = D == 64 ? (NQ == 2 ? 5 : 6) : 2;
+  static constexpr int NK = D == 256 ? 5 : 6;
+  static constexpr int NV = D == 64 ? 6 : NQ == 2 ? 3 : 2;
   static constexpr int RING = NK * KB + NV * VB;
   static constexpr int SMEM = RING + NQ * QT + STAGE;
   static constexpr int THREADS = SOFT * 32 + 256;
-  // tensor memory columns: 2 of S (and P), NQ of O
-  static constexpr int T_O = 2 * TK;
+  // tensor memory columns: 2 of S, P in their places or beside, NQ of O
+  static constexpr bool APART = NQ == 2;
+  static constexpr int T_P = APART ? 2 * TK : 0, P_STEP = APART ? TK / 2 : TK;
+  static constexpr int T_O = 512 - NQ * D;
   static constexpr int TMEM = 512;
-  static_assert(T_O + NQ * D <= TMEM && NK >= KU && NV >= VU && SMEM <= 224 * 1024, "");
+  static_assert(2 * TK + (APART ? TK : 0) <= T_O && TK % 16 == 0 && NK >= KU && NV >= VU && SMEM <= 224 * 1024, "");
 };
 
 constexpr uint32_t kWaitTries = 1u << 24;
@@ -159,6 +167,24 @@ __device__ __forceinline__ void tmem_issue32(uint32_t at, float* v) {
         "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
       : "r"(at));
 }
+__device__ __forceinline__ void tmem_issue16(uint32_t at, float* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+        "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+      : "r"(at));
+}
+__device__ __forceinline__ void landed16(float* v) {
+  asm volatile(""
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]));
+}
+__device__ __forceinline__ void tmem_put8(uint32_t at, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 // The values are there from here on: no use of them moves above.
 __device__ __forceinline__ void landed32(float* v) {
@@ -167,17 +193,6 @@ __device__ __forceinline__ void landed32(float* v) {
                  "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
                  "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
                  "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
-}
-__device__ __forceinline__ void tmem_put32(uint32_t at, const uint32_t* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-      "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-      "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-      : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -218,7 +233,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   constexpr bool TMA = C::TMA;
   constexpr int KFULL = TMA ? 1 : 32 + 1, VFULL = TMA ? 2 : 32 + 2;  // arrivals of a full unit
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ uint64_t b_kfull[NK], b_kempty[NK], b_vfull[NV], b_vempty[NV], b_qfull[NQ], b_qfree[NQ], b_s[2], b_p[2][2], b_h[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
+  __shared__ uint64_t b_kfull[NK], b_kempty[NK], b_vfull[NV], b_vempty[NV], b_qfull[NQ], b_qfree[NQ], b_s[2], b_sfree[2], b_p[2], b_o[2], b_look[kCheckRing], b_check[kCheckRing],
       b_pfull[kPieces], b_pempty[kPieces], b_drain;
   __shared__ UPiece s_piece[kPieces];
   __shared__ uint4 s_valid[kValidRing];  // live keys of a tile; a ring of tiles
@@ -235,7 +250,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     for (int i = 0; i < NK; ++i) umma::mbar_init(&b_kfull[i], KFULL), umma::mbar_init(&b_kempty[i], NQ);
     for (int i = 0; i < NV; ++i) umma::mbar_init(&b_vfull[i], VFULL), umma::mbar_init(&b_vempty[i], NQ);
     for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
-    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_p[i][0], 4), umma::mbar_init(&b_p[i][1], 4), umma::mbar_init(&b_h[i], 1), umma::mbar_init(&b_o[i], 1);
+    for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_sfree[i], 4), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
     for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 1 : 32) * VU), umma::mbar_init(&b_check[i], 2);
     for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 2 + 2 + 2);
     umma::mbar_init(&b_drain, 2);
@@ -338,22 +353,47 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           }
           z_acc = z, has_acc = cut != -INFINITY;
         }
-        const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
-        const bool masked = key0 + TK > all_see || (live[0] & live[1] & live[2] & live[3]) != ~0u;
-        // Half a tile at a time: P V of the first half is under way while the second one's
-        // weights are made.
+        const bool masked = key0 + TK > all_see || (valid.x & valid.y & valid.z & valid.w) != ~0u;
+        float s[TK];
+#pragma unroll
+        for (int k = 0; k + 32 <= TK; k += 32) tmem_issue32(ts + k, s + k);
+        if (TK % 32) tmem_issue16(ts + TK / 32 * 32, s + TK / 32 * 32);
+        tmem_loaded();
+#pragma unroll
+        for (int k = 0; k + 32 <= TK; k += 32) landed32(s + k);
+        if (TK % 32) landed16(s + TK / 32 * 32);
+        if (C::APART) {  // the next scores may come
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b_sfree[st]);
+        }
+        if (p.negate) {
+#pragma unroll
+          for (int k = 0; k < TK; ++k) s[k] = -s[k];
+        }
+        if (masked) {
+          const uint32_t live[4] = {valid.x, valid.y, valid.z, valid.w};
+#pragma unroll
+          for (int x = 0; x < TK; x += 32) {
+            const int n = sees - key0 - x;
+            const uint32_t vis = n <= 0 ? 0u : n >= 32 ? live[x / 32] : live[x / 32] & ((1u << n) - 1u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (x + k < TK && !((vis >> k) & 1u)) s[x + k] = -INFINITY;
+          }
+        }
+        uint32_t pk[TK / 2];
+        float sum = 0.0f;
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          float s[64], sum = 0.0f;
-          // the reference, and what follows from its move
-          auto refer = [&]() {
+        for (bool look_up = unset;; look_up = true) {
+          if (look_up) {  // the reference, and what follows from its move
             float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int k = 4; k < 60; k += 8)
+            for (int k = 4; k + 8 <= TK; k += 8)
 #pragma unroll
               for (int x = 0; x < 4; ++x) top[x] = max3(top[x], s[k + x], s[k + 4 + x]);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[60 + x]);
+            for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], s[TK - 4 + x]);
             const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
             float f = 1.0f;
             // (a row goes by its own scores alone, whatever made its warp look)
@@ -362,12 +402,8 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
               z = y0, cut = mx, l *= f;
             }
-            if ((h == 1 || !first) && __any_sync(~0u, f != 1.0f)) {
-              // the last product has ended
-              if (h == 0)
-                wait_o(ct - 1);
-              else
-                wait(&b_h[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+            if (!first && __any_sync(~0u, f != 1.0f)) {
+              wait_o(ct - 1);  // the last product has ended
               umma::fence_after_sync();
 #pragma unroll 1
               for (int d = 0; d < D; d += 8) {
@@ -379,90 +415,68 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               }
             }
             // a row that has seen nothing yet, and will see something
-            unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + 64 * (h + 1));
-          };
-          uint32_t pk[32];
-          for (bool look_up = unset;; look_up = true) {
-            tmem_issue32(ts + 64 * h, s);
-            tmem_issue32(ts + 64 * h + 32, s + 32);
-            tmem_loaded();
-            landed32(s);
-            landed32(s + 32);
-            if (p.negate) {
-#pragma unroll
-              for (int k = 0; k < 64; ++k) s[k] = -s[k];
-            }
-            if (masked) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const int n = sees - key0 - 64 * h - 32 * x;
-                const uint32_t w = h == 0 ? live[x] : live[2 + x];
-                const uint32_t vis = n <= 0 ? 0u : n >= 32 ? w : w & ((1u << n) - 1u);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (!((vis >> k) & 1u)) s[32 * x + k] = -INFINITY;
-              }
-            }
-            if (look_up) refer();
-            const uint64_t z2 = f2pack(z, z);
-            uint64_t add[2] = {0, 0};
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              float e0, e1;
-              f2unpack(ffma2(f2pack(s[2 * k], s[2 * k + 1]), scale2, z2), e0, e1);
-              e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
-              add[k & 1] = fadd2(add[k & 1], f2pack(e0, e1));
-              pk[k] = pack_bf16(e0, e1);
-            }
-            sum = f2sum(fadd2(add[0], add[1]));
-            if (look_up || !__any_sync(~0u, !(sum <= kMostSum))) break;
+            unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + TK);
           }
-          l += sum;
-          if (h == 0 && tile >= y.check0) {
-            wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
-            const uint4 wv = s_wild[chk & (kCheckRing - 1)];
-            ++chk;
-            if (wv.x | wv.y | wv.z | wv.w) {
-              if (!first) wait_o(ct - 1);
-              umma::fence_after_sync();
-              const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
-              const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
-#pragma unroll 1
-              for (int d = 0; d < D; d += 8) {
-                float o[8];
-                tmem_get8(to + d, o);
-                if (first) {  // the product adds to these, as it does not start from 0
+          const uint64_t z2 = f2pack(z, z);
+          uint64_t add[2] = {0, 0};
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) o[k] = 0.0f;
-                }
+          for (int k = 0; k < TK / 2; ++k) {
+            float e0, e1;
+            f2unpack(ffma2(f2pack(s[2 * k], s[2 * k + 1]), scale2, z2), e0, e1);
+            e0 = attn::exp2_fast(e0), e1 = attn::exp2_fast(e1);
+            add[k & 1] = fadd2(add[k & 1], f2pack(e0, e1));
+            pk[k] = pack_bf16(e0, e1);
+          }
+          sum = f2sum(fadd2(add[0], add[1]));
+          if (look_up || !__any_sync(~0u, !(sum <= kMostSum))) break;
+        }
+        l += sum;
+        if (tile >= y.check0) {
+          wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+          const uint4 wv = s_wild[chk & (kCheckRing - 1)];
+          ++chk;
+          if (wv.x | wv.y | wv.z | wv.w) {
+            if (!first) wait_o(ct - 1);
+            umma::fence_after_sync();
+            const uint32_t wild[4] = {wv.x, wv.y, wv.z, wv.w};
+            const char* vb = static_cast<const char*>(c.v) + a.layer * c.layer_stride + x.hk * c.head_stride;
 #pragma unroll 1
-                for (int g = 0; g < 4; ++g) {
-                  uint32_t left = g == 0 ? wild[0] : g == 1 ? wild[1] : g == 2 ? wild[2] : wild[3];
-                  for (; left; left &= left - 1) {
-                    const int t = key0 + 32 * g + __ffs(left) - 1;
-                    if (t >= sees) break;
-                    const int pg = page_of(p, t);
-                    const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
-                                    (t - pg * c.page_size) * c.token_stride + d * 2;
+            for (int d = 0; d < D; d += 8) {
+              float o[8];
+              tmem_get8(to + d, o);
+              if (first) {  // the product adds to these, as it does not start from 0
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                      const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);
-                      if (!isfinite(e)) o[k] += e;
-                    }
+                for (int k = 0; k < 8; ++k) o[k] = 0.0f;
+              }
+#pragma unroll 1
+              for (int g = 0; g < 4; ++g) {
+                uint32_t left = g == 0 ? wild[0] : g == 1 ? wild[1] : g == 2 ? wild[2] : wild[3];
+                for (; left; left &= left - 1) {
+                  const int t = key0 + 32 * g + __ffs(left) - 1;
+                  if (t >= sees) break;
+                  const int pg = page_of(p, t);
+                  const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
+                                  (t - pg * c.page_size) * c.token_stride + d * 2;
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) {
+                    const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);
+                    if (!isfinite(e)) o[k] += e;
                   }
                 }
-                __syncwarp();
-                tmem_set8(to + d, o);
               }
+              __syncwarp();
+              tmem_set8(to + d, o);
             }
           }
-          // (both halves' weights lie where the first half's scores were)
-          tmem_put32(ts + 32 * h, pk);
-          tmem_stored();
-          umma::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b_p[buf][h]);
         }
+        if (C::APART && ct > 0) wait_o(ct - 1);  // the last weights have been used
+        umma::fence_after_sync();
+#pragma unroll
+        for (int k = 0; k < TK / 2; k += 8) tmem_put8(tmem + t_lane + C::T_P + buf * C::P_STEP + k, pk + k);
+        tmem_stored();
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b_p[buf]);
         ++ct;
       }
       if (gone) break;
@@ -555,7 +569,8 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         if (TMA && n > 0) id = look(key);
 #pragma unroll 1
         for (int i = 0; i < n && !gone; ++i) {
-          uint32_t valid = 0;  // of keys 32 lane and on, in lanes 0 to 3
+          uint32_t valid = 0;  // of keys 32 lane and on, in lanes 0 to 3; 1 past the tile
+          const uint32_t past = 32 * lane >= TK ? ~0u : 32 * lane + 32 > TK ? ~0u << (TK & 31) : 0u;
           bool live = false;
           int in_page = 0, page = 0;
           int64_t off[4];      // (no TMA) of keys lane, lane + 32, ...
@@ -570,6 +585,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               if ((some >> ((32 * lane + b) / p.box & 31)) & 1u) valid |= whole << b;
             const int left = keys - key0 - 32 * lane;
             if (left < 32) valid = left <= 0 ? 0u : valid & ((1u << left) - 1u);
+            valid |= past;
             page = live ? id : c.num_pages;  // (past the last: zeros)
             key += TK;
             id = look(key);
@@ -582,7 +598,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               if (!is_v && k < keys && !ok) report(a.status, LIN_ST_BAD_PAGE);
               off[h] = ok ? at * c.page_stride + (k - pg * c.page_size) * c.token_stride : 0;
               const uint32_t some = __ballot_sync(~0u, ok);
-              if (lane == h) valid = some;
+              if (lane == h) valid = some | past;
             }
           }
           key0 += TK;
@@ -594,7 +610,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             for (int h = 0; h < 4; ++h) {
               const uint32_t ok = __shfl_sync(~0u, valid, h);
 #pragma unroll 4
-              for (int x = 0; x < 32; x += step) {
+              for (int x = 0; x < 32 && 32 * h + x < TK; x += step) {
                 const int row = x + lane / chunks;
                 const int64_t o = __shfl_sync(~0u, off[h], row);
                 attn::cp16(dst + umma::rp_offset(32 * h + row, ch * 8, TK), src + o + ch * 16, (ok >> row) & 1u);
@@ -672,7 +688,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       const int st = NQ == 2 ? me : 0;
       At<NK> rk{0, 0};
       At<NV> rv{0, 0};
-      uint32_t ct = 0, qn = 0, chk = 0;
+      uint32_t ct = 0, cs = 0, qn = 0, chk = 0;
       // (whole warps wait, and one lane issues)
       // all of a tile's K is there
       auto wait_k = [&]() {
@@ -708,7 +724,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           rk.step(1);
         }
       };
-      // O += P V of the next tile of V, by halves of its keys
+      // O += P V of the next tile of V
       auto make_o = [&](int buf, bool use, bool fresh, bool looked) {
 #pragma unroll
         for (int j = 0; j < VU; ++j) wait(&b_vfull[rv.plus(j).slot], rv.plus(j).phase);
@@ -718,22 +734,19 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         }
         if (!TMA) umma::fence_smem_to_async();
         if (use) {
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            wait(&b_p[buf][h], (NQ == 2 ? ct : ct >> 1) & 1);
-            umma::fence_after_sync();
-            if (elect_one()) {
+          wait(&b_p[buf], (NQ == 2 ? ct : ct >> 1) & 1);
+          umma::fence_after_sync();
+          if (elect_one()) {
 #pragma unroll
-              for (int j = 0; j < VU; ++j) {
-                const uint64_t vd = v_desc + ((rv.plus(j).slot * C::VB + h * (64 * 128)) >> 4);
+            for (int j = 0; j < VU; ++j) {
+              const uint64_t vd = v_desc + ((rv.plus(j).slot * C::VB) >> 4);
 #pragma unroll
-                for (int k = 0; k < 64; k += 16)
-                  mma_ts(t_o + st * D + j * DV, tmem + buf * TK + 32 * h + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || h > 0 || !fresh);
-              }
-              umma::mma_commit(h == 0 ? &b_h[buf] : &b_o[buf]);
+              for (int k = 0; k < TK; k += 16)
+                mma_ts(t_o + st * D + j * DV, tmem + C::T_P + buf * C::P_STEP + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || !fresh);
             }
-            __syncwarp();
+            umma::mma_commit(&b_o[buf]);
           }
+          __syncwarp();
         }
 #pragma unroll
         for (int j = 0; j < VU; ++j) {
@@ -757,11 +770,16 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         if (nt > 0 && (NQ == 2 || me == 0)) wait_q();
         if constexpr (NQ == 2) {
 #pragma unroll 1
-          for (int i = -1; i < n && !gone; ++i) {  // P V of tile i, S of tile i + 1
-            if (i + 1 < n) wait_k();
+          for (int i = -1; i < n && !gone; ++i) {  // S of tile i + 1, P V of tile i
+            if (i + 1 < n) {
+              const bool use = i + 1 < nt;
+              wait_k();
+              if (use && cs > 0) wait(&b_sfree[st], (cs - 1) & 1);  // the last scores are in registers
+              if (use) ++cs;
+              make_s(st, use, i + 2 == nt);
+            }
             if (i >= 0) make_o(st, i < nt, i % kRun == 0, i >= look0);
             if (i >= 0 && i < nt) ++ct;
-            if (i + 1 < n) make_s(st, i + 1 < nt, i + 2 == nt);
           }
         } else {
 #pragma unroll 1
@@ -863,7 +881,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll 2
-                for (int ch = 0; ch < DV / 8; ++ch) {
+                for (int ch = 0; ch < DV / 8 && h * 64 + me < TK; ++ch) {
                   uint4* at = reinterpret_cast<uint4*>(unit + umma::rp_offset(h * 64 + me, ch * 8, TK));
                   const uint4 v = *at;
                   uint32_t e[4] = {v.x, v.y, v.z, v.w};
