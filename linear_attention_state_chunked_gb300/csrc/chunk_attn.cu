@@ -190,6 +190,18 @@ bool encode(CUtensorMap* map, const lin_kv_cache_t& c, void* base, int layer, in
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The packed queries as [token][head][channel], in boxes of 64 channels of an item's heads.
+bool encode_q(CUtensorMap* map, const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int heads, int tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(c.head_dim) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.head_dim), static_cast<cuuint64_t>(a.num_q_heads), static_cast<cuuint64_t>(a.tokens)};
+  const cuuint64_t strides[2] = {row, a.tokens > 1 ? static_cast<cuuint64_t>(a.token_stride) : row * a.num_q_heads};
+  const cuuint32_t boxes[3] = {64, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(tokens)}, ones[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
 cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int64_t items, int rows) {
   const unsigned x = static_cast<unsigned>(items < p.grid ? items : p.grid), y = (rows + kJoinRows - 1) / kJoinRows;
@@ -248,17 +260,18 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.part_ml = reinterpret_cast<float2*>(w);
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
-  p.box = 0;
+  p.box = p.q_box = 0;
   cudaError_t e;
   if (f.umma) {
-    CUtensorMap k = {}, v = {};
+    chunk::Maps m = {};
     int box = 32;  // of whole pages and tiles
     while (box >= 8 && (c.page_size % box || p.tk % box)) box /= 2;
-    if (box < 8) box = 0;
-    if (box && chunk::encode(&k, c, c.k, a.layer, box) && chunk::encode(&v, c, c.v, a.layer, box)) p.box = box;
-    e = c.head_dim == 64    ? chunk::launch_umma_d64(p, k, v, s)
-        : c.head_dim == 128 ? chunk::launch_umma_d128(p, k, v, s)
-                            : chunk::launch_umma_d256(p, k, v, s);
+    if (box >= 8 && chunk::encode(&m.k, c, c.k, a.layer, box) && chunk::encode(&m.v, c, c.v, a.layer, box)) p.box = box;
+    // a row tile of whole tokens is one box of the queries
+    if (128 % p.bheads == 0 && chunk::encode_q(&m.q, c, a, p.bheads, 128 / p.bheads)) p.q_box = 128 / p.bheads;
+    e = c.head_dim == 64    ? chunk::launch_umma_d64(p, m, s)
+        : c.head_dim == 128 ? chunk::launch_umma_d128(p, m, s)
+                            : chunk::launch_umma_d256(p, m, s);
   } else {
     e = c.head_dim == 64    ? chunk::launch_mma_d64(p, s)
         : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)

@@ -43,6 +43,7 @@ struct Plan {
   int tk;           // keys of a tile
   int grid, item_cost;
   int box;          // tokens of a TMA box of the cache; 0: none
+  int q_box;        // and of one of the queries, a row tile's
   float scale_log2;  // |scale| log2(e), never 0; q is negated where scale < 0
   uint32_t negate;
   uint32_t page_mul, page_shift;    // t / page_size = (mulhi(t, mul) + t) >> shift
@@ -253,13 +254,18 @@ __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
   return x;
 }
 
+// Tensor maps of the layer's keys and values and of the queries.
+struct Maps {
+  CUtensorMap k, v, q;
+};
+
 // One translation unit per head_dim and kind of kernel.
 cudaError_t launch_mma_d64(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d64(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
+cudaError_t launch_umma_d64(const Plan& p, const Maps& m, cudaStream_t s);
 cudaError_t launch_mma_d128(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d128(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
+cudaError_t launch_umma_d128(const Plan& p, const Maps& m, cudaStream_t s);
 cudaError_t launch_mma_d256(const Plan& p, cudaStream_t s);
-cudaError_t launch_umma_d256(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s);
+cudaError_t launch_umma_d256(const Plan& p, const Maps& m, cudaStream_t s);
 
 }  // namespace chunk
 }  // namespace lin

@@ -56,14 +56,14 @@ struct UCfg {
   static constexpr int D = D_, NQ = NQ_;
   static constexpr bool TMA = TMA_;
   static constexpr int TK = NQ == 1 ? 128 : D == 64 ? 96 : 80;
-  // a ring unit: 64 channels of a tile's K, up to 128 of its V
-  static constexpr int KU = D / 64, KB = TK * 64 * 2;
+  // a ring unit: 64 or 128 channels of a tile's K, up to 128 of its V
+  static constexpr int DK = NQ == 2 && D == 128 ? 128 : 64, KU = D / DK, KB = TK * DK * 2;
   static constexpr int DV = D < 128 ? D : 128, VU = D / DV, VB = TK * DV * 2;
   static constexpr int QT = 128 * D * 2;        // a row tile's queries
   static constexpr int SOFT = 4 * NQ;           // softmax warps
   static constexpr int STAGE = SOFT * 4096;     // where outputs are turned into rows
   // units of the rings: at least a tile of each
-  static constexpr int NK = D == 256 ? 5 : 6;
+  static constexpr int NK = D == 256 ? 5 : DK == 128 ? 3 : 6;
   static constexpr int NV = D == 64 ? 6 : NQ == 2 ? 3 : 2;
   static constexpr int RING = NK * KB + NV * VB;
   static constexpr int SMEM = RING + NQ * QT + STAGE;
@@ -128,6 +128,13 @@ __device__ __forceinline__ void load_box(const CUtensorMap* map, uint32_t dst, u
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(channel), "r"(token), "r"(head), "r"(page), "r"(umma::smem_u32(bar))
+      : "memory");
+}
+// A box of 64 channels of the queries: the item's heads of the row tile's tokens.
+__device__ __forceinline__ void load_q(const CUtensorMap* map, uint32_t dst, uint64_t* bar, int channel, int head, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(channel), "r"(head), "r"(token), "r"(umma::smem_u32(bar))
       : "memory");
 }
 // One lane of the warp, always the same (what it does stays in uniform registers).
@@ -227,8 +234,9 @@ struct At {
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-  constexpr int D = C::D, NQ = C::NQ, TK = C::TK, KU = C::KU, VU = C::VU, DV = C::DV, NK = C::NK, NV = C::NV;
+chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const __grid_constant__ CUtensorMap q_map) {
+  constexpr int D = C::D, NQ = C::NQ, TK = C::TK, KU = C::KU, VU = C::VU, DV = C::DV, DK = C::DK, NK = C::NK, NV = C::NV;
   constexpr int NT = C::THREADS, SOFT = C::SOFT;
   constexpr bool TMA = C::TMA;
   constexpr int KFULL = TMA ? 1 : 32 + 1, VFULL = TMA ? 2 : 32 + 2;  // arrivals of a full unit
@@ -249,7 +257,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) umma::mbar_init(&b_kfull[i], KFULL), umma::mbar_init(&b_kempty[i], NQ);
     for (int i = 0; i < NV; ++i) umma::mbar_init(&b_vfull[i], VFULL), umma::mbar_init(&b_vempty[i], NQ);
-    for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], 64), umma::mbar_init(&b_qfree[i], 1);
+    for (int i = 0; i < NQ; ++i) umma::mbar_init(&b_qfull[i], p.q_box ? 1 : 64), umma::mbar_init(&b_qfree[i], 1);
     for (int i = 0; i < 2; ++i) umma::mbar_init(&b_s[i], 2), umma::mbar_init(&b_sfree[i], 4), umma::mbar_init(&b_p[i], 4), umma::mbar_init(&b_o[i], 1);
     for (int i = 0; i < kCheckRing; ++i) umma::mbar_init(&b_look[i], (TMA ? 1 : 32) * VU), umma::mbar_init(&b_check[i], 2);
     for (int i = 0; i < kPieces; ++i) umma::mbar_init(&b_pfull[i], 1), umma::mbar_init(&b_pempty[i], SOFT + 2 + 2 + 2);
@@ -427,7 +435,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             add[k & 1] = fadd2(add[k & 1], f2pack(e0, e1));
             pk[k] = pack_bf16(e0, e1);
           }
-          sum = f2sum(fadd2(add[0], add[1]));
+          sum = mine ? f2sum(fadd2(add[0], add[1])) : 0.0f;
           if (look_up || !__any_sync(~0u, !(sum <= kMostSum))) break;
         }
         l += sum;
@@ -627,10 +635,12 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               if constexpr (TMA) {
                 if (lane == 0) mbar_expect(&b_kfull[rk.slot], C::KB);  // and passes on s_valid
                 __syncwarp();
-                if (lane * p.box < TK)
-                  load_box(&k_map, dst + lane * p.box * 128, &b_kfull[rk.slot], j * 64, in_page, hk, page);
+#pragma unroll
+                for (int h = 0; h < DK / 64; ++h)
+                  if (lane * p.box < TK)
+                    load_box(&k_map, dst + h * (TK * 128) + lane * p.box * 128, &b_kfull[rk.slot], j * DK + h * 64, in_page, hk, page);
               } else {
-                copies(c.k, dst, 8, j * 64);
+                copies(c.k, dst, DK / 8, j * DK);
                 arrive_copies(&b_kfull[rk.slot]);  // when they have landed: nobody waits here
                 if (lane == 0) mbar_arrive(&b_kfull[rk.slot]);
               }
@@ -707,9 +717,10 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           if (use) {
             umma::fence_after_sync();
             if (elect_one()) {
-              const uint64_t kd = k_desc + rk.slot * (C::KB >> 4), qd = q_desc + ((st * C::QT + j * (128 * 128)) >> 4);
+              const uint64_t kd = k_desc + rk.slot * (C::KB >> 4), qd = q_desc + ((st * C::QT + j * (DK / 64 * 128 * 128)) >> 4);
 #pragma unroll
-              for (int k = 0; k < 64; k += 16) umma::mma_f16(tmem + buf * TK, qd + (k * 2 >> 4), kd + (k * 2 >> 4), id_s, j > 0 || k > 0);
+              for (int k = 0; k < DK; k += 16)
+                umma::mma_f16(tmem + buf * TK, qd + ((k / 64 * (128 * 128) + k % 64 * 2) >> 4), kd + ((k / 64 * (TK * 128) + k % 64 * 2) >> 4), id_s, j > 0 || k > 0);
               if (j == KU - 1) {
                 umma::mma_commit(&b_s[buf]);
                 if (last) umma::mma_commit(&b_qfree[st]);
@@ -745,19 +756,15 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
                 mma_ts(t_o + st * D + j * DV, tmem + C::T_P + buf * C::P_STEP + k / 2, vd + (k * 128 >> 4), id_o, k > 0 || !fresh);
             }
             umma::mma_commit(&b_o[buf]);
+#pragma unroll
+            for (int j = 0; j < VU; ++j) umma::mma_commit(&b_vempty[rv.plus(j).slot]);
           }
           __syncwarp();
-        }
+        } else if (lane == 0) {
 #pragma unroll
-        for (int j = 0; j < VU; ++j) {
-          if (use) {
-            if (elect_one()) umma::mma_commit(&b_vempty[rv.slot]);
-            __syncwarp();
-          } else if (lane == 0) {
-            mbar_arrive(&b_vempty[rv.slot]);
-          }
-          rv.step(1);
+          for (int j = 0; j < VU; ++j) mbar_arrive(&b_vempty[rv.plus(j).slot]);
         }
+        rv.step(VU);
       };
       auto wait_q = [&]() {
         wait(&b_qfull[st], qn++ & 1);
@@ -848,8 +855,8 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
 #pragma unroll 1
       while (const UPiece* piece = take()) {
         const int n = piece->n, look0 = piece->check0 - piece->x.t0, tokens = piece->x.tokens, heads = piece->x.heads;
-        const int nt[2] = {piece->nt[0], piece->nt[1]};
-        const char* const src = static_cast<const char*>(a.q) + int64_t(piece->x.row0) * a.token_stride + int64_t(piece->x.head0) * (D * 2);
+        const int nt[2] = {piece->nt[0], piece->nt[1]}, row0 = piece->x.row0, head0 = piece->x.head0;
+        const char* const src = static_cast<const char*>(a.q) + int64_t(row0) * a.token_stride + int64_t(head0) * (D * 2);
         give_back();
 #pragma unroll
         for (int st = 0; st < NQ; ++st) {
@@ -858,6 +865,15 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
           if (gone) break;
           ++qn[st];
           const uint32_t dst = umma::smem_u32(qbuf) + st * C::QT;
+          if (p.q_box) {  // (what other tokens' rows come with it, no output takes)
+            if (me == 0) {
+              mbar_expect(&b_qfull[st], C::QT);
+#pragma unroll
+              for (int d = 0; d < D; d += 64)
+                load_q(&q_map, dst + d / 64 * (128 * 128), &b_qfull[st], d, head0, row0 + st * p.q_box);
+            }
+            continue;
+          }
 #pragma unroll 2
           for (int k = me; k < 128 * CPR; k += 64) {
             const int row = k / CPR, ch = k % CPR;
@@ -910,6 +926,11 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         }
         if (gone) break;
       }
+      if (gone && p.q_box)  // copies in flight land before the block ends
+#pragma unroll
+        for (int st = 0; st < NQ; ++st)
+          for (uint32_t i = 0; qn[st] > 0 && i < kWaitTries >> 8 && !umma::mbar_try_wait(&b_qfull[st], (qn[st] - 1) & 1); ++i) {
+          }
       attn::cp_wait_all();
     }
   }
@@ -928,7 +949,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
 }
 
 template <class C>
-cudaError_t launch_umma(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+cudaError_t launch_umma(const Plan& p, const Maps& m, cudaStream_t s) {
   auto kern = chunk_umma_kernel<C>;
   static bool ready[kMaxDevices];  // set twice at worst, to the same value
   int dev = 0;
@@ -939,20 +960,20 @@ cudaError_t launch_umma(const Plan& p, const CUtensorMap& k, const CUtensorMap& 
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) ready[dev] = true;
   }
-  kern<<<p.grid, C::THREADS, C::SMEM, s>>>(p, k, v);
+  kern<<<p.grid, C::THREADS, C::SMEM, s>>>(p, m.k, m.v, m.q);
   return cudaGetLastError();
 }
 
 template <int D, int NQ>
-cudaError_t launch_umma_loads(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  return p.box ? launch_umma<UCfg<D, NQ, true>>(p, k, v, s) : launch_umma<UCfg<D, NQ, false>>(p, k, v, s);
+cudaError_t launch_umma_loads(const Plan& p, const Maps& m, cudaStream_t s) {
+  return p.box ? launch_umma<UCfg<D, NQ, true>>(p, m, s) : launch_umma<UCfg<D, NQ, false>>(p, m, s);
 }
 
 template <int D>
-cudaError_t launch_umma_tiles(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
+cudaError_t launch_umma_tiles(const Plan& p, const Maps& m, cudaStream_t s) {
   if constexpr (D <= 128)
-    if (p.rows == 256) return launch_umma_loads<D, 2>(p, k, v, s);
-  return launch_umma_loads<D, 1>(p, k, v, s);
+    if (p.rows == 256) return launch_umma_loads<D, 2>(p, m, s);
+  return launch_umma_loads<D, 1>(p, m, s);
 }
 
 }  // namespace chunk

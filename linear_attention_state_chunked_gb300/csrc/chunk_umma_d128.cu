@@ -5,8 +5,8 @@
 namespace lin {
 namespace chunk {
 
-cudaError_t launch_umma_d128(const Plan& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s) {
-  return launch_umma_tiles<128>(p, k, v, s);
+cudaError_t launch_umma_d128(const Plan& p, const Maps& m, cudaStream_t s) {
+  return launch_umma_tiles<128>(p, m, s);
 }
 
 }  // namespace chunk
