@@ -11,7 +11,8 @@ namespace {
 
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;      // rows of a block: a lane each
-constexpr int kManyParts = 8;      // see launch_attn_chunk
+constexpr int kManyParts = 8;      // of an item: see launch_attn_chunk
+constexpr int kManyItems = 4;      // of a CTA: the same
 
 // The x-th of the ranges whose last item goes on past them, by a whole warp; false
 // where there are fewer.
@@ -149,7 +150,7 @@ int sm_count() {
 
 size_t bytes_of(const lin_kv_cache_t& c, const Shape& f) {
   const size_t grid = size_t(sm_count()) * f.ctas;
-  return 2 * grid * f.rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(Split);
+  return 2 * grid * f.rows * (c.head_dim * sizeof(float) + sizeof(float2)) + grid * sizeof(Split) + 16;
 }
 
 // Granlund and Montgomery's division by an invariant: s = ceil(log2 d),
@@ -260,6 +261,14 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.part_ml = reinterpret_cast<float2*>(w);
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
+  w += size_t(p.grid) * sizeof(chunk::Split);
+  // Items of the batch at most. Many for a CTA: one by one from a counter.
+  const int64_t items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
+  p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid ? reinterpret_cast<int*>(w) : nullptr;
+  if (p.ticket) {
+    const cudaError_t e = cudaMemsetAsync(p.ticket, 0, sizeof(int), s);
+    if (e != cudaSuccess) return e;
+  }
   p.box = p.q_box = 0;
   cudaError_t e;
   if (f.umma) {
@@ -277,7 +286,7 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
         : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)
                             : chunk::launch_mma_d256(p, s);
   }
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.ticket) return e;
   // the join's launch overlaps the main kernel, and it waits there for its end
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -287,9 +296,8 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(chunk::kJoinWarps * 32);
-  // Items of the batch at most, and rows of one: few items have many parts each (one
-  // request's last tokens over a long cache), which the warps of a block then share.
-  const int64_t items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
+  // Few items have many parts each (one request's last tokens over a long cache), which
+  // the warps of a block then share.
   const int64_t most = int64_t(a.tokens) * p.bheads;
   const int rows = most < p.rows ? static_cast<int>(most) : p.rows;
   return c.head_dim == 64    ? chunk::launch_join<64>(cfg, p, items, rows)

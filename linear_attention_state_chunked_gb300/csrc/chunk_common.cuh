@@ -12,6 +12,13 @@
 // sum) of each piece in the workspace, and a second kernel joins them in range order, so
 // results do not depend on timing. A request's items have a closed sum (keys grow by m
 // from one to the next), so no kernel has to lay the items out.
+//
+// Batches of many items per CTA (the tensor-memory kernel) are not cut: a CTA takes the
+// next item from a counter whenever it begins one. So the items under way at a time are
+// neighbours, which share their keys and values in L2 (64 chunks of up to 512 tokens after
+// up to 8,000, heads of 256, whose cache is four times the L2: 1,707 us by ranges); a
+// request's items come longest first, so that the last ones are short. Whole items, so
+// again the result does not depend on who took them.
 #pragma once
 
 #include <cuda.h>
@@ -51,6 +58,7 @@ struct Plan {
   float* part;       // [2 grid][D / 4][rows][4] value sums of unfinished pieces: a warp's rows side by side
   float2* part_ml;   // [2 grid][rows] their (maximum, sum)
   Split* split;      // [grid]
+  int* ticket;       // items handed out so far, where they are taken one by one; else NULL
 };
 
 __device__ __forceinline__ int page_of(const Plan& p, int t) { return (__umulhi(t, p.page_mul) + t) >> p.page_shift; }
@@ -257,6 +265,57 @@ __device__ __forceinline__ Piece walk_next(const Plan& p, Walk& w) {
 // Tensor maps of the layer's keys and values and of the queries.
 struct Maps {
   CUtensorMap k, v, q;
+};
+
+// Hands out whole items by the counter, by a whole warp.
+struct Tickets {
+  int r0;           // lane l looks at request r0 + l
+  int64_t base;     // items before these
+  int64_t upto;     // and up to the lane's request, of these
+  Req q;
+  __device__ __forceinline__ void look(const Plan& p, int r) {
+    const int lane = threadIdx.x & 31;
+    r0 = r;
+    q.items = q.n = 0;
+    if (r0 + lane < p.a.batch) q = request(p, r0 + lane, false);
+    upto = int64_t(q.items) * p.heads;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, upto, o);
+      if (lane >= o) upto += x;
+    }
+  }
+  __device__ __forceinline__ void begin(const Plan& p) {
+    base = 0;
+    look(p, 0);
+  }
+  __device__ __forceinline__ Piece next(const Plan& p) {
+    const int lane = threadIdx.x & 31;
+    Piece x;
+    x.r = -1;
+    int64_t at = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
+    at = __shfl_sync(~0u, at, 0);
+    uint32_t past;
+#pragma unroll 1
+    while ((past = __ballot_sync(~0u, at < base + upto)) == 0) {
+      base += __shfl_sync(~0u, upto, 31);
+      if (r0 + 32 >= p.a.batch) return x;
+      look(p, r0 + 32);
+    }
+    const int l = __ffs(past) - 1;
+    const int items = __shfl_sync(~0u, q.items, l), n = __shfl_sync(~0u, q.n, l);
+    const int64_t off = at - base - (__shfl_sync(~0u, upto, l) - int64_t(items) * p.heads);
+    const int h = static_cast<int>(off / items), j = items - 1 - static_cast<int>(off - int64_t(h) * items);
+    const int kv = h / p.blocks, hb = h - kv * p.blocks;
+    x.r = r0 + l, x.hk = kv;
+    x.head0 = kv * p.group + hb * p.bheads, x.heads = min(p.bheads, p.group - hb * p.bheads);
+    x.row0 = __shfl_sync(~0u, q.cu, l) + j * p.m, x.tokens = min(p.m, n - j * p.m);
+    x.pos = __shfl_sync(~0u, q.base, l) + j * p.m;
+    x.keys = max(0, x.pos + x.tokens);
+    x.t0 = 0, x.t1 = (max(x.keys, 1) + p.tk - 1) / p.tk;
+    x.whole = 1, x.part = 2 * blockIdx.x + 1;
+    return x;
+  }
 };
 
 // One translation unit per head_dim and kind of kernel.

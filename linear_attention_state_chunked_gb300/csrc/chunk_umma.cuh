@@ -266,7 +266,14 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     s_dead = 0;
   }
   Walk w;
-  if (!walk_begin<NT>(p, w, s_walk)) return;
+  if (!p.ticket) {
+    if (!walk_begin<NT>(p, w, s_walk)) return;
+  } else if (blockIdx.x == 0) {
+#pragma unroll 1
+    for (int r = tid; r < a.batch; r += NT) request(p, r, true);
+  }
+  // pieces handed out ahead: the next alone where another CTA could take it
+  const int pieces = p.ticket ? 1 : kPieces;
   if (warp == SOFT + 2) umma::tmem_alloc(&s_tmem, C::TMEM);
   umma::fence_before_sync();
   __syncthreads();
@@ -302,7 +309,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   auto give_back = [&]() {
     __syncwarp();
     if (lane == 0) mbar_arrive(&b_pempty[at_piece]);
-    if (++at_piece == kPieces) at_piece = 0, piece_phase ^= 1;
+    if (++at_piece == pieces) at_piece = 0, piece_phase ^= 1;
   };
 
   if (warp < SOFT) {
@@ -810,12 +817,19 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       }
     } else if (warp == SOFT + 4) {
       // ---- pieces -------------------------------------------------------------------------
-      if (lane == 0) {
-        UPiece y;
-        int g = 0;
+      UPiece y;
+      Tickets tickets;
+      int g = 0;
+      if (p.ticket) tickets.begin(p);
 #pragma unroll 1
-        do {
+      do {
+        wait(&b_pempty[at_piece], piece_phase ^ 1);
+        if (gone) break;
+        if (p.ticket)
+          y.x = tickets.next(p);
+        else if (lane == 0)
           y.x = walk_next(p, w);
+        if (lane == 0) {
           const Piece& x = y.x;
           y.n = 0, y.g0 = g, y.check0 = INT_MAX;
           y.nt[0] = y.nt[1] = 0;
@@ -833,19 +847,12 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             if (TMA && x.keys % p.box) y.check0 = min(y.check0, x.keys / TK);
             g += y.n;
           }
-          uint32_t left = kWaitTries;
-#pragma unroll 1
-          while (left > 0 && !umma::mbar_try_wait(&b_pempty[at_piece], piece_phase ^ 1)) --left;
-          if (left == 0) {
-            gone = true;
-            break;
-          }
           s_piece[at_piece] = y;
           mbar_arrive(&b_pfull[at_piece]);
-          if (++at_piece == kPieces) at_piece = 0, piece_phase ^= 1;
-        } while (y.x.r >= 0);
-      }
-      __syncwarp();
+        }
+        if (++at_piece == pieces) at_piece = 0, piece_phase ^= 1;
+        y.x.r = __shfl_sync(~0u, y.x.r, 0);
+      } while (y.x.r >= 0);
     } else if (warp < SOFT + 7) {
       // ---- queries, and a look at the values -------------------------------------------------
       constexpr int CPR = D / 8;
@@ -942,7 +949,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     // a wait ran out: what this range leaves unwritten counts as left out
     for (int x = tid; x < 2 * p.rows; x += NT) p.part_ml[2 * int64_t(blockIdx.x) * p.rows + x] = make_float2(-INFINITY, attn::kLeftOut);
     if (tid == 0) {
-      p.split[blockIdx.x].parts = 0;
+      if (!p.ticket) p.split[blockIdx.x].parts = 0;
       report(a.status, LIN_ST_TIMEOUT);
     }
   }
