@@ -136,7 +136,7 @@ Shape shape_of(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int out_
   if (c.dtype == LIN_BF16 && out_dtype == LIN_BF16) {
     const int64_t rows = int64_t(a.tokens) * (a.num_q_heads / c.num_kv_heads);  // of a kv head
     const bool two = c.head_dim <= 128 && rows > 128 * int64_t(a.batch);
-    return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 192};
+    return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 384};
   }
   const int row_bytes = c.head_dim * dtype_size(c.dtype);
   return {false, 64, row_bytes >= 512 ? 16 : 32, row_bytes <= 256 ? 3 : row_bytes == 512 ? 2 : 1, 64};

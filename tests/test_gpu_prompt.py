@@ -362,12 +362,13 @@ def test_chunk_bad_pages_are_not_seen(dtype, D):
     assert not out[80:85].any()
 
 
-@pytest.mark.parametrize("dtype,D", [(BF, 64), (BF, 128), (BF, 256), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("dtype,D,ps", [(BF, 64, 16), (BF, 128, 16), (BF, 128, 7), (BF, 256, 16), (BF, 256, 9), (F32, 64, 16),
+                                        (F32, 256, 16)])
 @pytest.mark.parametrize("what", [float("nan"), float("inf")])
-def test_chunk_hidden_values_have_no_part(dtype, D, what):
+def test_chunk_hidden_values_have_no_part(dtype, D, ps, what):
     """Keys and values of a later token of the same prompt may be anything: queries before
     it keep their bits, those that see it do not pass for finite."""
-    cached, new, ps = [200, 0], [300, 290], 16
+    cached, new = [200, 0], [300, 290]
     cache, table, q, cu, lens = chunk_inputs(cached, new, ps, 4, 2, D, dtype, seed=8)
 
     def run():
@@ -408,6 +409,93 @@ def test_chunk_same_bits_again_and_on_another_stream(dtype):
                            kv_len=tables[2], stream=side)
     side.synchronize()
     assert torch.equal(a, b) and torch.equal(a, out)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n_hi,Hq", [(16, 8), (40, 4)])
+def test_chunk_tails_of_many_requests(D, n_hi, Hq):
+    """Items of a few tiles that cross the CTAs' ranges everywhere, several pieces to a
+    CTA, with one row tile and with two: the same bits each time."""
+    rng = np.random.default_rng(D + n_hi)
+    cached = rng.integers(300, 2200, 24).tolist()
+    new = rng.integers(1, n_hi + 1, 24).tolist()
+    x = chunk_inputs(cached, new, 48, Hq, 1, D, BF, seed=D)
+    a = check_chunk(*x, BF)
+    for _ in range(4):
+        assert torch.equal(a, check_chunk(*x, BF))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,ps", [(64, 8, 8, 16), (128, 4, 4, 12), (128, 16, 4, 64), (256, 16, 4, 8), (64, 3, 3, 20)])
+def test_chunk_batches_of_many_items(D, Hq, Hkv, ps):
+    """More than four items to a CTA, which are handed out one by one: requests without
+    tokens, with one, with many; padding; rows behind the last one."""
+    rng = np.random.default_rng(D)
+    cached = rng.integers(0, 200, 90).tolist()
+    new = rng.choice([0, 1, 2, 63, 64, 65, 130, 260], 90).tolist()
+    cached[7], new[7] = -1, 0
+    G, m = Hq // Hkv, (256 if D < 256 else 128)
+    rows = int(4.5 * 152 / Hkv * (m // G))  # a captured call's room
+    x = chunk_inputs(cached, new, ps, Hq, Hkv, D, BF, seed=D, spare=max(0, rows - sum(new)))
+    a = check_chunk(*x, BF)
+    assert torch.equal(a, check_chunk(*x, BF))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ps", [5, 20, 40])
+@pytest.mark.parametrize("hnd", [False, True])
+def test_chunk_pages_of_any_size(D, ps, hnd):
+    """Pages that TMA takes in boxes of 8 and those that it does not."""
+    cached, new = [5, 300, 0], [60, 70, 290]
+    x = chunk_inputs(cached, new, ps, 4, 2, D, BF, seed=ps, hnd=hnd, layers=2)
+    check_chunk(*x, BF, layer=1)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(300, 2), (3, 8)])
+def test_chunk_long_sums_keep_their_size(D, n, G):
+    """Values of one sign over more tokens than a run of the tensor unit, whose sums lose
+    towards 0: the mean output stays within 2^-11, the documented loss, and the weights'
+    rounding, which is of no sign (2^-9 rms over sqrt(tokens): nothing)."""
+    length, ps, H = 70000, 64, 1
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    pages = -(-length // ps)
+    k = torch.randn((1, pages, ps, H, D), generator=gen, device="cuda").to(BF)
+    v = (torch.rand((1, pages, ps, H, D), generator=gen, device="cuda") + 0.5).to(BF)
+    cache = L.KVCache(1, pages, ps, H, D, k=k, v=v)
+    q = (torch.randn((n, G, D), generator=gen, device="cuda") * 0.2).to(BF)
+    out = torch.empty_like(q)
+    # (one item of 70,000 keys is cut into ranges; many requests over the same pages are not)
+    B = 170 if n == 300 else 1
+    rep = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(B, 1)
+    qs, outs = q.repeat(B, 1, 1), out.repeat(B, 1, 1)
+    L.lin_state_attn_chunk(cache, layer=0, q=qs, out=outs, page_table=rep, cu_seqlens=i32(np.arange(B + 1) * n),
+                           kv_len=i32([length] * B))
+    got = outs[-n:].double()
+    kk, vv = k.reshape(-1, D)[:length].double(), v.reshape(-1, D)[:length].double()
+    rows = range(0, n, 37)
+    for j in rows:
+        s = (q[j].double() @ kk.T) * D ** -0.5
+        s[:, length - n + j + 1:] = -float("inf")
+        want = torch.softmax(s, -1) @ vv
+        assert abs(float((got[j] - want).mean() / want.mean())) < 2.0 ** -11
+        assert float(((got[j] - want) / want).abs().max()) < 2.0 ** -8 + 2.0 ** -10
+
+
+def test_chunk_references_move():
+    """Scores that grow along the keys by far more than a weight may: the reference moves
+    in many tiles, in the first and the last of a piece, and some rows' alone."""
+    for D, n, c in ((64, 200, 900), (128, 200, 900), (256, 100, 900), (128, 3, 5000)):
+        cache, table, q, cu, lens = chunk_inputs([c], [n], 16, 4, 2, D, BF, seed=D)
+        t = torch.arange(lens[0])
+        for h in range(2):
+            grow = (1.0 + t / 20.0) * (1.0 if h == 0 else (t % 3 == 0).float())
+            key = torch.zeros(lens[0], D)
+            key[:, 0] = grow
+            pages = table[0, t // 16].long().cuda()
+            cache.k[0][pages, (t % 16).cuda(), h] = key.to(BF).cuda()
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(1)).to(BF).cuda())
+        q[:, :, 0] = (torch.rand(q.shape[:2], generator=torch.Generator().manual_seed(2)) * 60 - 20).to(BF).cuda()
+        check_chunk(cache, table, q, cu, lens, BF)
 
 
 def test_a_captured_prompt_follows_its_lengths():
