@@ -127,16 +127,24 @@ LIN_API int lin_state_rope(const lin_kv_cache_t* cache, const lin_rope_args_t* a
  * (LIN_ST_BAD_SEQLEN). A page id outside [0, num_pages) sets LIN_ST_BAD_PAGE and that
  * page's tokens count as not seen.
  * Precision: scores, the softmax and the sums over values are fp32. bf16 caches with
- * bf16 outputs multiply on tensor cores with the weights rounded to bf16 (their sum is
- * that of the unrounded ones); fp32 outputs take the weights in three bf16 parts; fp32
- * caches multiply with every operand in two tf32 parts. Visible NaN give NaN; visible
- * infinities may, and values from 2^120 on infinities. Results do not depend on
- * timing: the same call gives the same bits.
- * Lengths are read on the device; the batch's work is cut into equal ranges for the
- * SMs, and blocks of queries that cross a border are joined by a second launch.
+ * bf16 outputs multiply on tensor cores with the weights rounded to bf16 (2^-8 at most,
+ * 2^-9 rms; their sum is that of the unrounded ones), and the tensor unit's own value
+ * sums, which cut off below the last place of fp32, end after 32,768 tokens at most: less
+ * than 2^-11 of the sum p |v| at any length. fp32 outputs take the weights in three bf16
+ * parts, fp32 caches every operand in two tf32 parts, and add every 16 tokens with
+ * rounding. Visible NaN give NaN; visible infinities may, and values from 2^120 on
+ * infinities. Results do not depend on timing: the same call gives the same bits. Nor does
+ * a row depend on what other rows see.
+ * Lengths are read on the device. The batch's work is cut into equal ranges for the SMs,
+ * and blocks of queries that cross a border are joined by a second launch; where `tokens`
+ * allows many blocks for each SM (bf16 outputs), they are taken one by one from a counter
+ * in the workspace, which a memset zeroes.
+ * Pages of a multiple of 8 tokens load faster (by TMA) than others, and so do queries
+ * whose heads per kv head divide 128.
+ * out must not overlap anything that is read.
  * Workspace: lin_state_attn_chunk_workspace() bytes of device memory, 16-byte aligned,
  * not shared by calls that may overlap. The size never shrinks as batch, tokens,
- * num_q_heads or max_pages grow and covers either output type, up to some 80 MB. Its
+ * num_q_heads or max_pages grow and covers either output type, some 40 MB at most (152 SMs). Its
  * contents before the call do not matter. Longest request: 2^31 - 65536 tokens. */
 typedef struct {
   int32_t layer, batch, tokens, num_q_heads;

@@ -264,7 +264,7 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   w += size_t(p.grid) * sizeof(chunk::Split);
   // Items of the batch at most. Many for a CTA: one by one from a counter.
   const int64_t items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
-  p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid ? reinterpret_cast<int*>(w) : nullptr;
+  p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid && items < (1 << 30) ? reinterpret_cast<int*>(w) : nullptr;
   if (p.ticket) {
     const cudaError_t e = cudaMemsetAsync(p.ticket, 0, sizeof(int), s);
     if (e != cudaSuccess) return e;
