@@ -139,7 +139,7 @@ Shape shape_of(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int out_
     return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 384};
   }
   const int row_bytes = c.head_dim * dtype_size(c.dtype);
-  return {false, 64, row_bytes >= 512 ? 16 : 32, row_bytes <= 256 ? 3 : row_bytes == 512 ? 2 : 1, 64};
+  return {false, 64, row_bytes >= 512 ? 16 : 32, c.head_dim == 256 ? 1 : c.head_dim == 128 ? 2 : 3, c.head_dim == 256 ? 128 : 64};
 }
 
 int sm_count() {

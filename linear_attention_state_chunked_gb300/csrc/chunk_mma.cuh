@@ -4,9 +4,13 @@
 //
 // over the tokens up to the query's own; one pass over tiles of TK keys with a running
 // maximum m and sum per row. A warp owns 16 rows (tokens x query heads of one kv head)
-// and keeps their softmax state and value sums in registers; K and V tiles come by
-// 16-byte asynchronous copies (pages may end anywhere) into a ring of three, swizzled so
-// that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
+// and keeps their softmax state and value sums in registers. Four warps have an item's 64
+// rows; for heads of 256, whose rows leave room for one block on an SM, there are two such
+// groups, which take every other tile and are joined at a piece's end (fp32, 1,000 tokens
+// after 1,000, 16 / 4 heads: of 256 811 us with one group, 618 with two; of 128, where two
+// blocks fit, 310 and 335). K and V
+// tiles come by 16-byte asynchronous copies (pages may end anywhere), two tiles ahead,
+// swizzled so that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
 // (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
 // so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
 #pragma once
@@ -22,19 +26,31 @@ struct MCfg {
   static constexpr int D = D_, DT = DT_;
   static constexpr bool BF = DT == LIN_BF16;
   static constexpr int ES = BF ? 2 : 4, ROWB = D * ES;
-  static constexpr int WARPS = 4, NT = WARPS * 32, ROWS = WARPS * 16;
+  static constexpr int GROUPS = D == 256 ? 2 : 1, GT = 128, NT = GROUPS * GT, ROWS = 64;
   static constexpr int TK = ROWB >= 512 ? 16 : 32;
-  static constexpr int STAGES = 3, STAGE = 2 * TK * ROWB;
+  static constexpr int STAGES = GROUPS == 1 ? 3 : 4, STAGE = 2 * TK * ROWB;
   static constexpr int QB = ROWS * ROWB;
   static constexpr int SMEM = STAGES * STAGE + QB;
-  static constexpr int FIT = 220 * 1024 / SMEM;
-  static constexpr int CTAS = FIT < 3 ? FIT : 3;
+  static constexpr int CTAS = D == 256 ? 1 : D == 128 ? 2 : 3;
+  static_assert(SMEM * CTAS <= 220 * 1024 && SMEM >= GT * (D / 2 + 4) * 4, "");
 };
+
+// Barriers of a group's four warps.
+__device__ __forceinline__ bool group_any(int group, bool x) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbar.red.or.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(static_cast<int>(x)), "r"(group + 1)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void group_wait(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
 
 template <class C, int PT>
 __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p) {
   using namespace attn;
-  constexpr int D = C::D, TK = C::TK, NT = C::NT, ROWB = C::ROWB, CPR = ROWB / 16;
+  constexpr int D = C::D, TK = C::TK, NT = C::NT, GT = C::GT, ROWB = C::ROWB, CPR = ROWB / 16;
   constexpr bool BF = C::BF;
   constexpr int NB = TK / 8;  // key blocks of a tile
   constexpr uint32_t ALL = TK == 32 ? ~0u : (1u << (TK & 31)) - 1u;
@@ -43,7 +59,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
   __shared__ Piece s_piece;
   __shared__ uint32_t s_valid[4];
   asm volatile("griddepcontrol.launch_dependents;");
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, group = tid / C::GT, gtid = tid % C::GT, warp = gtid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const lin_kv_cache_t& c = p.c;
   const lin_attn_chunk_args_t& a = p.a;
@@ -64,12 +80,12 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
     // lane l of every warp looks up key l % TK of a tile
     int key = x.t0 * TK + (lane & (TK - 1));
     int id = key < x.keys ? table[page_of(p, key)] : -1;
-    auto fill = [&](int tile, int stage) {
+    auto fill = [&](int, int stage) {
       const bool live = static_cast<uint32_t>(id) < static_cast<uint32_t>(c.num_pages);
       if (key < x.keys && !live && tid < TK) report(a.status, LIN_ST_BAD_PAGE);
       const int64_t off = live ? id * c.page_stride + (key - page_of(p, key) * c.page_size) * c.token_stride : 0;
       const uint32_t valid = __ballot_sync(~0u, live) & ALL;
-      if (tid == 0) s_valid[tile & 3] = valid;
+      if (tid == 0) s_valid[stage] = valid;
       const uint32_t dst = ring + stage * C::STAGE;
 #pragma unroll
       for (int i = 0; i < TK * CPR / NT; ++i) {
@@ -113,20 +129,27 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
       for (int k = 0; k < 4; ++k) o[i][k] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
+    // Tile i of the piece lies in stage i % STAGES and is group i % GROUPS's; GROUPS tiles
+    // at a time, and as many (2 with one group) under way.
+    constexpr int STEP = C::GROUPS, AHEAD = C::STAGES - STEP;
     const int tiles = x.t1 - x.t0;
-    fill(x.t0, 0);
-    cp_commit();
-    if (tiles > 1) fill(x.t0 + 1, 1);
-    cp_commit();
-    int stage = 0;
-    for (int i = 0; i < tiles; ++i) {
-      const int tile = x.t0 + i, key0 = tile * TK;
-      cp_wait<1>();
-      __syncthreads();
-      if (i + 2 < tiles) fill(tile + 2, stage == 0 ? 2 : stage - 1);
+    auto fill_next = [&](int i) {
+#pragma unroll
+      for (int k = 0; k < STEP; ++k)
+        if (i + k < tiles) fill(i + k, (i + k) % C::STAGES);
       cp_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < AHEAD; i += STEP) fill_next(i);
+#pragma unroll 1
+    for (int i0 = 0; i0 < tiles; i0 += STEP) {
+      cp_wait<AHEAD / STEP - 1>();
+      __syncthreads();  // these tiles are there, and the last ones have been used
+      fill_next(i0 + AHEAD);
+      const int i = i0 + group;
+      if (i >= tiles) continue;
+      const int key0 = (x.t0 + i) * TK, stage = i % C::STAGES;
       const uint32_t ks = ring + stage * C::STAGE, vs = ks + TK * ROWB;
-      if (++stage == C::STAGES) stage = 0;
 
       // ---- scores ---------------------------------------------------------------
       float s[NB][4];
@@ -185,7 +208,7 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
       }
 
       // ---- softmax ----------------------------------------------------------------
-      const uint32_t valid = s_valid[tile & 3];
+      const uint32_t valid = s_valid[stage];
       const bool masked = key0 + TK > all_see || valid != ALL;
       uint32_t vis[2] = {~0u, ~0u};
       if (masked) {
@@ -228,14 +251,14 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
       // rows that see them (0 NaN is NaN, and hidden ones must have no part).
       if (masked) {
         bool wild = false;
-        for (int y = tid; y < TK * CPR; y += NT) {
+        for (int y = gtid; y < TK * CPR; y += GT) {
           const uint4 v = *reinterpret_cast<const uint4*>(smem + (vs - ring) + y * 16);
           const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             wild |= (q[k] & 0x7f800000u) == 0x7f800000u || (BF && (q[k] & 0x7f80u) == 0x7f80u);
         }
-        if (__syncthreads_or(wild)) {
+        if (group_any(group, wild)) {
 #pragma unroll 1
           for (int t = 0; t < TK; ++t) {
 #pragma unroll
@@ -251,15 +274,15 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
                 }
               }
           }
-          __syncthreads();
-          for (int y = tid; y < TK * ROWB / 4; y += NT) {
+          group_wait(group);
+          for (int y = gtid; y < TK * ROWB / 4; y += GT) {
             uint32_t& v = reinterpret_cast<uint32_t*>(smem + (vs - ring))[y];
             if (BF)
               v = finite_bf16(v);
             else if ((v & 0x7f800000u) == 0x7f800000u)
               v = 0;
           }
-          __syncthreads();
+          group_wait(group);
         }
       }
 
@@ -323,12 +346,41 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
     }
     cp_wait_all();
 
-    // ---- the piece's end ------------------------------------------------------------
+    // ---- the piece's end: the second group's sums go to the first --------------------
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      float sum = l[k];
-      sum += __shfl_xor_sync(~0u, sum, 1);
-      sum += __shfl_xor_sync(~0u, sum, 2);
+      l[k] += __shfl_xor_sync(~0u, l[k], 1);
+      l[k] += __shfl_xor_sync(~0u, l[k], 2);
+    }
+    if constexpr (C::GROUPS == 2) {
+      float* const other = reinterpret_cast<float*>(smem) + gtid;  // a thread's values GT apart
+      __syncthreads();
+      if (group == 1) {
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) other[(d * 4 + k) * GT] = o[d][k];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) other[(D / 2 + k) * GT] = m[k], other[(D / 2 + 2 + k) * GT] = l[k];
+      }
+      __syncthreads();
+      if (group == 1) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float m1 = other[(D / 2 + k) * GT], l1 = other[(D / 2 + 2 + k) * GT], top = fmaxf(m[k], m1);
+        // 0 where a group saw nothing (a NaN sum goes on)
+        const float f0 = l[k] == 0.0f ? 0.0f : m[k] == top ? 1.0f : exp2_fast(m[k] - top);
+        const float f1 = l1 == 0.0f ? 0.0f : m1 == top ? 1.0f : exp2_fast(m1 - top);
+        l[k] = fmaf(f0, l[k], f1 * l1), m[k] = top;
+#pragma unroll
+        for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+          for (int y = 2 * k; y < 2 * k + 2; ++y) o[d][y] = fmaf(f0, o[d][y], f1 * other[(d * 4 + y) * GT]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float sum = l[k];
       const int row = warp * 16 + g + 8 * k, i = token_of(p, row);
       const float f = !x.whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       if (!mine[k]) continue;
