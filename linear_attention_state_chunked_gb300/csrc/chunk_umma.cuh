@@ -3,8 +3,15 @@
 //   S = Q K^T,  P = 2^(S scale log2(e) - m),  O = sum over tiles of P V,  out = O / sum P
 //
 // in tiles of 128 rows (new tokens x query heads of one kv head) and TK keys, with a
-// running maximum and sum per row. Bound by the tensor unit for prompts: 4 head_dim
-// flops per visible (row, key); by HBM for a few rows over a long cache.
+// running maximum and sum per row. A prompt's floor is the tensor unit's (4 head_dim flops
+// per visible row and key), that of a few rows over a long cache HBM's. Measured:
+//   8 prompts of 4,096 tokens, 16 / 2 heads of 128             447 us, 1,232 TFLOP/s
+//   1,024 tokens after 31,000, 32 / 8 heads of 128             369 us, 1,433 TFLOP/s
+//   64 x 1-512 after 200-8,000, 16 / 2 heads of 256          1,345 us,   854 TFLOP/s
+//   4 x 1,500-2,500 after 0-3,000, 8 / 8 heads of 64            79 us,   520 TFLOP/s
+//   32 x 1-16 after 1,000-16,000, 16 / 2 heads of 128           69 us, 4.2 TB/s
+// What bounds prompts now is the chain below and the items' starts and ends (tensor pipe
+// busy 49% of 2 prompts of 4,096); heads of 256 wait for K and V from L2.
 //
 // An item has NQ row tiles. What counts is that the unit always has a product to make: a
 // tile's chain (S, its way to the registers, the weights, their way back, P V) is some
@@ -26,7 +33,7 @@
 // 32 tokens; others, whose tokens may begin anywhere in a tile's swizzle, by 16-byte
 // asynchronous copies, after which the products need a proxy fence.
 //
-// P goes back to tensor memory in the place of its S, as the A operand of P V, rounded to
+// P goes back to tensor memory, as the A operand of P V, rounded to
 // bf16: one more rounding of 2^-9 rms beside the output's own; the sums are of the
 // unrounded weights.
 //
@@ -249,7 +256,6 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
   __shared__ WalkShared s_walk;
   __shared__ uint32_t s_tmem;
   __shared__ int s_dead;
-  asm volatile("griddepcontrol.launch_dependents;");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const lin_kv_cache_t& c = p.c;

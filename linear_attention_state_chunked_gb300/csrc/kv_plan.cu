@@ -4,7 +4,8 @@
 //   table[r][ceil(len / P) + i] = free[before[r] + i],  cu = the running sum of n,
 //   position = len + j (or + depth),  slot = table[r][(len + j) / P] P + (len + j) % P
 //
-// Bound by latency: a launch, the lengths, a block scan, the first page ids. One
+// Bound by latency: a launch, the lengths, a block scan, the first page ids (256 requests
+// of one token 5.7 us, 64 chunks of up to 2,048 tokens 5.6 us). One
 // launch: every CTA scans the whole batch by itself (a kernel in front would cost more
 // than the repeated loads, which come from L2) and then serves kPlanTokens packed
 // rows. The scan leaves a mark at the row where a request begins, and a row's request

@@ -41,6 +41,7 @@ int lin_state_kv_plan(const lin_kv_plan_args_t* a, void* stream) {
   if (!a) return fail(LIN_EINVAL, "plan args is NULL");
   if (a->batch < 0 || a->tokens < 0 || a->max_pages < 0 || a->num_free < 0)
     return fail(LIN_EINVAL, "plan: negative batch / tokens / max_pages / num_free");
+  if (a->batch > 1 << 30) return fail(LIN_EUNSUPPORTED, "plan: batch above 2^30");
   if (a->page_size < 1 || a->num_pages < 1) return fail(LIN_EINVAL, "plan: page_size and num_pages must be positive");
   if (!a->n_new && a->n < 0) return fail(LIN_EINVAL, "plan: negative n");
   if (a->parent && a->n_new) return fail(LIN_EINVAL, "plan: n_new and a draft tree exclude each other");

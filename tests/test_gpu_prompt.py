@@ -440,6 +440,32 @@ def test_chunk_batches_of_many_items(D, Hq, Hkv, ps):
     assert torch.equal(a, check_chunk(*x, BF))
 
 
+def test_chunk_requests_over_the_same_rows_end():
+    """Requests whose packed rows overlap have more items than a batch of that many rows:
+    it is told, and the counter that hands items out stops at what a batch can have. (Both
+    requests are alike, so it does not matter whose rows are written last.)"""
+    T = 9760  # 305 items of 32 tokens to a head: more than four to a CTA
+    cache, table, q, _, _ = chunk_inputs([50], [T], 64, 16, 2, 64, BF, seed=12)
+    one, many = (torch.zeros(q.shape, dtype=BF, device="cuda") for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L.lin_state_attn_chunk(cache, layer=0, q=q, out=one, page_table=table.cuda(), cu_seqlens=i32([0, T]),
+                           kv_len=i32([50 + T]), status=status)
+    assert L.lin_state_read_status(status) == 0
+    L.lin_state_attn_chunk(cache, layer=0, q=q, out=many, page_table=table.cuda().repeat(3, 1),
+                           cu_seqlens=i32([0, T, 0, T]), kv_len=i32([50 + T] * 3), status=status)
+    assert L.lin_state_read_status(status) == L.LIN_ST_BAD_SEQLEN
+    assert torch.equal(one, many)
+
+
+@pytest.mark.parametrize("rot", [2, 30, 62, 100, 126])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rope_parts_that_end_inside_a_chunk(rot, interleaved, dtype):
+    """Partners in other chunks of the row, more rows than a block takes at a time, in place."""
+    check_rope(700, 7, 3, 128, rot, dtype, interleaved, 100000, rot)
+    check_rope(9, 7, 3, 128, rot, dtype, interleaved, 100000, rot, in_place=True)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("ps", [5, 20, 40])
 @pytest.mark.parametrize("hnd", [False, True])

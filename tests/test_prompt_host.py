@@ -60,6 +60,10 @@ def test_plan_refusals(change, code, text):
     refused(L.lib.lin_state_kv_plan(ctypes.byref(plan_args(**change)), None), code, text)
 
 
+def test_plan_batches_past_its_arithmetic_are_refused():
+    refused(L.lib.lin_state_kv_plan(ctypes.byref(plan_args(batch=(1 << 30) + 1)), None), L.LIN_EUNSUPPORTED, "batch")
+
+
 @pytest.mark.parametrize("change,code,text", [
     (dict(tokens=-1), L.LIN_EINVAL, "negative"),
     (dict(dtype=5), L.LIN_EINVAL, "dtype"),
