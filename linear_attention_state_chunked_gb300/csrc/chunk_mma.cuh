@@ -14,8 +14,8 @@
 // (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
 // so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
 // Bound by the ALUs that split operands (each warp splits every key and value that it
-// takes) beside the tensor pipe: 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, 104 us,
-// 39 TFLOP/s.
+// takes) beside the tensor pipe: 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, 101 us,
+// 40 TFLOP/s.
 #pragma once
 
 #include "attn_kernel.cuh"
@@ -187,20 +187,21 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
             ldsm4(q, qs + chunk_at<ROWB>(warp * 16 + (lane & 15), 2 * d + (lane >> 4)));
 #pragma unroll
             for (int k = 0; k < 4; ++k) split_tf32(__uint_as_float(q[k]), hi[k], lo[k]);
+            // a sum's three products wait for one another: those of all keys in turn
+            uint32_t bh[NB][2], bl[NB][2];
 #pragma unroll
             for (int n = 0; n < NB; n += 2) {
               uint32_t b[4];
               ldsm4(b, ks + chunk_at<ROWB>(n * 8 + (lane & 7) + (lane >> 4) * 8, 2 * d + ((lane >> 3) & 1)));
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                uint32_t h0, l0, h1, l1;
-                split_tf32(__uint_as_float(b[2 * k]), h0, l0);
-                split_tf32(__uint_as_float(b[2 * k + 1]), h1, l1);
-                mma_tf32(part[n + k], lo, h0, h1);
-                mma_tf32(part[n + k], hi, l0, l1);
-                mma_tf32(part[n + k], hi, h0, h1);
-              }
+              for (int k = 0; k < 4; ++k) split_tf32(__uint_as_float(b[k]), bh[n + k / 2][k & 1], bl[n + k / 2][k & 1]);
             }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_tf32(part[n], lo, bh[n][0], bh[n][1]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_tf32(part[n], hi, bl[n][0], bl[n][1]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) mma_tf32(part[n], hi, bh[n][0], bh[n][1]);
           }
 #pragma unroll
           for (int n = 0; n < NB; ++n)
@@ -326,22 +327,33 @@ __global__ void __launch_bounds__(C::NT, C::CTAS) chunk_mma_kernel(const Plan p)
             split_weight(s[n + y][3], hi[y][3], lo[y][3]);
           }
 #pragma unroll
-          for (int d = 0; d < D / 8; ++d) {
-            float u[4] = {0, 0, 0, 0};
+          for (int d = 0; d < D / 8; d += 4) {
+            float u[4][4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[z][k] = 0.0f;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              const int t = (n + y) * 8 + 2 * t4, ch = d * 2 + (g >> 2);
-              const float v0 = lds32(vs + chunk_at<ROWB>(t, ch) + (g & 3) * 4);
-              const float v1 = lds32(vs + chunk_at<ROWB>(t + 1, ch) + (g & 3) * 4);
-              uint32_t h0, l0, h1, l1;
-              split_tf32(v0, h0, l0);
-              split_tf32(v1, h1, l1);
-              mma_tf32(u, lo[y], h0, h1);
-              mma_tf32(u, hi[y], l0, l1);
-              mma_tf32(u, hi[y], h0, h1);
+              uint32_t bh[4][2], bl[4][2];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t at = vs + chunk_at<ROWB>((n + y) * 8 + 2 * t4 + k, (d + z) * 2 + (g >> 2)) + (g & 3) * 4;
+                  split_tf32(lds32(at), bh[z][k], bl[z][k]);
+                }
+#pragma unroll
+              for (int z = 0; z < 4; ++z) mma_tf32(u[z], lo[y], bh[z][0], bh[z][1]);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) mma_tf32(u[z], hi[y], bl[z][0], bl[z][1]);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) mma_tf32(u[z], hi[y], bh[z][0], bh[z][1]);
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[d][k] += u[k];
+            for (int z = 0; z < 4; ++z)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[d + z][k] += u[z][k];
           }
         }
       }
