@@ -7,15 +7,17 @@
 // and keeps their softmax state and value sums in registers. Four warps have an item's 64
 // rows; for heads of 256, whose rows leave room for one block on an SM, there are two such
 // groups, which take every other tile and are joined at a piece's end (fp32, 1,000 tokens
-// after 1,000, 16 / 4 heads: of 256 811 us with one group, 618 with two; of 128, where two
-// blocks fit, 310 and 335). K and V
+// after 1,000, 16 / 4 heads: of 256 811 us with one group, 615 with two, and 600 now; of 128,
+// where two blocks fit, 310 and 335, and 289 now). K and V
 // tiles come by 16-byte asynchronous copies (pages may end anywhere), two tiles ahead,
 // swizzled so that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
 // (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
 // so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
-// Bound by the ALUs that split operands (each warp splits every key and value that it
-// takes) beside the tensor pipe: 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, 101 us,
-// 40 TFLOP/s.
+// 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, fp32: 101 us, 40 TFLOP/s. Registers
+// leave two or three warps to a scheduler, and no unit is full (heads of 128: tensor pipe
+// 45%, ALU 44%, issue 53%): what bounds it is how little of a warp's splits, products and
+// softmax goes on beside another's. Splitting a tile once for the block in shared memory,
+// instead of in each warp, took as long (101 us, heads of 128 289 to 302).
 #pragma once
 
 #include "attn_kernel.cuh"
