@@ -130,20 +130,35 @@ struct Shape {
   int rows, tk, ctas, item_cost;
 };
 
-Shape shape_of(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, int out_dtype) {
-  if (c.dtype == LIN_BF16 && out_dtype == LIN_BF16) {
-    const int64_t rows = int64_t(a.tokens) * (a.num_q_heads / c.num_kv_heads);  // of a kv head
-    const bool two = c.head_dim <= 128 && rows > 128 * int64_t(a.batch);
-    return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 384};
-  }
-  const int row_bytes = c.head_dim * dtype_size(c.dtype);
-  return {false, 64, row_bytes >= 512 ? 16 : 32, c.head_dim == 256 ? 1 : c.head_dim == 128 ? 2 : 3, c.head_dim == 256 ? 128 : 64};
-}
-
 int sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) == cudaSuccess) sms = device_sm_count(dev);
   return sms > 0 ? sms : 152;  // no device: the size of a GB300
+}
+
+// Whether an item has two row tiles of 128 (heads of 64 and 128): where a request has more
+// rows than one tile, and the call more work than `kTwoFrom` tiles of 128 x 128 for each SM,
+// by what the host knows of it. Two read a tile of K and V for twice the rows and share the
+// unit better, one makes more and shorter items. Heads of 128, one against two: 64 tokens
+// after 1,000 18.3 and 21.7 us, 256 after 8,000 33.9 and 40.9, 512 after 8,000 46.8 and
+// 45.1, 32 x 64 after 4,000 89 and 76, 32 after 400,000 105 and 96.
+constexpr int kTwoFrom = 20;
+
+bool two_tiles(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a) {
+  const int64_t rows = int64_t(a.tokens) * (a.num_q_heads / c.num_kv_heads);  // of a kv head
+  const double keys = double(a.max_pages) * c.page_size;
+  return rows > 128 * int64_t(a.batch) && double(rows) * c.num_kv_heads * keys > double(kTwoFrom) * 128 * 128 * sm_count();
+}
+
+// item_cost: what an item's start and end take, in keys (tensor-memory kernel, 2 prompts of
+// 4,096 tokens: as 96 keys 183 us, as 192 156, as 320 140, as 384 137).
+Shape shape_of(const lin_kv_cache_t& c, int out_dtype, bool two) {
+  if (c.dtype == LIN_BF16 && out_dtype == LIN_BF16) {
+    two = two && c.head_dim <= 128;
+    return {true, two ? 256 : 128, !two ? 128 : c.head_dim == 64 ? 96 : 80, 1, 384};
+  }
+  const int row_bytes = c.head_dim * dtype_size(c.dtype);
+  return {false, 64, row_bytes >= 512 ? 16 : 32, c.head_dim == 256 ? 1 : c.head_dim == 128 ? 2 : 3, c.head_dim == 256 ? 128 : 64};
 }
 
 size_t bytes_of(const lin_kv_cache_t& c, const Shape& f) {
@@ -215,25 +230,22 @@ cudaError_t launch_join(const Plan& p, int64_t items, int rows, cudaStream_t s) 
 }  // namespace chunk
 
 size_t chunk_need(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a) {
-  return chunk::bytes_of(c, chunk::shape_of(c, a, a.out_dtype));
+  return chunk::bytes_of(c, chunk::shape_of(c, a.out_dtype, chunk::two_tiles(c, a)));
 }
 
-size_t chunk_workspace(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a) {
+size_t chunk_workspace(const lin_kv_cache_t& c, const lin_attn_chunk_args_t&) {
   // of every kernel that a call over this cache may take
   size_t most = 0;
-  lin_attn_chunk_args_t x = a;
-  x.batch = 1;
   for (const int out : {LIN_BF16, LIN_F32})
-    for (const int tokens : {1, 129}) {
-      x.tokens = tokens;
-      const size_t n = chunk::bytes_of(c, chunk::shape_of(c, x, out));
+    for (const bool two : {false, true}) {
+      const size_t n = chunk::bytes_of(c, chunk::shape_of(c, out, two));
       if (n > most) most = n;
     }
   return most;
 }
 
 cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args_t& a, void* ws, cudaStream_t s) {
-  const chunk::Shape f = chunk::shape_of(c, a, a.out_dtype);
+  const chunk::Shape f = chunk::shape_of(c, a.out_dtype, chunk::two_tiles(c, a));
   chunk::Plan p;
   p.c = c;
   p.a = a;
@@ -259,7 +271,8 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
   w += size_t(p.grid) * sizeof(chunk::Split);
-  // Items of the batch at most. Many for a CTA: one by one from a counter.
+  // Items of the batch at most. Many for a CTA: one by one from a counter (8 prompts of 4,096
+  // tokens 504 us by ranges, 447 so; from two items a CTA on, heads of 64, 80 and 103).
   const int64_t items = p.items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
   p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid && items < (1 << 30) ? reinterpret_cast<int*>(w) : nullptr;
   if (p.ticket) {
@@ -285,7 +298,8 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   }
   if (e != cudaSuccess || p.ticket) return e;
   // Few items have many parts each (one request's last tokens over a long cache), which
-  // the warps of a block then share.
+  // the warps of a block then share (8 tokens after 100,000: 39 us, rows alone 65; 32 x 32
+  // after 4,000, the other way: 52, and 84 with shared parts).
   const int64_t most = int64_t(a.tokens) * p.bheads;
   const int rows = most < p.rows ? static_cast<int>(most) : p.rows;
   return c.head_dim == 64    ? chunk::launch_join<64>(p, items, rows, s)

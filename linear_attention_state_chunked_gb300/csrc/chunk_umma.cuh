@@ -18,7 +18,8 @@
 // 4,000 cycles long for 128 keys of heads of 128, of which the unit works 1,100. So the
 // next S is made while the softmax works on the last, which takes room in tensor memory
 // for a second S or for P beside S.
-//   NQ = 1 (heads of 256, whose O alone takes half of tensor memory, and few rows): two
+//   NQ = 1 (heads of 256, whose O alone takes half of tensor memory, few rows, and calls with
+//   little work): two
 //   buffers of S with TK = 128, P in its S's place. A warp issues S, another P V.
 //   NQ = 2 (heads of 64 and 128): one S each, which is free once it is in registers, and P
 //   beside it: TK = 96 and 80, as S, P and O of both fit. (With TK = 128 and P in S's
@@ -291,7 +292,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
 
   // A warp whose wait runs out waits for nothing more and goes to the end, and so do the
   // others in their turn. Called by whole warps, and the same for all lanes. (A look at a
-  // barrier takes 70 cycles, a wait that may sleep 200 even where the phase is over.)
+  // barrier takes 45 cycles, a wait that may sleep 200 even where the phase is over.)
   bool gone = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (gone || __all_sync(~0u, mbar_test(bar, parity))) return;

@@ -240,10 +240,21 @@ def test_rope_single_outputs():
 # ---- attention of packed new tokens ---------------------------------------------------------
 
 def check_chunk(cache, table, q, cu, lens, out_dtype, scale=None, layer=0, status_want=0, **kw):
+    """Looks over the call's outputs, and again with room for so many pages that requests of
+    many rows go in items of two row tiles, which calls with little work do not."""
+    if status_want != L.LIN_ST_BAD_SEQLEN:
+        wide = -(-(1 << 26) // (q.shape[0] * q.shape[1] * cache.page_size)) + table.shape[1]
+        more = torch.full((table.shape[0], wide), 1 << 30, dtype=torch.int32)  # (never looked up)
+        more[:, :table.shape[1]] = table
+        look_chunk(cache, more, q, cu, lens, out_dtype, scale, layer, status_want, table, **kw)
+    return look_chunk(cache, table, q, cu, lens, out_dtype, scale, layer, status_want, table, **kw)
+
+
+def look_chunk(cache, given, q, cu, lens, out_dtype, scale, layer, status_want, table, **kw):
     T, Hq, D = q.shape
     out = torch.full((T, Hq, D), 7.0, dtype=out_dtype, device="cuda")
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    L.lin_state_attn_chunk(cache, layer=layer, q=q, out=out, page_table=table.cuda(), cu_seqlens=i32(cu),
+    L.lin_state_attn_chunk(cache, layer=layer, q=q, out=out, page_table=given.cuda(), cu_seqlens=i32(cu),
                            kv_len=i32(lens), scale=scale, status=status, **kw)
     assert L.lin_state_read_status(status) == status_want
     s = D ** -0.5 if scale is None else scale
@@ -438,6 +449,37 @@ def test_chunk_batches_of_many_items(D, Hq, Hkv, ps):
     x = chunk_inputs(cached, new, ps, Hq, Hkv, D, BF, seed=D, spare=max(0, rows - sum(new)))
     a = check_chunk(*x, BF)
     assert torch.equal(a, check_chunk(*x, BF))
+
+
+def test_a_captured_batch_of_many_items_follows_its_lengths():
+    """Items handed out by the counter, which each replay begins anew; the same call eagerly,
+    then on another stream with a workspace of its own, gives the same bits."""
+    T, B, ps, H, D = 9760, 5, 16, 2, 64
+    cache, table, gen = make_cache([4000] * B, ps, H, D, BF, 3)
+    q = torch.randn((T, 8 * H, D), generator=gen).to(BF).cuda()
+    table = table.cuda()
+    cu, lens = torch.zeros(B + 1, dtype=torch.int32, device="cuda"), torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(q.shape, dtype=BF, device="cuda")
+    size = L.lin_state_attn_chunk_workspace(cache, batch=B, tokens=T, num_q_heads=8 * H, max_pages=table.shape[1])
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    args = dict(layer=0, q=q, page_table=table, cu_seqlens=cu, kv_len=lens)
+    L.lin_state_attn_chunk(cache, out=out, workspace=work, **args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        L.lin_state_attn_chunk(cache, out=out, workspace=work, **args)
+    for new, cached in (([3000, 1, 0, 777, 2500], [1000, 0, 5, 3000, 64]), ([1, 2, 3, 4, 5], [9, 9, 9, 9, 9]),
+                        ([4000, 4000, 1000, 700, 60], [0, 0, 0, 0, 3940])):
+        cu.copy_(i32(np.concatenate([[0], np.cumsum(new)])))
+        lens.copy_(i32([a + b for a, b in zip(new, cached)]))
+        out.zero_()
+        graph.replay()
+        again, side = torch.zeros_like(out), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        L.lin_state_attn_chunk(cache, out=again, stream=side, **args)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(out, again) and not out[sum(new):].any() and out[:sum(new)].any()
 
 
 def test_chunk_requests_over_the_same_rows_end():
