@@ -40,7 +40,7 @@
 //
 // The reference m. A piece's first tile takes its rows' maxima. After that the weights
 // are made at once with the reference at hand, and only where a tile's sum of a row passes
-// 2^8 (or is no number) are the maxima looked up, the row's sums rescaled and the weights
+// 2^8 are the maxima looked up, the row's sums rescaled and the weights
 // made again: a tile in some thousand, which saves the others the pass over the scores.
 //
 // Hidden values: 0 NaN is NaN, so in tiles that some row of the item does not see whole
@@ -406,8 +406,12 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         }
         uint32_t pk[TK / 2];
         float sum = 0.0f;
+        // Looked up beforehand while some row of the warp has no reference (which moves no
+        // other row's: sum is not made yet), and after the weights where a sum says so. A NaN
+        // in a row's sum is there to stay, and wants no look.
+        bool told = false;  // the look-up has seen the sums
 #pragma unroll 1
-        for (bool look_up = unset;; look_up = true) {
+        for (bool look_up = unset;; look_up = told = true) {
           if (look_up) {  // the reference, and what follows from its move
             float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -419,7 +423,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]);
             float f = 1.0f;
             // (a row goes by its own scores alone, whatever made its warp look)
-            if (mx > cut && (cut == -INFINITY || !(sum <= kMostSum))) {
+            if (mx > cut && (cut == -INFINITY || sum > kMostSum)) {
               const float y0 = -mx * p.scale_log2;
               f = cut == -INFINITY ? 0.0f : attn::exp2_fast(y0 - z);
               z = y0, cut = mx, l *= f;
@@ -437,7 +441,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
               }
             }
             // a row that has seen nothing yet, and will see something
-            unset = __any_sync(~0u, cut == -INFINITY && sees > key0 + TK);
+            unset = __any_sync(~0u, cut == -INFINITY && l == l && sees > key0 + TK);
           }
           const uint64_t z2 = f2pack(z, z);
           uint64_t add[2] = {0, 0};
@@ -450,7 +454,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
             pk[k] = pack_bf16(e0, e1);
           }
           sum = mine ? f2sum(fadd2(add[0], add[1])) : 0.0f;
-          if (look_up || !__any_sync(~0u, !(sum <= kMostSum))) break;
+          if (told || !__any_sync(~0u, sum > kMostSum)) break;
         }
         l += sum;
         if (tile >= y.check0) {
