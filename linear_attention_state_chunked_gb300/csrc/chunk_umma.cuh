@@ -459,6 +459,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
         l += sum;
         if (tile >= y.check0) {
           wait(&b_check[chk & (kCheckRing - 1)], (chk / kCheckRing) & 1);
+          if (gone) break;  // s_wild may hold anything
           const uint4 wv = s_wild[chk & (kCheckRing - 1)];
           ++chk;
           if (wv.x | wv.y | wv.z | wv.w) {
@@ -480,9 +481,9 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
                 for (; left; left &= left - 1) {
                   const int t = key0 + 32 * g + __ffs(left) - 1;
                   if (t >= sees) break;
-                  const int pg = page_of(p, t);
-                  const char* v = vb + a.page_table[x.r * a.page_table_stride + pg] * c.page_stride +
-                                  (t - pg * c.page_size) * c.token_stride + d * 2;
+                  const int pg = page_of(p, t), id = a.page_table[x.r * a.page_table_stride + pg];
+                  if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(c.num_pages)) continue;  // (its values were 0)
+                  const char* v = vb + id * c.page_stride + (t - pg * c.page_size) * c.token_stride + d * 2;
 #pragma unroll
                   for (int k = 0; k < 8; ++k) {
                     const float e = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(v)[k]);

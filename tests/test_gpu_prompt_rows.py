@@ -71,3 +71,34 @@ def test_a_query_that_is_no_number_leaves_its_neighbours_alone(dtype, D, B, n, c
             assert torch.equal(out[other], plain[other]), (token, head)
             if what != what:
                 assert torch.isnan(out[token::n, head]).all()
+
+
+@pytest.mark.parametrize("two", [False, True])
+@pytest.mark.parametrize("D,ps", [(64, 16), (64, 7), (128, 16), (128, 9), (256, 16), (256, 5)])
+def test_values_that_are_no_number_beside_pages_that_are_none(D, ps, two):
+    """Tiles that are looked over, with infinities and NaN on some pages and others that are
+    not to be read: rows before the values keep their bits, rows that see them do not pass
+    for finite, and what lies on no page counts for nothing."""
+    cache, table, q, cu, lens = chunk_inputs([40, 0], [150, 290], ps, 4, 2, D, BF, seed=D + ps)
+    bad = [-1, cache.num_pages, 1 << 30, -(1 << 31)]
+    for r in (0, 1):
+        for k, page in enumerate(range(50 // ps, lens[r] // ps, 60 // ps)):
+            table[r, page] = bad[k % 4]
+    wide = room(q, table, ps, two)
+    plain, status = attend(cache, wide, q, cu, lens, BF)
+    assert status == L.LIN_ST_BAD_PAGE and torch.isfinite(plain).all()
+    check_chunk(cache, table, q, cu, lens, BF, status_want=L.LIN_ST_BAD_PAGE)
+    # one visible from token 100 (or the next that has a page) on, and one later
+    first = []
+    for r in (0, 1):
+        for at in (100, lens[r] - 20):
+            t = next(t for t in range(at, lens[r]) if 0 <= table[r, t // ps] < cache.num_pages)
+            cache.v[0, table[r, t // ps], t % ps] = float("nan") if at == 100 else float("inf")
+            if at == 100:
+                first.append(t)
+    wild, status = attend(cache, wide, q, cu, lens, BF)
+    assert status == L.LIN_ST_BAD_PAGE
+    for r, cached in ((0, 40), (1, 0)):
+        row = int(cu[r]) + first[r] - cached  # whose query is the first to see it
+        assert torch.equal(wild[cu[r]:row], plain[cu[r]:row])
+        assert not torch.isfinite(wild[row:cu[r + 1]]).any()
