@@ -136,9 +136,11 @@ LIN_API int lin_state_rope(const lin_kv_cache_t* cache, const lin_rope_args_t* a
  * infinities. Results do not depend on timing: the same call gives the same bits. Nor does
  * a row depend on what other rows see.
  * Lengths are read on the device. The batch's work is cut into equal ranges for the SMs,
- * and blocks of queries that cross a border are joined by a second launch; where `tokens`
- * allows many blocks for each SM (bf16 outputs), they are taken one by one from a counter
- * in the workspace, which a memset zeroes.
+ * and blocks of queries that cross a border are joined by a second launch. Where `tokens`
+ * allows many blocks for each SM (bf16 outputs), a launch in front looks whether the lengths
+ * do: if so, whole blocks are taken one by one from a counter in the workspace. Which way,
+ * and the rows of a block, go by batch, tokens, num_q_heads, max_pages and the lengths: the
+ * same tokens in a call with other room may differ in their last bits.
  * Pages of a multiple of 8 tokens load faster (by TMA) than others, and so do queries
  * whose heads per kv head divide 128.
  * out must not overlap anything that is read.

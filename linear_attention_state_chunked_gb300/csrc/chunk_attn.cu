@@ -12,7 +12,46 @@ namespace {
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 32;      // rows of a block: a lane each
 constexpr int kManyParts = 8;      // of an item: see launch_attn_chunk
-constexpr int kManyItems = 4;      // of a CTA: the same
+constexpr int kShareThreads = 512;
+
+// Whether the batch's items are taken one by one: where the last one ends in time
+// (chunk_common.cuh). Of a request's last head that is the item from which on the items get
+// shorter by more (m) than passes until their turn (their units / CTAs). One block.
+__global__ void __launch_bounds__(kShareThreads) share_kernel(const Plan p) {
+  __shared__ int64_t s_sum[kShareThreads / 32], s_late[kShareThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, batch = p.a.batch;
+  const int span = (batch + kShareThreads - 1) / kShareThreads;
+  const int r0 = min(batch, tid * span), r1 = min(batch, r0 + span);
+  // units of this thread's requests, and the last end with none before them, in units x CTAs
+  int64_t mine = 0, late = 0;
+#pragma unroll 1
+  for (int r = r0; r < r1; ++r) {
+    const Req q = request(p, r, false);
+    if (q.items == 0) continue;
+    const int64_t turn = int64_t(p.grid) - 1 - q.base / p.m;
+    const int j = static_cast<int>(max(int64_t(0), min(int64_t(q.items) - 1, turn)));
+    mine += units_before(p, q, q.items) * p.heads;
+    late = max(late, mine - units_before(p, q, j + 1) + (keys_of(p, q, j) + p.item_cost) * p.grid);
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(~0u, upto, o);
+    if (lane >= o) upto += x;
+  }
+  late += upto - mine;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) late = max(late, __shfl_xor_sync(~0u, late, o));
+  if (lane == 31) s_sum[warp] = upto, s_late[warp] = late;
+  __syncthreads();
+  if (tid == 0) {
+    int64_t total = 0, last = 0;
+#pragma unroll
+    for (int x = 0; x < kShareThreads / 32; ++x) last = max(last, total + s_late[x]), total += s_sum[x];
+    p.ticket[0] = 0;
+    p.ticket[1] = last <= total + total / kManyItems;
+  }
+}
 
 // The x-th of the ranges whose last item goes on past them, by a whole warp; false
 // where there are fewer.
@@ -45,6 +84,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const Plan p) {
   __shared__ float s_sum[kJoinRows];
   __shared__ float4 s_part[WP > 1 ? WP : 1][CG][kJoinRows];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wp = warp % WP, wc = warp / WP;
+  if (one_by_one(p)) return;
   Split s;
   int c;
   if (!find_split(p, blockIdx.x, c, s)) return;
@@ -271,12 +311,13 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
   w += size_t(2) * p.grid * p.rows * sizeof(float2);
   p.split = reinterpret_cast<chunk::Split*>(w);
   w += size_t(p.grid) * sizeof(chunk::Split);
-  // Items of the batch at most. Many for a CTA: one by one from a counter (8 prompts of 4,096
-  // tokens 504 us by ranges, 447 so; from two items a CTA on, heads of 64, 80 and 103).
+  // Items of the batch at most. Where it could have many for a CTA, a first launch tells by
+  // the lengths whether they are taken one by one.
   const int64_t items = p.items = int64_t(p.heads) * (a.tokens / p.m + a.batch);
   p.ticket = f.umma && items >= int64_t(chunk::kManyItems) * p.grid && items < (1 << 30) ? reinterpret_cast<int*>(w) : nullptr;
   if (p.ticket) {
-    const cudaError_t e = cudaMemsetAsync(p.ticket, 0, sizeof(int), s);
+    chunk::share_kernel<<<1, chunk::kShareThreads, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   p.box = p.q_box = 0;
@@ -296,7 +337,7 @@ cudaError_t launch_attn_chunk(const lin_kv_cache_t& c, const lin_attn_chunk_args
         : c.head_dim == 128 ? chunk::launch_mma_d128(p, s)
                             : chunk::launch_mma_d256(p, s);
   }
-  if (e != cudaSuccess || p.ticket) return e;
+  if (e != cudaSuccess) return e;
   // Few items have many parts each (one request's last tokens over a long cache), which
   // the warps of a block then share (8 tokens after 100,000: 39 us, rows alone 65; 32 x 32
   // after 4,000, the other way: 52, and 84 with shared parts).

@@ -13,12 +13,13 @@
 // results do not depend on timing. A request's items have a closed sum (keys grow by m
 // from one to the next), so no kernel has to lay the items out.
 //
-// Batches of many items per CTA (the tensor-memory kernel) are not cut: a CTA takes the
-// next item from a counter whenever it begins one. So the items under way at a time are
-// neighbours, which share their keys and values in L2 (64 chunks of up to 512 tokens after
-// up to 8,000, heads of 256, whose cache is four times the L2: 1,707 us by ranges); a
-// request's items come longest first, so that the last ones are short. Whole items, so
-// again the result does not depend on who took them.
+// Batches of many items per CTA (the tensor-memory kernel) are not cut, where the lengths,
+// which a call's room says nothing of, allow that: a CTA takes the next item from a counter
+// whenever it begins one. So the items under way at a time are neighbours, which share their
+// keys and values in L2. A request's items come longest first. An item whose turn comes
+// after u units begins when u / CTAs of them are done at the latest, so the last end can be
+// told before: the counter is used where it lies within 1 / kManyItems of an equal share.
+// Whole items, so again the result does not depend on who took them.
 #pragma once
 
 #include <cuda.h>
@@ -31,6 +32,15 @@ namespace lin {
 namespace chunk {
 
 constexpr int64_t kLongest = attn::kLongest;
+
+// By the counter and by ranges, us (and the last end by the counter in equal shares): 64 x
+// 1-512 tokens after 200-8,000, 16 / 2 heads of 256 (1.1) 1,350 and 1,515, 32 / 8 of 128 904
+// and 967, 8,192 after 120,000 (1.1) 11,454 and 13,421; 8 prompts of 4,096, 16 / 2 of 128,
+// 446 and 445, with one token after 24,000 before them (1.1) 451 and 458, after 12,000 behind
+// them (1.4) 536 and 454, after 128,000 1,805 and 473; 256 single tokens after 1,000, the
+// last after 4,000 (1.2) 225 and 202, after 16,000 (1.9) 346 and 213; 64 tokens after 129,000
+// in a call with room for 32,768 1,569 and 83.
+constexpr int kManyItems = 4;
 
 struct Split {       // the item that begins in range c and goes on past it
   int parts;         // 0: there is none
@@ -58,7 +68,7 @@ struct Plan {
   float* part;       // [2 grid][D / 4][rows][4] value sums of unfinished pieces: a warp's rows side by side
   float2* part_ml;   // [2 grid][rows] their (maximum, sum)
   Split* split;      // [grid]
-  int* ticket;       // items handed out so far, where they are taken one by one; else NULL
+  int* ticket;       // [0] items handed out so far, [1] whether they are: share_kernel's; NULL: they are not
   int64_t items;     // of the batch at most
 };
 
@@ -83,6 +93,9 @@ struct Req {
   int cu, n, base;   // first packed row, rows, position of the first
   int items, few;    // per head; the first `few` see one key at most and count as one
 };
+
+// Whether the batch's items are taken one by one.
+__device__ __forceinline__ bool one_by_one(const Plan& p) { return p.ticket && p.ticket[1]; }
 
 __device__ __forceinline__ int64_t longest(const Plan& p) { return min(int64_t(p.a.max_pages) * p.c.page_size, kLongest); }
 

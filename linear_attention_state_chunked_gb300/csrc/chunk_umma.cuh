@@ -273,14 +273,15 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     s_dead = 0;
   }
   Walk w;
-  if (!p.ticket) {
+  const bool tickets_on = one_by_one(p);
+  if (!tickets_on) {
     if (!walk_begin<NT>(p, w, s_walk)) return;
   } else if (blockIdx.x == 0) {
 #pragma unroll 1
     for (int r = tid; r < a.batch; r += NT) request(p, r, true);
   }
   // pieces handed out ahead: the next alone where another CTA could take it
-  const int pieces = p.ticket ? 1 : kPieces;
+  const int pieces = tickets_on ? 1 : kPieces;
   if (warp == SOFT + 2) umma::tmem_alloc(&s_tmem, C::TMEM);
   umma::fence_before_sync();
   __syncthreads();
@@ -832,12 +833,12 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
       UPiece y;
       Tickets tickets;
       int g = 0;
-      if (p.ticket) tickets.begin(p);
+      if (pieces == 1) tickets.begin(p);
 #pragma unroll 1
       do {
         wait(&b_pempty[at_piece], piece_phase ^ 1);
         if (gone) break;
-        if (p.ticket)
+        if (pieces == 1)
           y.x = tickets.next(p);
         else if (lane == 0)
           y.x = walk_next(p, w);
@@ -961,7 +962,7 @@ chunk_umma_kernel(const Plan p, const __grid_constant__ CUtensorMap k_map, const
     // a wait ran out: what this range leaves unwritten counts as left out
     for (int x = tid; x < 2 * p.rows; x += NT) p.part_ml[2 * int64_t(blockIdx.x) * p.rows + x] = make_float2(-INFINITY, attn::kLeftOut);
     if (tid == 0) {
-      if (!p.ticket) p.split[blockIdx.x].parts = 0;
+      p.split[blockIdx.x].parts = 0;
       report(a.status, LIN_ST_TIMEOUT);
     }
   }
