@@ -115,8 +115,12 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, linear: Optional[fl
     linear: positions divided by the factor. ntk: the base grown so that the slowest
     pair's wave is that much longer and the fastest stays. yarn (Peng et al. 2023, "YaRN"):
     pairs that turn more than beta_fast times in `trained` tokens stay, those that turn
-    less than beta_slow times are divided by the factor, a ramp between; and cosines and
-    sines are scaled by 0.1 ln(factor) + 1."""
+    less than beta_slow times are divided by the factor, between them the share that stays
+    grows linearly with the turns, as the paper has it; and cosines and sines are scaled by
+    0.1 ln(factor) + 1. Checkpoints trained with a ramp that is linear in the pair's index
+    instead (common, and log-linear in the turns: a pair of 5.7 turns keeps 0.50 of its
+    frequency there, 0.15 here), or with another scale, need their own inv_freq and scale,
+    which lin_state_rope takes as well."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim: want an even number of channels, got {rot_dim}")
     given = [x for x in (linear, ntk, yarn) if x is not None]
