@@ -141,8 +141,9 @@ LIN_API int lin_state_rope(const lin_kv_cache_t* cache, const lin_rope_args_t* a
  * do: if so, whole blocks are taken one by one from a counter in the workspace. Which way,
  * and the rows of a block, go by batch, tokens, num_q_heads, max_pages and the lengths: the
  * same tokens in a call with other room may differ in their last bits.
- * Pages of a multiple of 8 tokens load faster (by TMA) than others, and so do queries
- * whose heads per kv head divide 128.
+ * bf16 outputs: pages of a multiple of 8 tokens load faster (by TMA) than others, and so do
+ * queries whose heads per kv head divide 128 (with 7 of them a prompt takes 1.2 times as
+ * long for its work as with 8). fp32 outputs of a bf16 cache take 2 to 6 times as long.
  * out must not overlap anything that is read.
  * Workspace: lin_state_attn_chunk_workspace() bytes of device memory, 16-byte aligned,
  * not shared by calls that may overlap. The size never shrinks as batch, tokens,

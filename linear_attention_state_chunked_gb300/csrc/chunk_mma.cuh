@@ -13,7 +13,10 @@
 // swizzled so that no fragment load conflicts. fp32 operands go as two tf32 parts, three products
 // (attn_kernel.cuh); the tensor unit cuts off below the last place of what it adds to,
 // so the products of 32 channels of a score, and of 16 tokens, are added with rounding.
-// 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, fp32: 101 us, 40 TFLOP/s. Registers
+// 8 x 1-300 tokens after 0-2,000, 12 / 4 heads of 64, fp32: 101 us, 39 TFLOP/s; 4 x 1,000
+// after 1,000, 16 / 4 heads of 64, 128 and 256: fp32 492, 1,092 and 2,331 us (either output
+// type), bf16 caches with fp32 outputs 192, 325 and 798 (with bf16 outputs, chunk_umma.cuh's,
+// 54, 68 and 128). Registers
 // leave two or three warps to a scheduler, and no unit is full (heads of 128: tensor pipe
 // 45%, ALU 44%, issue 53%): what bounds it is how little of a warp's splits, products and
 // softmax goes on beside another's. Splitting a tile once for the block in shared memory,

@@ -5,13 +5,20 @@
 // in tiles of 128 rows (new tokens x query heads of one kv head) and TK keys, with a
 // running maximum and sum per row. A prompt's floor is the tensor unit's (4 head_dim flops
 // per visible row and key), that of a few rows over a long cache HBM's. Measured:
-//   8 prompts of 4,096 tokens, 16 / 2 heads of 128             447 us, 1,232 TFLOP/s
-//   1,024 tokens after 31,000, 32 / 8 heads of 128             369 us, 1,433 TFLOP/s
-//   64 x 1-512 after 200-8,000, 16 / 2 heads of 256          1,345 us,   854 TFLOP/s
-//   4 x 1,500-2,500 after 0-3,000, 8 / 8 heads of 64            79 us,   520 TFLOP/s
-//   32 x 1-16 after 1,000-16,000, 16 / 2 heads of 128           69 us, 4.2 TB/s
-// What bounds prompts now is the chain below and the items' starts and ends (tensor pipe
-// busy 49% of 2 prompts of 4,096); heads of 256 wait for K and V from L2.
+//   8 prompts of 4,096 tokens, 16 / 2 heads of 128             451 us, 1,219 TFLOP/s
+//   1,024 tokens after 31,000, 32 / 8 heads of 128             370 us, 1,430 TFLOP/s
+//   64 x 1-512 after 200-8,000, 16 / 2 heads of 256          1,350 us,   938 TFLOP/s
+//   4 x 1,500-2,500 after 0-3,000, 8 / 8 heads of 64            79 us,   533 TFLOP/s
+//   32 x 1-16 after 1,000-16,000, 16 / 2 heads of 128           69 us, 4.5 TB/s
+// What bounds prompts now is the chain below and the items' starts and ends: with heads of
+// 128 the tensor pipe is busy 49% of the time, with heads of 64, whose products are half as
+// long to a weight, 26%, and no unit is full (issue 43%, exponentials 27%). Heads of 256
+// (tensor pipe 43%) wait for loads, which begin about a tile ahead, as the rings hold 1.25
+// tiles of K and one of V: 5 GB from L2 at 6.8 TB/s, 23% of what L2 gives. Groups of query
+// heads that do not divide 128 load their queries by 16-byte copies: 8 prompts of 2,048,
+// 28 / 4 heads of 128 814 TFLOP/s, 32 / 4 998.
+// The two-tile kernels (128 registers at launch, which setmaxnreg hands out anew) spill some
+// 100 bytes.
 //
 // An item has NQ row tiles. What counts is that the unit always has a product to make: a
 // tile's chain (S, its way to the registers, the weights, their way back, P V) is some
